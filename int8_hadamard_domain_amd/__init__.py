@@ -22,6 +22,12 @@ Functions (same names as the C entry points):
                              drafter's linears)
   i8_quantize_activations    per-token, per-128 int8 activation quantizer (W8A8)
   moe_gateup_i8g_grouped     grouped W8A8 int8 g128 gate_up + epilogue
+  mxfp4_quantize             MXFP4 codes and scales of a matrix (blocks of 32)
+  mxfp4_dequantize           the values that codes and scales stand for
+  moe_gateup_mxfp4_grouped   grouped MXFP4 gate_up + epilogue
+  moe_down_mxfp4_combine     grouped MXFP4 down projection + weighted combine
+  draft_verify               which drafted tokens of a verify batch stay, and
+                             the token sampled after them
 """
 
 import ctypes
@@ -35,6 +41,7 @@ LIB_PATH = os.path.join(_HERE, "lib", "libi8h.so")
 I8H_OK, I8H_EINVAL, I8H_EUNSUPPORTED, I8H_EHIP = 0, -1, -2, -3
 PATHS = {"auto": 0, "gemv": 1, "gemm": 2, "tall": 3, "skinny": 4}
 DOWN_PATHS = {"auto": 0, "gemv": 1, "gemm": 2}
+TYPES = {torch.float32: 0, torch.bfloat16: 1}
 
 _lib = None
 
@@ -84,6 +91,14 @@ def lib():
         "moe_down_bf16_act_bf16_workspace_size": (SZ, [I, I, I, I]),
         "moe_down_bf16_combine_act_bf16": (I, [P, I, I, P, I, I, I, P, P, P, P, P, P, SZ, I, P]),
         "linear_i8f16": (I, [P, I, I, P, P, I, P, P]),
+        "mxfp4_quantize": (I, [P, I, I, I, P, P, P]),
+        "mxfp4_dequantize": (I, [P, P, I, I, P, I, P]),
+        "moe_gateup_mxfp4_workspace_size": (SZ, [I, I]),
+        "moe_gateup_mxfp4_grouped": (I, [P, I, I, P, P, I, I, I, P, P, P, P, I, P, SZ, P]),
+        "moe_down_mxfp4_workspace_size": (SZ, [I, I, I, I]),
+        "moe_down_mxfp4_combine": (I, [P, I, I, I, P, P, I, I, I, P, P, P, P, P, P, SZ, P]),
+        "draft_verify_workspace_size": (SZ, [I, I]),
+        "draft_verify": (I, [P, P, I, P, P, P, P, I, I, I, P, P, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -476,3 +491,151 @@ def i8g_workspace_views(workspace, T, K):
     qx = workspace[:T * K].view(torch.int8).view(T, K)
     sx = workspace[a:a + T * (K // 128) * 4].view(torch.float32).view(T, K // 128)
     return qx, sx
+
+
+def _type(t, name):
+    """The library's element type of a float32 or bfloat16 tensor."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in TYPES:
+        raise TypeError(f"{name} must be a float32 or bfloat16 tensor")
+    return TYPES[t.dtype]
+
+
+def _mx_weights(codes, scales, K, dev):
+    """Check MXFP4 weights of K columns: codes [E, R, K/2], scales [E, R, K/32]. Returns (E, R)."""
+    _dev(codes, "codes", torch.uint8, 3, device=dev)
+    E, R, _ = codes.shape
+    _dev(codes, "codes", torch.uint8, shape=(E, R, K // 2))
+    _dev(scales, "scales", torch.uint8, shape=(E, R, K // 32), device=dev)
+    return E, R
+
+
+def _rows(n):
+    if n >= 1 << 31:
+        raise ValueError(f"at most {(1 << 31) - 1} rows (got {n})")
+
+
+def mxfp4_quantize(x, codes=None, scales=None):
+    """x [..., K] float32 or bfloat16 (K % 32 == 0) -> (codes uint8 [..., K/2],
+    scales uint8 [..., K/32]): MXFP4, two E2M1 codes a byte (lower index in
+    the low nibble) and an E8M0 scale per 32 values."""
+    xt = _type(x, "x")
+    _dev(x, "x", x.dtype)
+    if x.dim() == 0 or x.shape[-1] == 0 or x.shape[-1] % 32:
+        raise ValueError(f"x must have a last dimension of whole blocks of 32 (got {tuple(x.shape)})")
+    lead, K = tuple(x.shape[:-1]), x.shape[-1]
+    _rows(x.numel() // K)
+    want = {"codes": lead + (K // 2,), "scales": lead + (K // 32,)}
+    codes, scales = (torch.empty(want[n], dtype=torch.uint8, device=x.device) if t is None
+                     else _dev(t, n, torch.uint8, shape=want[n], device=x.device)
+                     for n, t in (("codes", codes), ("scales", scales)))
+    _check("mxfp4_quantize", lib().mxfp4_quantize(
+        _ptr(x), xt, x.numel() // K, K, _ptr(codes), _ptr(scales), _stream(x.device)))
+    return codes, scales
+
+
+def mxfp4_dequantize(codes, scales, dtype=torch.bfloat16, out=None):
+    """The values of MXFP4 codes [..., K/2] and scales [..., K/32] (uint8) as
+    [..., K] float32 or bfloat16 (dtype, or the dtype of a given out)."""
+    _dev(codes, "codes", torch.uint8)
+    if codes.dim() == 0 or codes.shape[-1] == 0 or codes.shape[-1] % 16:
+        raise ValueError(f"codes must have a last dimension of whole blocks of 16 bytes (got {tuple(codes.shape)})")
+    lead, K = tuple(codes.shape[:-1]), 2 * codes.shape[-1]
+    _rows(codes.numel() * 2 // K)
+    _dev(scales, "scales", torch.uint8, shape=lead + (K // 32,), device=codes.device)
+    if out is None:
+        if dtype not in TYPES:
+            raise TypeError(f"dtype must be float32 or bfloat16 (got {dtype})")
+        out = torch.empty(lead + (K,), dtype=dtype, device=codes.device)
+    ot = _type(out, "out")
+    _dev(out, "out", out.dtype, shape=lead + (K,), device=codes.device)
+    _check("mxfp4_dequantize", lib().mxfp4_dequantize(
+        _ptr(codes), _ptr(scales), codes.numel() * 2 // K, K, _ptr(out), ot, _stream(codes.device)))
+    return out
+
+
+def moe_gateup_mxfp4_grouped(x, codes, scales, topk, expert_off, sorted_pairs,
+                             gate_up=True, act=True, workspace=None, act_dtype=torch.float32):
+    """Grouped MXFP4 gate_up.
+
+    x [T, K] bf16 (quantised to MXFP4 inside the call), codes [E, N, K/2]
+    uint8, scales [E, N, K/32] uint8. gate_up, act and act_dtype as for
+    moe_gateup_i8h_grouped. Returns (gate_up, act).
+    """
+    _dev(x, "x", torch.bfloat16, 2)
+    T, K = x.shape
+    dev = x.device
+    E, N = _mx_weights(codes, scales, K, dev)
+    _dev(expert_off, "expert_off", torch.int32, shape=(E + 1,), device=dev)
+    _dev(sorted_pairs, "sorted_pairs", torch.int32, shape=(T * topk,), device=dev)
+    workspace = _workspace(workspace, "workspace", lib().moe_gateup_mxfp4_workspace_size(T, K), dev)
+    gu = _out(gate_up, (T * topk, N), dev)
+    adt = _act_dtype(act, act_dtype)
+    ac = _out(act, (T * topk, N // 2), dev, adt)
+    _check("moe_gateup_mxfp4_grouped", lib().moe_gateup_mxfp4_grouped(
+        _ptr(x), T, K, _ptr(codes), _ptr(scales), E, N, topk, _ptr(expert_off), _ptr(sorted_pairs),
+        _ptr(gu), _ptr(ac), TYPES[adt], _ptr(workspace), workspace.numel(), _stream(dev)))
+    return gu, ac
+
+
+def moe_down_mxfp4_combine(act, codes, scales, routing, out=None, workspace=None):
+    """MXFP4 grouped down projection of the expert-sorted act rows [P, I]
+    (float32 or bfloat16, quantised inside the call) against codes [E, H, I/2]
+    and scales [E, H, I/32] uint8, merged per token with the router weights:
+    returns out [T, H] float32. `routing` is moe_route_permute's dict."""
+    at = _type(act, "act")
+    _dev(act, "act", act.dtype, 2)
+    P, I = act.shape
+    dev = act.device
+    E, H = _mx_weights(codes, scales, I, dev)
+    ids = _dev(routing["topk_ids"], "topk_ids", torch.int32, 2, device=dev)
+    T, topk = ids.shape
+    if P != T * topk:
+        raise ValueError(f"act must have T * topk = {T * topk} rows (got {P})")
+    tw = _dev(routing["topk_w"], "topk_w", torch.float32, shape=(T, topk), device=dev)
+    off = _dev(routing["expert_off"], "expert_off", torch.int32, shape=(E + 1,), device=dev)
+    pos = _dev(routing["pair_pos"], "pair_pos", torch.int32, shape=(P,), device=dev)
+    workspace = _workspace(workspace, "workspace", lib().moe_down_mxfp4_workspace_size(T, I, H, topk), dev)
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.float32, device=dev)
+    else:
+        _dev(out, "out", torch.float32, shape=(T, H), device=dev)
+    _check("moe_down_mxfp4_combine", lib().moe_down_mxfp4_combine(
+        _ptr(act), at, T, I, _ptr(codes), _ptr(scales), E, H, topk, _ptr(ids), _ptr(tw), _ptr(off), _ptr(pos),
+        _ptr(out), _ptr(workspace), workspace.numel(), _stream(dev)))
+    return out
+
+
+def draft_verify(target_probs, draft_probs, drafted, u, u_next, draft_len=None, tokens=None, accepted=None,
+                 workspace=None):
+    """Verification of drafted tokens (speculative sampling).
+
+    target_probs [B, D+1, V], draft_probs [B, D, V] of the same type (float32
+    or bfloat16), or None for tokens drafted without sampling; drafted [B, D]
+    int32; u [B, D] and u_next [B] float32 uniform in [0, 1); draft_len [B]
+    int32, or None for D everywhere. Returns (tokens [B, D+1] int32: the
+    drafted tokens that stay, the token sampled after them, then -1; accepted
+    [B] int32: how many stay).
+    """
+    pt = _type(target_probs, "target_probs")
+    _dev(target_probs, "target_probs", target_probs.dtype, 3)
+    B, D, V = target_probs.shape
+    D -= 1
+    dev = target_probs.device
+    if D < 0:
+        raise ValueError("target_probs must hold a row for each drafted token and one more")
+    if draft_probs is not None:
+        _dev(draft_probs, "draft_probs", target_probs.dtype, shape=(B, D, V), device=dev)
+    _dev(drafted, "drafted", torch.int32, shape=(B, D), device=dev)
+    _dev(u, "u", torch.float32, shape=(B, D), device=dev)
+    _dev(u_next, "u_next", torch.float32, shape=(B,), device=dev)
+    if draft_len is not None:
+        _dev(draft_len, "draft_len", torch.int32, shape=(B,), device=dev)
+    tokens = (torch.empty((B, D + 1), dtype=torch.int32, device=dev) if tokens is None
+              else _dev(tokens, "tokens", torch.int32, shape=(B, D + 1), device=dev))
+    accepted = (torch.empty((B,), dtype=torch.int32, device=dev) if accepted is None
+                else _dev(accepted, "accepted", torch.int32, shape=(B,), device=dev))
+    workspace = _workspace(workspace, "workspace", lib().draft_verify_workspace_size(B, V), dev)
+    _check("draft_verify", lib().draft_verify(
+        _ptr(target_probs), _ptr(draft_probs), pt, _ptr(drafted), _ptr(draft_len), _ptr(u), _ptr(u_next), B, D, V,
+        _ptr(tokens), _ptr(accepted), _ptr(workspace), workspace.numel(), _stream(dev)))
+    return tokens, accepted

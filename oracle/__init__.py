@@ -31,10 +31,12 @@ Modules:
              transform) and their product
   w8a8     - the int8 g128 W8A8 form: RTN weight and per-token activation
              quantizers and the grouped gate_up on integer group sums
+  mxfp4    - MXFP4 (OCP microscaling) quantiser and the grouped products on it
+  draft    - verification of drafted tokens, in rational arithmetic
 
 Every function here is pinned by tests/test_oracle_*.py against closed
 forms, invariants, library special cases or brute force; none is marked
 "parity unpinned".
 """
 
-from . import numfmt, hadamard, quant, router, gateup, down, dense, w8a8  # noqa: F401
+from . import numfmt, hadamard, quant, router, gateup, down, dense, w8a8, mxfp4, draft  # noqa: F401

@@ -1,0 +1,122 @@
+"""Host-side checks of the MXFP4 and draft-verification entry points (no GPU):
+every declared function is exported, invalid arguments are refused with the
+documented status codes before anything is launched (dummy addresses that are
+never read), and the binding refuses tensors that do not fit."""
+
+import ctypes
+import os
+import re
+
+import pytest
+import torch
+
+import int8_hadamard_domain_amd as i8h
+
+INCLUDE = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include")
+EINVAL, EUNSUP, OK = i8h.I8H_EINVAL, i8h.I8H_EUNSUPPORTED, i8h.I8H_OK
+A = ctypes.c_void_p(0x10000)      # a 256-byte aligned dummy address, never touched
+ODD = ctypes.c_void_p(0x10002)    # misaligned for 4- and 16-byte data
+BYTE = ctypes.c_void_p(0x10001)   # misaligned for everything but bytes
+EIGHT = ctypes.c_void_p(0x10008)  # misaligned for 16-byte data
+BIG = 1 << 62
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not os.path.exists(i8h.LIB_PATH):
+        pytest.skip("libi8h.so not built")
+    return i8h.lib()
+
+
+@pytest.mark.parametrize("header", ["i8h_mxfp4.h", "i8h_draft.h"])
+def test_every_declared_function_is_exported_and_bound(L, header):
+    with open(os.path.join(INCLUDE, header)) as f:
+        src = re.sub(r"/\*.*?\*/", "", f.read(), flags=re.S)
+    names = set(re.findall(r"\b([a-z][a-z0-9_]*)\s*\(", src)) - {"defined"}
+    assert names
+    for n in names:
+        assert getattr(L, n).argtypes is not None, n
+        if not n.endswith("_workspace_size"):
+            assert callable(getattr(i8h, n))
+
+
+@pytest.mark.parametrize("name", ["mxfp4_quantize", "mxfp4_dequantize"])
+def test_quantiser_validation(L, name):
+    def call(x=A, t=0, T=4, K=64, c=A, s=A):
+        if name == "mxfp4_quantize":
+            return L.mxfp4_quantize(x, t, T, K, c, s, None)
+        return L.mxfp4_dequantize(c, s, T, K, x, t, None)
+    assert call(t=2) == EINVAL and call(t=-1) == EINVAL
+    assert call(T=-1) == EINVAL and call(K=0) == EINVAL and call(K=48) == EINVAL and call(K=-32) == EINVAL
+    assert call(x=None) == EINVAL and call(c=None) == EINVAL and call(s=None) == EINVAL
+    assert call(x=EIGHT) == EINVAL and call(c=EIGHT) == EINVAL
+    assert call(T=(1 << 31) - 1, K=2048) == EUNSUP          # more workgroups than a launch takes
+    assert call(T=0) == OK and call(T=0, x=None, c=None, s=None) == OK
+
+
+def test_gateup_validation(L):
+    need = L.moe_gateup_mxfp4_workspace_size(8, 256)
+    assert need == 1024 + 256
+    assert L.moe_gateup_mxfp4_workspace_size(0, 256) == 0 and L.moe_gateup_mxfp4_workspace_size(8, 100) == 0
+
+    def call(x=A, T=8, K=256, c=A, s=A, E=4, N=128, k=2, off=A, sp=A, gu=A, act=A, t=0, ws=A, wsb=need):
+        return L.moe_gateup_mxfp4_grouped(x, T, K, c, s, E, N, k, off, sp, gu, act, t, ws, wsb, None)
+    for bad in (dict(T=-1), dict(K=0), dict(K=96), dict(E=0), dict(N=0), dict(N=127), dict(k=0), dict(t=2),
+                dict(x=None), dict(c=None), dict(s=None), dict(off=None), dict(sp=None), dict(x=EIGHT), dict(c=EIGHT),
+                dict(s=ODD), dict(off=ODD), dict(sp=ODD), dict(gu=EIGHT), dict(act=EIGHT), dict(ws=None),
+                dict(ws=EIGHT), dict(wsb=need - 1)):
+        assert call(**bad) == EINVAL, bad
+    for bad in (dict(N=96), dict(E=1025), dict(k=5), dict(E=64, k=33), dict(T=1 << 28, k=32, E=64)):
+        assert call(**bad) == EUNSUP, bad
+    assert call(T=0) == OK and call(gu=None, act=None) == OK
+
+
+def test_down_validation(L):
+    need = L.moe_down_mxfp4_workspace_size(8, 96, 64, 2)
+    assert need == 768 + 256 + 16 * 64 * 4
+    assert L.moe_down_mxfp4_workspace_size(0, 96, 64, 2) == 0 and L.moe_down_mxfp4_workspace_size(8, 100, 64, 2) == 0
+
+    def call(a=A, t=0, T=8, I=96, c=A, s=A, E=4, H=64, k=2, ids=A, w=A, off=A, pos=A, out=A, ws=A, wsb=need):
+        return L.moe_down_mxfp4_combine(a, t, T, I, c, s, E, H, k, ids, w, off, pos, out, ws, wsb, None)
+    for bad in (dict(T=-1), dict(I=0), dict(I=48), dict(E=0), dict(H=0), dict(H=36), dict(k=0), dict(t=2),
+                dict(a=None), dict(c=None), dict(s=None), dict(ids=None), dict(w=None), dict(off=None), dict(pos=None),
+                dict(out=None), dict(a=EIGHT), dict(c=EIGHT), dict(s=ODD), dict(ids=ODD), dict(w=ODD), dict(off=ODD),
+                dict(pos=ODD), dict(out=EIGHT), dict(ws=None), dict(ws=EIGHT), dict(wsb=need - 1)):
+        assert call(**bad) == EINVAL, bad
+    for bad in (dict(H=72), dict(E=1025), dict(k=5), dict(E=64, k=33), dict(T=1 << 28, k=32, E=64)):
+        assert call(**bad) == EUNSUP, bad
+    assert call(T=0) == OK
+
+
+def test_draft_validation(L):
+    need = L.draft_verify_workspace_size(3, 5000)
+    assert need > 0 and need % 256 == 0
+    assert L.draft_verify_workspace_size(0, 5000) == 0 and L.draft_verify_workspace_size(3, 0) == 0
+
+    def call(p=A, q=A, t=0, x=A, ln=A, u=A, un=A, B=3, D=4, V=5000, tok=A, acc=A, ws=A, wsb=need):
+        return L.draft_verify(p, q, t, x, ln, u, un, B, D, V, tok, acc, ws, wsb, None)
+    for bad in (dict(t=2), dict(B=-1), dict(D=-1), dict(V=0), dict(p=None), dict(x=None), dict(u=None), dict(un=None),
+                dict(tok=None), dict(acc=None), dict(p=ODD), dict(q=ODD), dict(p=BYTE, t=1), dict(q=BYTE, t=1),
+                dict(x=ODD), dict(ln=ODD), dict(u=ODD), dict(un=ODD), dict(tok=ODD), dict(acc=ODD), dict(ws=None),
+                dict(ws=EIGHT), dict(wsb=need - 1)):
+        assert call(**bad) == EINVAL, bad
+    assert call(D=1024) == EUNSUP and call(B=65536, wsb=BIG) == EUNSUP
+    assert call(B=0) == OK
+
+
+def test_binding_refuses_what_does_not_fit():
+    """On CPU tensors: the first check that fails says so; nothing reaches the library."""
+    with pytest.raises(TypeError):
+        i8h.mxfp4_quantize(torch.zeros((2, 32), dtype=torch.float16))
+    with pytest.raises(TypeError):
+        i8h.mxfp4_quantize([1.0] * 32)
+    with pytest.raises(ValueError):
+        i8h.mxfp4_quantize(torch.zeros((2, 32)))                       # not on the GPU
+    with pytest.raises(ValueError):
+        i8h.mxfp4_dequantize(torch.zeros((2, 16), dtype=torch.uint8), torch.zeros((2, 1), dtype=torch.uint8))
+    with pytest.raises(ValueError):
+        i8h.moe_gateup_mxfp4_grouped(torch.zeros((2, 128), dtype=torch.bfloat16), None, None, 1, None, None)
+    with pytest.raises(TypeError):
+        i8h.moe_down_mxfp4_combine(torch.zeros((2, 32), dtype=torch.float16), None, None, {})
+    with pytest.raises(TypeError):
+        i8h.draft_verify(torch.zeros((1, 2, 3), dtype=torch.float64), None, None, None, None)
