@@ -51,8 +51,8 @@ int mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int T, int K, 
  * with the epilogue, row order and outputs of moe_gateup_i8h_grouped.
  *
  * codes [E, N, K/2] 16-B aligned, scales [E, N, K/32] 4-B aligned; K % 128 ==
- * 0; N positive and even (odd: I8H_EINVAL) and a multiple of 64 (else
- * I8H_EUNSUPPORTED). gate_up float32 [T*topk, N] or NULL; act [T*topk, N/2]
+ * 0; N positive and even (odd: I8H_EINVAL) and a multiple of 64, N*K < 2^32 and T*(K + 256) <
+ * 2^32 (else I8H_EUNSUPPORTED). gate_up float32 [T*topk, N] or NULL; act [T*topk, N/2]
  * of act_type (bf16: each value rounded to nearest even from the float32
  * one) or NULL; both 16-B aligned. workspace: at least
  * moe_gateup_mxfp4_workspace_size(T, K) bytes, 256-B aligned; what it holds
@@ -69,7 +69,8 @@ int moe_gateup_mxfp4_grouped(const uint16_t* x, int T, int K, const uint8_t* cod
  *   y[r, h]   = sum_b 2^(sw[e,h,b] + sa[r,b] - 254) sum_{i in b} qw[e,h,i] qa[r,i]
  *   out[t, h] = sum_j topk_w[t, j] * y[pair_pos[t*topk + j], h]   (slot order)
  * codes [E, H, I/2] 16-B aligned, scales [E, H, I/32] 4-B aligned; H % 32 ==
- * 0 (H % 8 != 0: I8H_EINVAL, else I8H_EUNSUPPORTED). out float32 [T, H],
+ * 0 (H % 8 != 0: I8H_EINVAL, else I8H_EUNSUPPORTED), H*I < 2^32 and
+ * T*topk*(I + 256) < 2^32 (else I8H_EUNSUPPORTED). out float32 [T, H],
  * 16-B aligned. topk_ids, topk_w, expert_off, pair_pos: as moe_route_permute
  * writes them. workspace: at least moe_down_mxfp4_workspace_size(T, I, H,
  * topk) bytes, 256-B aligned, contents unspecified afterwards. */

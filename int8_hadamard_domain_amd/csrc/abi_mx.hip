@@ -22,14 +22,19 @@ inline hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s);
 inline size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 inline bool is_type(int t) { return t == I8H_F32 || t == I8H_BF16; }
 
-// the quantised rows in a workspace: codes [rows, K/2], then scales [rows, K/32]
+// the quantised rows in a workspace, padded to whole stages of the products:
+// codes [rows, Kp/2], then scales [rows, Kp/32]
 struct MxRows {
+  int Kp;
   size_t scales, total;
-  MxRows(size_t rows, size_t K) {
-    scales = round_up(rows * (K / 2), 256);
-    total = scales + round_up(rows * (K / 32), 256);
+  MxRows(size_t rows, int K) {
+    Kp = (int)round_up((size_t)K, i8h::kMxStage);
+    scales = round_up(rows * (Kp / 2), 256);
+    total = scales + round_up(rows * (Kp / 32), 256);
   }
 };
+// the products address the codes with 32-bit offsets
+inline bool rows_fit(int64_t rows, int K) { return rows * ((int64_t)K + i8h::kMxStage) < ((int64_t)1 << 32); }
 
 // a kernel per 8 values, 256 threads a workgroup
 inline bool quant_fits(int64_t rows, int K) { return rows * (K / 8) < ((int64_t)1 << 38); }
@@ -43,7 +48,7 @@ int mxfp4_quantize(const void* x, int x_type, int T, int K, uint8_t* codes, uint
   if (!quant_fits(T, K)) return I8H_EUNSUPPORTED;
   if (T == 0) return I8H_OK;
   if (!x || !codes || !scales || !aligned(x, 16) || !aligned(codes, 16)) return I8H_EINVAL;
-  return from_hip(i8h::launch_mxfp4_quantize(x, x_type == I8H_BF16, (int64_t)T * K, codes, scales,
+  return from_hip(i8h::launch_mxfp4_quantize(x, x_type == I8H_BF16, T, K, K, codes, scales,
                                              as_stream(stream)));
 }
 
@@ -69,9 +74,9 @@ int moe_gateup_mxfp4_grouped(const uint16_t* x, int T, int K, const uint8_t* cod
   if (!is_type(act_type) || T < 0 || K <= 0 || (K % 128) != 0 || E <= 0 || N <= 0 || topk <= 0) return I8H_EINVAL;
   if (E > kMaxExperts || topk > kMaxTopk || topk > E) return I8H_EUNSUPPORTED;
   if ((N % 2) != 0) return I8H_EINVAL;          // gate and up halves
-  if ((N % 64) != 0) return I8H_EUNSUPPORTED;
+  if ((N % 64) != 0 || (int64_t)N * K >= (int64_t)1 << 32) return I8H_EUNSUPPORTED;   // 32-bit offsets in an expert
   if ((int64_t)T * topk >= (int64_t)1 << 31) return I8H_EUNSUPPORTED;
-  if (!quant_fits(T, K)) return I8H_EUNSUPPORTED;
+  if (!rows_fit(T, K)) return I8H_EUNSUPPORTED;
   if (T == 0) return I8H_OK;
   if (!x || !codes || !scales || !expert_off || !sorted_pairs) return I8H_EINVAL;
   if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(expert_off, 4) ||
@@ -84,8 +89,8 @@ int moe_gateup_mxfp4_grouped(const uint16_t* x, int T, int K, const uint8_t* cod
   uint8_t* xq = static_cast<uint8_t*>(workspace);
   uint8_t* xs = xq + lay.scales;
   hipStream_t st = as_stream(stream);
-  if (i8h::launch_mxfp4_quantize(x, true, (int64_t)T * K, xq, xs, st) != hipSuccess) return I8H_EHIP;
-  return from_hip(i8h::launch_gateup_mxfp4(xq, xs, K, codes, scales, E, N, topk, expert_off, sorted_pairs, gate_up,
+  if (i8h::launch_mxfp4_quantize(x, true, T, K, lay.Kp, xq, xs, st) != hipSuccess) return I8H_EHIP;
+  return from_hip(i8h::launch_gateup_mxfp4(xq, xs, T, K, codes, scales, E, N, topk, expert_off, sorted_pairs, gate_up,
                                            act, act_type == I8H_BF16, st));
 }
 
@@ -102,10 +107,10 @@ int moe_down_mxfp4_combine(const void* act, int act_type, int T, int I, const ui
   if (!is_type(act_type) || T < 0 || I <= 0 || (I % 32) != 0 || H <= 0 || (H % 8) != 0 || E <= 0 || topk <= 0)
     return I8H_EINVAL;
   if (E > kMaxExperts || topk > kMaxTopk || topk > E) return I8H_EUNSUPPORTED;
-  if ((H % 32) != 0) return I8H_EUNSUPPORTED;
+  if ((H % 32) != 0 || (int64_t)H * I >= (int64_t)1 << 32) return I8H_EUNSUPPORTED;
   const int64_t P = (int64_t)T * topk;
   if (P >= (int64_t)1 << 31) return I8H_EUNSUPPORTED;
-  if (!quant_fits(P, I)) return I8H_EUNSUPPORTED;
+  if (!rows_fit(P, I)) return I8H_EUNSUPPORTED;
   if (T == 0) return I8H_OK;
   if (!act || !codes || !scales || !topk_ids || !topk_w || !expert_off || !pair_pos || !out) return I8H_EINVAL;
   if (!aligned(act, 16) || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(out, 16)) return I8H_EINVAL;
@@ -118,7 +123,7 @@ int moe_down_mxfp4_combine(const void* act, int act_type, int T, int I, const ui
   uint8_t* as = aq + lay.scales;
   float* y = reinterpret_cast<float*>(aq + lay.total);
   hipStream_t st = as_stream(stream);
-  if (i8h::launch_mxfp4_quantize(act, act_type == I8H_BF16, P * I, aq, as, st) != hipSuccess) return I8H_EHIP;
+  if (i8h::launch_mxfp4_quantize(act, act_type == I8H_BF16, P, I, lay.Kp, aq, as, st) != hipSuccess) return I8H_EHIP;
   return from_hip(i8h::launch_down_mxfp4(aq, as, T, I, codes, scales, E, H, topk, topk_w, expert_off, pair_pos, y,
                                          out, st));
 }

@@ -66,14 +66,14 @@ def test_gateup_validation(L):
                 dict(s=ODD), dict(off=ODD), dict(sp=ODD), dict(gu=EIGHT), dict(act=EIGHT), dict(ws=None),
                 dict(ws=EIGHT), dict(wsb=need - 1)):
         assert call(**bad) == EINVAL, bad
-    for bad in (dict(N=96), dict(E=1025), dict(k=5), dict(E=64, k=33), dict(T=1 << 28, k=32, E=64)):
+    for bad in (dict(N=96), dict(E=1025), dict(k=5), dict(E=64, k=33), dict(T=1 << 28, k=32, E=64), dict(T=1 << 25)):
         assert call(**bad) == EUNSUP, bad
     assert call(T=0) == OK and call(gu=None, act=None) == OK
 
 
 def test_down_validation(L):
     need = L.moe_down_mxfp4_workspace_size(8, 96, 64, 2)
-    assert need == 768 + 256 + 16 * 64 * 4
+    assert need == 16 * 128 + 256 + 16 * 64 * 4        # rows padded to 256 values
     assert L.moe_down_mxfp4_workspace_size(0, 96, 64, 2) == 0 and L.moe_down_mxfp4_workspace_size(8, 100, 64, 2) == 0
 
     def call(a=A, t=0, T=8, I=96, c=A, s=A, E=4, H=64, k=2, ids=A, w=A, off=A, pos=A, out=A, ws=A, wsb=need):
@@ -83,7 +83,7 @@ def test_down_validation(L):
                 dict(out=None), dict(a=EIGHT), dict(c=EIGHT), dict(s=ODD), dict(ids=ODD), dict(w=ODD), dict(off=ODD),
                 dict(pos=ODD), dict(out=EIGHT), dict(ws=None), dict(ws=EIGHT), dict(wsb=need - 1)):
         assert call(**bad) == EINVAL, bad
-    for bad in (dict(H=72), dict(E=1025), dict(k=5), dict(E=64, k=33), dict(T=1 << 28, k=32, E=64)):
+    for bad in (dict(H=72), dict(E=1025), dict(k=5), dict(E=64, k=33), dict(T=1 << 28, k=32, E=64), dict(T=1 << 25)):
         assert call(**bad) == EUNSUP, bad
     assert call(T=0) == OK
 
