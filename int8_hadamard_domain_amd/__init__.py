@@ -93,9 +93,9 @@ def lib():
         "linear_i8f16": (I, [P, I, I, P, P, I, P, P]),
         "mxfp4_quantize": (I, [P, I, I, I, P, P, P]),
         "mxfp4_dequantize": (I, [P, P, I, I, P, I, P]),
-        "moe_gateup_mxfp4_workspace_size": (SZ, [I, I]),
+        "moe_gateup_mxfp4_workspace_size": (SZ, [I, I, I, I]),
         "moe_gateup_mxfp4_grouped": (I, [P, I, I, P, P, I, I, I, P, P, P, P, I, P, SZ, P]),
-        "moe_down_mxfp4_workspace_size": (SZ, [I, I, I, I]),
+        "moe_down_mxfp4_workspace_size": (SZ, [I, I, I, I, I]),
         "moe_down_mxfp4_combine": (I, [P, I, I, I, P, P, I, I, I, P, P, P, P, P, P, SZ, P]),
         "draft_verify_workspace_size": (SZ, [I, I]),
         "draft_verify": (I, [P, P, I, P, P, P, P, I, I, I, P, P, P, SZ, P]),
@@ -567,7 +567,7 @@ def moe_gateup_mxfp4_grouped(x, codes, scales, topk, expert_off, sorted_pairs,
     E, N = _mx_weights(codes, scales, K, dev)
     _dev(expert_off, "expert_off", torch.int32, shape=(E + 1,), device=dev)
     _dev(sorted_pairs, "sorted_pairs", torch.int32, shape=(T * topk,), device=dev)
-    workspace = _workspace(workspace, "workspace", lib().moe_gateup_mxfp4_workspace_size(T, K), dev)
+    workspace = _workspace(workspace, "workspace", lib().moe_gateup_mxfp4_workspace_size(T, K, E, topk), dev)
     gu = _out(gate_up, (T * topk, N), dev)
     adt = _act_dtype(act, act_dtype)
     ac = _out(act, (T * topk, N // 2), dev, adt)
@@ -594,7 +594,7 @@ def moe_down_mxfp4_combine(act, codes, scales, routing, out=None, workspace=None
     tw = _dev(routing["topk_w"], "topk_w", torch.float32, shape=(T, topk), device=dev)
     off = _dev(routing["expert_off"], "expert_off", torch.int32, shape=(E + 1,), device=dev)
     pos = _dev(routing["pair_pos"], "pair_pos", torch.int32, shape=(P,), device=dev)
-    workspace = _workspace(workspace, "workspace", lib().moe_down_mxfp4_workspace_size(T, I, H, topk), dev)
+    workspace = _workspace(workspace, "workspace", lib().moe_down_mxfp4_workspace_size(T, I, E, H, topk), dev)
     if out is None:
         out = torch.empty((T, H), dtype=torch.float32, device=dev)
     else:

@@ -22,18 +22,7 @@ inline hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s);
 inline size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 inline bool is_type(int t) { return t == I8H_F32 || t == I8H_BF16; }
 
-// the quantised rows in a workspace, padded to whole stages of the products:
-// codes [rows, Kp/2], then scales [rows, Kp/32]
-struct MxRows {
-  int Kp;
-  size_t scales, total;
-  MxRows(size_t rows, int K) {
-    Kp = (int)round_up((size_t)K, i8h::kMxStage);
-    scales = round_up(rows * (Kp / 2), 256);
-    total = scales + round_up(rows * (Kp / 32), 256);
-  }
-};
-// the products address the codes with 32-bit offsets
+// the products address the quantised rows with 32-bit offsets (144 bytes a stage of 256)
 inline bool rows_fit(int64_t rows, int K) { return rows * ((int64_t)K + i8h::kMxStage) < ((int64_t)1 << 32); }
 
 // a kernel per 8 values, 256 threads a workgroup
@@ -48,7 +37,7 @@ int mxfp4_quantize(const void* x, int x_type, int T, int K, uint8_t* codes, uint
   if (!quant_fits(T, K)) return I8H_EUNSUPPORTED;
   if (T == 0) return I8H_OK;
   if (!x || !codes || !scales || !aligned(x, 16) || !aligned(codes, 16)) return I8H_EINVAL;
-  return from_hip(i8h::launch_mxfp4_quantize(x, x_type == I8H_BF16, T, K, K, codes, scales,
+  return from_hip(i8h::launch_mxfp4_quantize(x, x_type == I8H_BF16, (int64_t)T * K, codes, scales,
                                              as_stream(stream)));
 }
 
@@ -62,9 +51,9 @@ int mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int T, int K, 
                                                as_stream(stream)));
 }
 
-size_t moe_gateup_mxfp4_workspace_size(int T, int K) {
-  if (T <= 0 || K <= 0 || (K % 128) != 0) return 0;
-  return MxRows(T, K).total;
+size_t moe_gateup_mxfp4_workspace_size(int T, int K, int E, int topk) {
+  if (T <= 0 || K <= 0 || (K % 128) != 0 || E <= 0 || topk <= 0) return 0;
+  return i8h::MxWorkspace(T, K, (int64_t)T * topk, E).total;
 }
 
 int moe_gateup_mxfp4_grouped(const uint16_t* x, int T, int K, const uint8_t* codes, const uint8_t* scales, int E,
@@ -83,21 +72,18 @@ int moe_gateup_mxfp4_grouped(const uint16_t* x, int T, int K, const uint8_t* cod
       !aligned(sorted_pairs, 4))
     return I8H_EINVAL;
   if ((gate_up && !aligned(gate_up, 16)) || (act && !aligned(act, 16))) return I8H_EINVAL;
-  const MxRows lay(T, K);
-  if (!workspace || workspace_bytes < lay.total || !aligned(workspace, 256)) return I8H_EINVAL;
+  if (!workspace || workspace_bytes < moe_gateup_mxfp4_workspace_size(T, K, E, topk) || !aligned(workspace, 256))
+    return I8H_EINVAL;
   if (!gate_up && !act) return I8H_OK;          // nothing requested
-  uint8_t* xq = static_cast<uint8_t*>(workspace);
-  uint8_t* xs = xq + lay.scales;
-  hipStream_t st = as_stream(stream);
-  if (i8h::launch_mxfp4_quantize(x, true, T, K, lay.Kp, xq, xs, st) != hipSuccess) return I8H_EHIP;
-  return from_hip(i8h::launch_gateup_mxfp4(xq, xs, T, K, codes, scales, E, N, topk, expert_off, sorted_pairs, gate_up,
-                                           act, act_type == I8H_BF16, st));
+  return from_hip(i8h::launch_gateup_mxfp4(x, T, K, codes, scales, E, N, topk, expert_off, sorted_pairs, gate_up, act,
+                                           act_type == I8H_BF16, static_cast<uint8_t*>(workspace),
+                                           as_stream(stream)));
 }
 
-size_t moe_down_mxfp4_workspace_size(int T, int I, int H, int topk) {
-  if (T <= 0 || I <= 0 || (I % 32) != 0 || H <= 0 || topk <= 0) return 0;
-  const size_t P = (size_t)T * topk;
-  return MxRows(P, I).total + round_up(P * H * sizeof(float), 256);
+size_t moe_down_mxfp4_workspace_size(int T, int I, int E, int H, int topk) {
+  if (T <= 0 || I <= 0 || (I % 32) != 0 || E <= 0 || H <= 0 || topk <= 0) return 0;
+  const int64_t P = (int64_t)T * topk;
+  return i8h::MxWorkspace(P, I, P, E).total + round_up((size_t)P * H * sizeof(float), 256);
 }
 
 int moe_down_mxfp4_combine(const void* act, int act_type, int T, int I, const uint8_t* codes, const uint8_t* scales,
@@ -116,16 +102,12 @@ int moe_down_mxfp4_combine(const void* act, int act_type, int T, int I, const ui
   if (!aligned(act, 16) || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(out, 16)) return I8H_EINVAL;
   if (!aligned(topk_ids, 4) || !aligned(topk_w, 4) || !aligned(expert_off, 4) || !aligned(pair_pos, 4))
     return I8H_EINVAL;
-  const MxRows lay(P, I);
-  if (!workspace || workspace_bytes < moe_down_mxfp4_workspace_size(T, I, H, topk) || !aligned(workspace, 256))
+  if (!workspace || workspace_bytes < moe_down_mxfp4_workspace_size(T, I, E, H, topk) || !aligned(workspace, 256))
     return I8H_EINVAL;
-  uint8_t* aq = static_cast<uint8_t*>(workspace);
-  uint8_t* as = aq + lay.scales;
-  float* y = reinterpret_cast<float*>(aq + lay.total);
-  hipStream_t st = as_stream(stream);
-  if (i8h::launch_mxfp4_quantize(act, act_type == I8H_BF16, P, I, lay.Kp, aq, as, st) != hipSuccess) return I8H_EHIP;
-  return from_hip(i8h::launch_down_mxfp4(aq, as, T, I, codes, scales, E, H, topk, topk_w, expert_off, pair_pos, y,
-                                         out, st));
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  float* y = reinterpret_cast<float*>(ws + i8h::MxWorkspace(P, I, P, E).total);
+  return from_hip(i8h::launch_down_mxfp4(act, act_type == I8H_BF16, T, I, codes, scales, E, H, topk, topk_w, expert_off,
+                                         pair_pos, ws, y, out, as_stream(stream)));
 }
 
 size_t draft_verify_workspace_size(int B, int V) {

@@ -88,22 +88,25 @@ hipError_t launch_down_gemm_combine(const void* act, bool act_bf16, int T, int I
 hipError_t launch_linear_i8f16(const uint16_t* x, int T, int K, const int8_t* codes, const uint16_t* scales, int N,
                                float* y, hipStream_t st);
 
-// MXFP4 quantiser and its inverse (mxfp4.hip): whole blocks of 32 values; rows
-// of K go to rows of Kp (K, or more: zero codes with scale 1 behind the row)
-hipError_t launch_mxfp4_quantize(const void* x, bool bf16, int64_t rows, int K, int Kp, uint8_t* codes,
-                                 uint8_t* scales, hipStream_t st);
+// MXFP4 quantiser and its inverse (mxfp4.hip): whole blocks of 32 values
+hipError_t launch_mxfp4_quantize(const void* x, bool bf16, int64_t values, uint8_t* codes, uint8_t* scales,
+                                 hipStream_t st);
 hipError_t launch_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t values, void* out, bool bf16,
                                    hipStream_t st);
 
-// grouped MXFP4 products (moe_mx.hip) on quantised activations, rows padded to
-// whole stages of K
+// grouped MXFP4 products (moe_mx.hip): the workspace holds the quantised rows,
+// padded to whole stages of K, and the list of passes
 constexpr int kMxStage = 256;
-hipError_t launch_gateup_mxfp4(const uint8_t* xq, const uint8_t* xs, int T, int K, const uint8_t* codes,
-                               const uint8_t* scales, int E, int N, int k, const int32_t* expert_off,
-                               const int32_t* sorted_pairs, float* gu, void* act, bool act_bf16, hipStream_t st);
-hipError_t launch_down_mxfp4(const uint8_t* aq, const uint8_t* as, int T, int I, const uint8_t* codes,
+struct MxWorkspace {
+  size_t items, total;
+  MxWorkspace(int64_t rows, int K, int64_t P, int E);
+};
+hipError_t launch_gateup_mxfp4(const uint16_t* x, int T, int K, const uint8_t* codes, const uint8_t* scales, int E,
+                               int N, int k, const int32_t* expert_off, const int32_t* sorted_pairs, float* gu,
+                               void* act, bool act_bf16, uint8_t* ws, hipStream_t st);
+hipError_t launch_down_mxfp4(const void* act, bool act_bf16, int T, int I, const uint8_t* codes,
                              const uint8_t* scales, int E, int H, int k, const float* tw, const int32_t* expert_off,
-                             const int32_t* pos, float* y, float* out, hipStream_t st);
+                             const int32_t* pos, uint8_t* ws, float* y, float* out, hipStream_t st);
 
 // verification of drafted tokens (draft.hip): sums holds 2 doubles per chunk of each sequence's row
 int draft_chunks(int V);

@@ -10,19 +10,22 @@
 // (products far below the largest of an instruction are kept, unlike the E4M3
 // forms), so the result is as exact as a float32 sum.
 //
-// The weights are the A operand (32 rows: for gate_up 16 gate rows and the
-// matching 16 up rows, so both halves of an output meet in one lane), the
-// activation rows the B operand (32 columns).
+// The weights are the A operand (tiles of 32 rows: for gate_up 16 gate rows and
+// the matching 16 up rows, so both halves of an output meet in one lane), the
+// activation rows the B operand (32 columns). Within a stage of K = 256, step j
+// takes block 4 (lane / 32) + j of both operands, so a lane's four scale bytes
+// are one dword, picked by the instruction's byte select, and its codes 64
+// contiguous bytes of its row.
 //
-// Work item = one pass of up to 32 MT rows of one expert x 128 weight rows, a
-// workgroup of 4 waves, a 32-row weight tile each. The weights go straight from
-// memory into operand registers, PD stages of K = 256 ahead (lane l reads 64
-// contiguous bytes of row l % 32; this pattern streams at 5.8 TB/s by itself,
-// 16-byte loads in address order at 5.9): every wave has its own, so LDS would
-// only add a copy. The activation rows are shared: double-buffered in LDS,
-// loaded up to three stages ahead through registers.
-// Within a stage, step j takes block 4 (lane / 32) + j of both operands, so a
-// lane's four scale bytes are one dword, picked by the instruction's byte select.
+// k_mx_prepare quantises the activation rows and lists the passes: up to 32 MT
+// sorted rows of one expert each. Then
+//   k_mx_stream  the passes' weight tiles, one after another, are dealt in equal
+//                runs to one workgroup of 8 waves per CU. A workgroup keeps the
+//                pass's activation rows in LDS, whole K, and its waves stream
+//                tiles past them from memory straight into operand registers,
+//                PD stages ahead and on into the next tile: no barrier, no wait
+//                but for the weights themselves.
+//   k_mx_ring    for K too long for that: activation rows in stages through LDS
 
 #include <type_traits>
 
@@ -31,69 +34,27 @@
 
 namespace i8h {
 
-namespace {
-
-constexpr int kMgThreads = 256;   // 4 waves, a 32-row weight tile each
-constexpr int kMgWaves = kMgThreads / kWave;
-constexpr int kMgRows = 32 * kMgWaves;   // weight rows of a work item
-constexpr int kStB = 8;                  // blocks of a stage (K = 256)
-constexpr int kRowBytes = 144;           // LDS row: 128 B of codes, 8 B of scales, 8 B so that 16 rows meet all 64 banks
-constexpr int kXcds = 8;
-
-struct MxArgs {
-  const uint8_t* xq;   // activation codes, rows of 128 stages bytes (padded to whole stages)
-  const uint8_t* xs;   // activation scales, rows of 8 stages
-  const uint8_t* wq;   // [E, R, K/2]
-  const uint8_t* ws;   // [E, R, K/32]
-  uint32_t xq_n;       // bytes of xq (xs has a sixteenth)
-  int E, R, nb, topk, ntiles, items;
-  const int32_t* expert_off;
-  const int32_t* sorted_pairs;   // gate_up: activation row of sorted row r is sorted_pairs[r] / topk
+// one pass: up to 32 MT sorted rows of one expert (the list's entry 0 holds the
+// number of passes in e)
+struct MxItem {
+  int e, r0, m, pad;
 };
 
-// Item i of the passes of up to `rows` rows, experts in order: its expert,
-// first sorted row and row count; false past the last item. Every wave of the
-// workgroup finds it by itself, from one batch of expert_off loads.
-__device__ __forceinline__ bool mx_item(const int32_t* __restrict__ off, int E, int i, int rows, int& e, int& r0,
-                                        int& m) {
-  const int lane = threadIdx.x % kWave;
-  int before = 0;
-  for (int e0 = 0; e0 < E; e0 += kWave) {
-    const int x = e0 + lane;
-    const int lo = off[min(x, E)], hi = off[min(x + 1, E)];
-    const int n = (hi - lo + rows - 1) / rows;
-    int inc = n;
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) {
-      const int o = __shfl_up(inc, d, kWave);
-      if (lane >= d) inc += o;
-    }
-    const uint64_t past = __ballot(before + inc > i);
-    if (past != 0) {
-      const int src = __ffsll((unsigned long long)past) - 1;
-      const int first = i - (before + __shfl(inc - n, src, kWave));   // pass of that expert
-      const int l = __shfl(lo, src, kWave), h = __shfl(hi, src, kWave);
-      e = __builtin_amdgcn_readfirstlane(e0 + src);
-      r0 = __builtin_amdgcn_readfirstlane(l + first * rows);
-      m = __builtin_amdgcn_readfirstlane(min(rows, h - r0));
-      return true;
-    }
-    before += __shfl(inc, kWave - 1, kWave);
-  }
-  return false;
-}
+namespace {
 
-// LDS writes before it are seen by the workgroup after it; loads from global
-// memory stay in flight (__syncthreads may wait for them)
-__device__ __forceinline__ void lds_barrier() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
+constexpr int kStB = 8;             // blocks of a stage (K = 256)
+constexpr int kXcds = 8;
+constexpr int kPrThreads = 256;     // k_mx_prepare, k_mx_combine
 
-struct MxW {
-  u32x4 q[4];
-  uint32_t s;
+struct MxArgs {
+  const uint8_t* x;    // activation rows of row_bytes: codes padded to whole stages, then their scales
+  const uint8_t* wq;   // [E, R, K/2]
+  const uint8_t* ws;   // [E, R, K/32]
+  uint32_t x_n;        // bytes of x, rounded up so that 16-byte reads of scales end inside
+  int row_bytes;
+  int E, R, nb, topk, ntiles;
+  const MxItem* items;
+  const int32_t* sorted_pairs;   // gate_up: activation row of sorted row r is sorted_pairs[r] / topk
 };
 
 // Loads go through buffer descriptors: an offset past the descriptor's size
@@ -111,26 +72,20 @@ __device__ __forceinline__ uint32_t mx_get4(mx_rsrc r, uint32_t off) {
   return __builtin_amdgcn_raw_buffer_load_b32(r, (int)off, 0, 0);
 }
 
-// The lane's four blocks of stage s of its weight row, qo and so the row's
-// offsets. TAIL: rows that are not whole stages. What is read past the row's
-// last block meets activation codes of zero, and its scale is set to 1, so
-// that another row's NaN scale stays out. Rows of scales may then start
-// anywhere: two aligned words hold the four bytes.
-template <bool TAIL>
-__device__ __forceinline__ void mx_load_w(mx_rsrc wq, mx_rsrc ws, uint32_t qo, uint32_t so, int s, int half, int nb,
-                                          MxW& w) {
-  const uint32_t o = qo + 128 * s + 64 * half;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) w.q[j] = mx_get16(wq, o + 16 * j);
-  const uint32_t c = so + kStB * s + 4 * half;
-  if constexpr (!TAIL) {
-    w.s = mx_get4(ws, c);
-  } else {
-    const uint32_t v = __builtin_amdgcn_alignbyte(mx_get4(ws, (c & ~3u) + 4), mx_get4(ws, c & ~3u), c & 3);
-    const int left = nb - (kStB * s + 4 * half);   // blocks of the row from here on
-    const uint32_t m = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
-    w.s = (v & m) | (0x7f7f7f7fu & ~m);
-  }
+// The four scale bytes v of a lane's blocks, of which the row has `left` from
+// there on: what is read past a row's last block meets activation codes of
+// zero, and the scale 1 keeps another row's NaN scale out.
+__device__ __forceinline__ uint32_t mx_mask_scales(uint32_t v, int left) {
+  const uint32_t m = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+  return (v & m) | (0x7f7f7f7fu & ~m);
+}
+
+// LDS writes before it are seen by the workgroup after it; loads from global
+// memory stay in flight (__syncthreads may wait for them)
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
 __device__ __forceinline__ void put4(float* p, const f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
@@ -138,166 +93,420 @@ __device__ __forceinline__ void put4(uint16_t* p, const f32x4 v) {
   *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
 }
 
-// GU: gate_up with epilogue (out0 = gate_up or NULL, out1 = act or NULL);
-// otherwise out0 = y [P, R]
-template <bool GU, int MT, bool TAIL, int PD, typename AT>
-__global__ void __launch_bounds__(kMgThreads, MT == 1 ? 4 : MT == 2 ? 3 : 2)
-k_mx_grouped(const MxArgs a, float* __restrict__ out0, AT* __restrict__ out1) {
-  static_assert(PD % 2 == 0, "the activation registers and LDS buffers alternate by stage");
-  __shared__ __attribute__((aligned(16))) uint8_t buf[2][32 * MT * kRowBytes];
-  // the tiles of an item run on one XCD (they share its activation rows) once
-  // there are items for every XCD; with fewer, consecutive tiles on all of them
-  const int blk = blockIdx.x;
-  int i, nt;
-  if (a.items >= 4 * kXcds) {
-    i = blk % kXcds + kXcds * (blk / (kXcds * a.ntiles));
-    nt = (blk / kXcds) % a.ntiles;
-  } else {
-    i = blk / a.ntiles;
-    nt = blk % a.ntiles;
-  }
-  int e, r0, m;
-  if (!mx_item(a.expert_off, a.E, i, 32 * MT, e, r0, m)) return;
-  const int tid = threadIdx.x, lane = tid % kWave, half = lane / 32, col = lane % 32;
-  const int tile = nt * kMgWaves + __builtin_amdgcn_readfirstlane(tid / kWave);
-  const int I = a.R / 2, nb = a.nb, S = (nb + kStB - 1) / kStB;
-  const bool live = tile * 32 < a.R;
-  // weight row of this lane (dead waves repeat row 0: they still copy and meet the barriers)
-  int n = 0;
-  if (live) n = GU ? (col < 16 ? tile * 16 + col : I + tile * 16 + col - 16) : tile * 32 + col;
-  const uint8_t* wq = a.wq + (size_t)e * a.R * (16 * nb);
-  const uint8_t* ws = a.ws + (size_t)e * a.R * nb;
-  const uint32_t wq_n = (uint32_t)a.R * (16 * nb), ws_n = (uint32_t)a.R * nb;
-  const uint32_t qo = (uint32_t)n * (16 * nb), so = (uint32_t)n * nb;
-  auto load_w = [&](int s, MxW& w) __attribute__((always_inline)) {
-    mx_load_w<TAIL>(mx_buffer(wq, s < S ? wq_n : 0), mx_buffer(ws, s < S ? ws_n : 0), qo, so, s, half, nb, w);
-  };
-  MxW w[PD];
+// The results of one 32-row weight tile for NA x 32 rows from sorted row r0 (m
+// of them live). GU: out0 = gate_up or NULL, out1 = act or NULL; else out0 = y.
+template <bool GU, int NA, typename AT>
+__device__ __forceinline__ void mx_store(const f32x16 (&acc)[NA], int tile, int R, int r0, int m, float* out0,
+                                         AT* out1) {
+  const int lane = threadIdx.x % kWave, half = lane / 32, col = lane % 32, I = R / 2;
+  // uniform bases and 32-bit lane offsets, opaque so that the compiler does not
+  // keep the addresses of every store across the tiles
+  uint32_t og = (uint32_t)(col * R + 4 * half), oa = (uint32_t)(col * I + 4 * half);
+  asm volatile("" : "+v"(og), "+v"(oa));
 #pragma unroll
-  for (int d = 0; d < PD; ++d) load_w(d, w[d]);
+  for (int q = 0; q < NA; ++q) {
+    if (32 * q + col >= m) continue;
+    if constexpr (GU) {
+      float* g_b = out0 ? out0 + (size_t)(r0 + 32 * q) * R + tile * 16 : nullptr;
+      AT* a_b = out1 ? out1 + (size_t)(r0 + 32 * q) * I + tile * 16 : nullptr;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        // gate rows 8 h + 4 half .. +3 of the tile in registers 4 h .. +3, their up rows in 8 + 4 h .. +3
+        f32x4 g, u, v;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          g[j] = acc[q][4 * h + j];
+          u[j] = acc[q][8 + 4 * h + j];
+          v[j] = gelu_tanh(g[j]) * u[j];
+        }
+        if (g_b) {
+          put4(g_b + (og + 8 * h), g);
+          put4(g_b + (og + I + 8 * h), u);
+        }
+        if (a_b) put4(a_b + (oa + 8 * h), v);
+      }
+    } else {
+      float* y_b = out0 + (size_t)(r0 + 32 * q) * R + tile * 32;
+#pragma unroll
+      for (int h = 0; h < 4; ++h)
+        put4(y_b + (og + 8 * h), f32x4{acc[q][4 * h], acc[q][4 * h + 1], acc[q][4 * h + 2], acc[q][4 * h + 3]});
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Activation rows resident in LDS, weights streamed
+
+constexpr int kSmThreads = 512;                   // 8 waves, two a SIMD
+constexpr int kSmWaves = kSmThreads / kWave;
+constexpr int kSmBlocks = 256;                    // one workgroup a CU
+constexpr int kSmX = 128 * 1104;                  // LDS for activation rows: 128 of K = 2048
+constexpr int kSmGroup = 64;                      // blocks of a row whose scales a wave holds at a time
+constexpr int kSmSc = 32 * kSmGroup + 16;         // LDS for a wave's scales: a tile's 32 rows
+
+// how a wave copies its tile's scales to LDS
+enum class MxSc {
+  kRun,     // nb <= 64: whole rows, one or two contiguous runs of 16 nb or 32 nb bytes
+  kPiece,   // 64 blocks of each row at a time, 16 bytes a load (nb % 16 == 0)
+  kWord     // the same, 4 bytes a load (nb % 4 == 0)
+};
+
+template <bool GU, int MT, int PD, MxSc SM, typename AT>
+__global__ void __launch_bounds__(kSmThreads, 2)
+k_mx_stream(const MxArgs a, float* __restrict__ out0, AT* __restrict__ out1) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds_x[kSmX];
+  __shared__ __attribute__((aligned(16))) uint8_t lds_sc[kSmWaves][kSmSc];
+  __shared__ uint32_t lds_row[32 * MT];
+  const int tid = threadIdx.x, lane = tid % kWave, half = lane / 32, col = lane % 32;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int R = a.R, I = R / 2, nb = a.nb, S = (nb + kStB - 1) / kStB, SP = (S + PD - 1) / PD * PD;
+  const int row_bytes = a.row_bytes, pieces = row_bytes / 16, xsc = S * 128;   // xsc: a row's scales
+  const uint32_t wq_n = (uint32_t)R * (16 * nb), ws_n = (uint32_t)R * nb;
+
+  // this workgroup's run of (pass, tile) pairs; neighbouring runs on one XCD
+  const int64_t total = (int64_t)a.items[0].e * a.ntiles;
+  const int rank = blockIdx.x % kXcds * (kSmBlocks / kXcds) + blockIdx.x / kXcds;
+  int64_t u = total * rank / kSmBlocks;
+  const int64_t end = total * (rank + 1) / kSmBlocks;
+
+  while (u < end) {
+    const int64_t idx = u / a.ntiles;
+    const int t0 = (int)(u - idx * a.ntiles), tend = (int)min((int64_t)a.ntiles, t0 + (end - u));
+    u += tend - t0;
+    const MxItem it = a.items[1 + idx];
+    const int e = it.e, r0 = it.r0, m = it.m;
+    const uint8_t* wq = a.wq + (size_t)e * wq_n;
+    const uint8_t* ws = a.ws + (size_t)e * ws_n;
+    // offsets of the lane's row of tile 0; tstep rows further on for each tile
+    const int n0 = GU ? (col < 16 ? col : I + col - 16) : col;
+    constexpr int tstep = GU ? 16 : 32;
+    const uint32_t qo = (uint32_t)n0 * (16 * nb) + 64 * half;
+
+    // stage s of the wave's tile t, or past SP of its next one
+    u32x4 w[PD][4];
+    auto load_w = [&](int t, int s, int d) __attribute__((always_inline)) {
+      if (s >= SP) {
+        s -= SP;
+        t += kSmWaves;
+      }
+      const mx_rsrc q = mx_buffer(wq, s < S && t < tend ? wq_n : 0);
+      const uint32_t o = qo + ((uint32_t)(t * tstep) * (16 * nb) + 128 * s);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[d][j] = mx_get16(q, o + 16 * j);
+    };
+    // scales of tile t, blocks 64 g and on (g past the last group: of the next tile)
+    const int groups = SM == MxSc::kRun ? 1 : (nb + kSmGroup - 1) / kSmGroup;
+    u32x4 sr[2];
+    auto load_sc = [&](int t, int g) __attribute__((always_inline)) {
+      if (g >= groups) {
+        g = 0;
+        t += kSmWaves;
+      }
+      const mx_rsrc r = mx_buffer(ws, t < tend ? ws_n : 0);
+      const uint32_t b0 = (uint32_t)(t * tstep) * nb;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int p = lane + i * kWave;
+        if constexpr (SM == MxSc::kRun) {
+          // 2 nb pieces; for gate_up the second half is the run of up rows
+          sr[i] = mx_get16(r, b0 + 16 * p + (GU && p >= nb ? (uint32_t)(I - 16) * nb : 0u));
+        } else {
+          // piece p % 4 of row p / 4
+          const int row = p / 4, n = GU && row >= 16 ? I + row - 16 : row;
+          const uint32_t o = b0 + (uint32_t)n * nb + kSmGroup * g + 16 * (p % 4);
+          if constexpr (SM == MxSc::kPiece) sr[i] = mx_get16(r, o);
+          else sr[i] = u32x4{mx_get4(r, o), mx_get4(r, o + 4), mx_get4(r, o + 8), mx_get4(r, o + 12)};
+        }
+      }
+    };
+    auto store_sc = [&]() __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) *reinterpret_cast<u32x4*>(&lds_sc[wave][16 * (lane + i * kWave)]) = sr[i];
+    };
+    const int lsc = col * (SM == MxSc::kRun ? nb : kSmGroup) + 4 * half;
+
+    int t = t0 + wave;
+#pragma unroll
+    for (int d = 0; d < PD; ++d) load_w(t, d, d);
+    load_sc(t, 0);
+
+    // the pass's activation rows
+    lds_barrier();   // no wave still reads the last pass's
+    if (tid < m) lds_row[tid] = (uint32_t)(GU ? a.sorted_pairs[r0 + tid] / a.topk : r0 + tid) * (uint32_t)row_bytes;
+    lds_barrier();
+    {
+      constexpr int U = 4;
+      const int n = m * pieces;
+      const mx_rsrc x = mx_buffer(a.x, a.x_n);
+      for (int p0 = tid; p0 < n; p0 += U * kSmThreads) {
+        u32x4 v[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const int p = min(p0 + i * kSmThreads, n - 1), row = p / pieces;
+          v[i] = mx_get16(x, lds_row[row] + 16 * (p - row * pieces));
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const int p = min(p0 + i * kSmThreads, n - 1);
+          *reinterpret_cast<u32x4*>(&lds_x[16 * p]) = v[i];
+        }
+      }
+    }
+    lds_barrier();
+
+    auto run = [&](auto na_c) __attribute__((always_inline)) {
+      constexpr int NA = decltype(na_c)::value;   // live 32-row tiles of the pass
+      for (; t < tend; t += kSmWaves) {
+        f32x16 acc[NA];
+#pragma unroll
+        for (int q = 0; q < NA; ++q) acc[q] = f32x16{};
+        for (int s0 = 0; s0 < SP; s0 += PD) {
+          if (s0 % kStB == 0) {
+            store_sc();
+            load_sc(t, s0 / kStB + 1);
+          }
+#pragma unroll
+          for (int d = 0; d < PD; ++d) {
+            const int s = s0 + d;
+            // stages past the last one multiply its zero weights with stage 0's codes
+            const int sx = s < S ? s : 0;
+            uint32_t sw;
+            if constexpr (SM == MxSc::kRun) {
+              const int o = lsc + kStB * sx;   // the four bytes may start anywhere
+              const uint32_t* p = reinterpret_cast<const uint32_t*>(&lds_sc[wave][o & ~3]);
+              sw = __builtin_amdgcn_alignbyte(p[1], p[0], o & 3);
+            } else {
+              sw = *reinterpret_cast<const uint32_t*>(&lds_sc[wave][lsc + kStB * (s % kStB)]);
+            }
+            sw = mx_mask_scales(sw, nb - kStB * s - 4 * half);
+            const uint8_t* x = &lds_x[col * row_bytes + 128 * sx + 64 * half];
+            uint32_t xs[NA];
+#pragma unroll
+            for (int q = 0; q < NA; ++q)
+              xs[q] = *reinterpret_cast<const uint32_t*>(&lds_x[(32 * q + col) * row_bytes + xsc + kStB * sx + 4 * half]);
+            auto step = [&](auto jc) __attribute__((always_inline)) {
+              constexpr int J = decltype(jc)::value;
+#pragma unroll
+              for (int q = 0; q < NA; ++q) {
+                const u32x4 xv = *reinterpret_cast<const u32x4*>(x + 32 * q * row_bytes + 16 * J);
+                acc[q] = mx_mfma32<J, J>(w[d][J], xv, acc[q], sw, xs[q]);
+              }
+            };
+            step(std::integral_constant<int, 0>{});
+            step(std::integral_constant<int, 1>{});
+            step(std::integral_constant<int, 2>{});
+            step(std::integral_constant<int, 3>{});
+            __builtin_amdgcn_sched_barrier(0);   // the next use of these registers is loaded after their products
+            load_w(t, s + PD, d);
+          }
+        }
+        mx_store<GU, NA>(acc, t, R, r0, m, out0, out1);
+      }
+    };
+    const int na = (m + 31) / 32;
+    if (MT >= 4 && na == 4) run(std::integral_constant<int, 4>{});
+    else if (MT >= 3 && na == 3) run(std::integral_constant<int, 3>{});
+    else if (MT >= 2 && na == 2) run(std::integral_constant<int, 2>{});
+    else run(std::integral_constant<int, 1>{});
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Long rows: activation rows in stages through LDS. A work item is one pass x
+// 128 weight rows, a workgroup of 4 waves, a 32-row tile each; weights and
+// their scales from memory into registers two stages ahead, activation rows
+// double-buffered in LDS.
+
+constexpr int kRgThreads = 256;
+constexpr int kRgWaves = kRgThreads / kWave;
+constexpr int kRgTile = 144;                 // a row's stage in LDS: 128 B of codes, 8 scales, 8 B unused
+constexpr int kRgPieces = kRgTile / 16;
+constexpr int kRgMt = 3;
+
+template <bool GU, typename AT>
+__global__ void __launch_bounds__(kRgThreads, 2)
+k_mx_ring(const MxArgs a, float* __restrict__ out0, AT* __restrict__ out1) {
+  constexpr int PD = 2;   // stages of weights in flight; also the parity of the LDS buffers
+  __shared__ __attribute__((aligned(16))) uint8_t buf[2][32 * kRgMt * kRgTile];
+  const int ntg = (a.ntiles + kRgWaves - 1) / kRgWaves;
+  const int i = blockIdx.x / ntg;
+  if (i >= a.items[0].e) return;
+  const MxItem it = a.items[1 + i];
+  const int e = it.e, r0 = it.r0, m = it.m;
+  const int tid = threadIdx.x, lane = tid % kWave, half = lane / 32, col = lane % 32;
+  const int tile = blockIdx.x % ntg * kRgWaves + __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int R = a.R, I = R / 2, nb = a.nb, S = (nb + kStB - 1) / kStB;
+  const uint32_t wq_n = (uint32_t)R * (16 * nb), ws_n = (uint32_t)R * nb;
+  const uint8_t* wq = a.wq + (size_t)e * wq_n;
+  const uint8_t* ws = a.ws + (size_t)e * ws_n;
+  const bool live = tile < a.ntiles;   // dead waves read zeros; they still copy and meet the barriers
+  const int n = GU ? tile * 16 + (col < 16 ? col : I + col - 16) : tile * 32 + col;
+  const uint32_t qo = (uint32_t)n * (16 * nb) + 64 * half, so = (uint32_t)n * nb + 4 * half;
+  u32x4 w[PD][4];
+  uint32_t wsc[PD];
+  auto load_w = [&](int s, int d) __attribute__((always_inline)) {
+    const bool on = live && s < S;
+    const mx_rsrc q = mx_buffer(wq, on ? wq_n : 0), c = mx_buffer(ws, on ? ws_n : 0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[d][j] = mx_get16(q, qo + 128 * s + 16 * j);
+    // rows of scales may start anywhere: two aligned words hold the four bytes
+    const uint32_t o = so + kStB * s;
+    wsc[d] = mx_mask_scales(__builtin_amdgcn_alignbyte(mx_get4(c, (o & ~3u) + 4), mx_get4(c, o & ~3u), o & 3),
+                            nb - kStB * s - 4 * half);
+  };
+#pragma unroll
+  for (int d = 0; d < PD; ++d) load_w(d, d);
 
   auto run = [&](auto na_c) __attribute__((always_inline)) {
     constexpr int NA = decltype(na_c)::value;   // live 32-row tiles of the pass
-    // activation pieces this thread copies: 16 bytes of row 32 q + tid / 8; the
-    // scales (8 bytes) of row tid % (32 NA): several threads write the same bytes,
-    // with no branch (rows past the pass repeat its last one)
-    uint32_t xo[NA], xso;
-    {
-      auto src = [&](int row) {
-        const int r = r0 + min(row, m - 1);
-        return (uint32_t)(GU ? a.sorted_pairs[r] / a.topk : r);
-      };
+    // activation pieces this thread copies: 16 bytes of a row's stage, pieces
+    // tid, tid + 256, .. of the pass (rows past it repeat its last one); piece 8
+    // of a row is its stage's scales and the 8 bytes behind them
+    constexpr int kPieces = 32 * NA * kRgPieces, kCopies = (kPieces + kRgThreads - 1) / kRgThreads;
+    uint32_t xo[kCopies];
+    int xstep[kCopies];
 #pragma unroll
-      for (int q = 0; q < NA; ++q) xo[q] = src(32 * q + tid / 8) * (uint32_t)(128 * S) + 16 * (tid % 8);
-      xso = src(tid % (32 * NA)) * (uint32_t)(8 * S);
+    for (int q = 0; q < kCopies; ++q) {
+      const int p = min(tid + q * kRgThreads, kPieces - 1), row = p / kRgPieces, c = p - row * kRgPieces;
+      const int r = r0 + min(row, m - 1);
+      xo[q] = (uint32_t)(GU ? a.sorted_pairs[r] / a.topk : r) * (uint32_t)a.row_bytes + (c < kStB ? 16 * c : 128 * S);
+      xstep[q] = c < kStB ? 128 : kStB;
     }
-    u32x4 xr[2][NA];
-    uint32_t sr[2][2];
-    auto load_x = [&](int s, u32x4 (&xr)[NA], uint32_t (&sr)[2]) __attribute__((always_inline)) {
-      const mx_rsrc q = mx_buffer(a.xq, s < S ? a.xq_n : 0), c = mx_buffer(a.xs, s < S ? a.xq_n / 16 : 0);
+    u32x4 xr[2][kCopies];
+    auto load_x = [&](int s, u32x4 (&xr)[kCopies]) __attribute__((always_inline)) {
+      const mx_rsrc q = mx_buffer(a.x, s < S ? a.x_n : 0);
 #pragma unroll
-      for (int i = 0; i < NA; ++i) xr[i] = mx_get16(q, xo[i] + 128 * s);
-      sr[0] = mx_get4(c, xso + 8 * s);
-      sr[1] = mx_get4(c, xso + 8 * s + 4);
+      for (int i = 0; i < kCopies; ++i) xr[i] = mx_get16(q, xo[i] + xstep[i] * s);
     };
-    auto store_x = [&](int b, const u32x4 (&xr)[NA], const uint32_t (&sr)[2]) __attribute__((always_inline)) {
+    auto store_x = [&](int b, const u32x4 (&xr)[kCopies]) __attribute__((always_inline)) {
+      // threads past the last piece write that piece again: no branch
 #pragma unroll
-      for (int q = 0; q < NA; ++q)
-        *reinterpret_cast<u32x4*>(&buf[b][(32 * q + tid / 8) * kRowBytes + 16 * (tid % 8)]) = xr[q];
-      *reinterpret_cast<u32x2*>(&buf[b][(tid % (32 * NA)) * kRowBytes + 128]) = u32x2{sr[0], sr[1]};
+      for (int i = 0; i < kCopies; ++i)
+        *reinterpret_cast<u32x4*>(&buf[b][16 * min(tid + i * kRgThreads, kPieces - 1)]) = xr[i];
     };
 
     f32x16 acc[NA];
 #pragma unroll
     for (int q = 0; q < NA; ++q) acc[q] = f32x16{};
-    load_x(0, xr[0], sr[0]);
-    load_x(1, xr[1], sr[1]);
-    store_x(0, xr[0], sr[0]);
-    load_x(2, xr[0], sr[0]);
+    load_x(0, xr[0]);
+    load_x(1, xr[1]);
+    store_x(0, xr[0]);
+    load_x(2, xr[0]);
     lds_barrier();
-    // stages past the last one (S up to a multiple of PD) add products with zero codes
+    // a stage past the last one (S odd) adds products with zero codes
     for (int s0 = 0; s0 < S; s0 += PD) {
 #pragma unroll
       for (int d = 0; d < PD; ++d) {
         const int s = s0 + d;
-        const uint8_t* x = &buf[s & 1][col * kRowBytes + 64 * half];
+        const uint8_t* x = &buf[d][col * kRgTile + 64 * half];
         uint32_t xs[NA];
 #pragma unroll
         for (int q = 0; q < NA; ++q)
-          xs[q] = *reinterpret_cast<const uint32_t*>(&buf[s & 1][(32 * q + col) * kRowBytes + 128 + 4 * half]);
+          xs[q] = *reinterpret_cast<const uint32_t*>(&buf[d][(32 * q + col) * kRgTile + 128 + 4 * half]);
         auto step = [&](auto jc) __attribute__((always_inline)) {
           constexpr int J = decltype(jc)::value;
 #pragma unroll
           for (int q = 0; q < NA; ++q) {
-            const u32x4 xv = *reinterpret_cast<const u32x4*>(x + 32 * q * kRowBytes + 16 * J);
-            acc[q] = mx_mfma32<J, J>(w[d].q[J], xv, acc[q], w[d].s, xs[q]);
+            const u32x4 xv = *reinterpret_cast<const u32x4*>(x + 32 * q * kRgTile + 16 * J);
+            acc[q] = mx_mfma32<J, J>(w[d][J], xv, acc[q], wsc[d], xs[q]);
           }
         };
         step(std::integral_constant<int, 0>{});
         step(std::integral_constant<int, 1>{});
         step(std::integral_constant<int, 2>{});
         step(std::integral_constant<int, 3>{});
-        __builtin_amdgcn_sched_barrier(0);   // the next use of these registers is loaded after their products
-        load_w(s + PD, w[d]);
-        store_x((s + 1) & 1, xr[(d + 1) & 1], sr[(d + 1) & 1]);
-        load_x(s + 3, xr[(d + 1) & 1], sr[(d + 1) & 1]);
+        __builtin_amdgcn_sched_barrier(0);
+        load_w(s + PD, d);
+        store_x(d ^ 1, xr[d ^ 1]);
+        load_x(s + 3, xr[d ^ 1]);
         lds_barrier();
       }
     }
-    if (!live) return;
-#pragma unroll
-    for (int q = 0; q < NA; ++q) {
-      if (32 * q + col >= m) continue;
-      const size_t r = (size_t)r0 + 32 * q + col;
-      if constexpr (GU) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          // gate rows 8 h + 4 half .. +3 of the tile in registers 4 h .. +3, their up rows in 8 + 4 h .. +3
-          const int i0 = tile * 16 + 8 * h + 4 * half;
-          f32x4 g, u, v;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            g[j] = acc[q][4 * h + j];
-            u[j] = acc[q][8 + 4 * h + j];
-            v[j] = gelu_tanh(g[j]) * u[j];
-          }
-          if (out0) {
-            put4(out0 + r * a.R + i0, g);
-            put4(out0 + r * a.R + I + i0, u);
-          }
-          if (out1) put4(out1 + r * I + i0, v);
-        }
-      } else {
-#pragma unroll
-        for (int h = 0; h < 4; ++h)
-          put4(out0 + r * a.R + tile * 32 + 8 * h + 4 * half,
-               f32x4{acc[q][4 * h], acc[q][4 * h + 1], acc[q][4 * h + 2], acc[q][4 * h + 3]});
-      }
-    }
+    if (live) mx_store<GU, NA>(acc, tile, R, r0, m, out0, out1);
   };
   const int na = (m + 31) / 32;
-  if constexpr (MT == 1) {
-    run(std::integral_constant<int, 1>{});
-  } else if constexpr (MT == 2) {
-    if (na == 1) run(std::integral_constant<int, 1>{});
-    else run(std::integral_constant<int, 2>{});
-  } else {
-    switch (na) {
-      case 1: run(std::integral_constant<int, 1>{}); break;
-      case 2: run(std::integral_constant<int, 2>{}); break;
-      case 3: run(std::integral_constant<int, 3>{}); break;
-      case 4: run(std::integral_constant<int, 4>{}); break;
-      default: run(std::integral_constant<int, 5>{}); break;
+  if (na == 3) run(std::integral_constant<int, 3>{});
+  else if (na == 2) run(std::integral_constant<int, 2>{});
+  else run(std::integral_constant<int, 1>{});
+}
+
+// ---------------------------------------------------------------------------
+
+// What the products need ready, in one launch: workgroup 0 lists the passes
+// (an expert of m > 0 rows has n = ceil(m / rows) of them, of ceil(m / n) rows
+// each, so that they take alike), the others quantise the activation rows, eight
+// values a thread, into rows of nbp blocks of codes and their scales; the blocks
+// behind a row hold zero codes with scale 1.
+template <typename XT>
+__global__ void __launch_bounds__(kPrThreads)
+k_mx_prepare(const XT* __restrict__ x, int64_t n8, int nb, int nbp, int row_bytes, uint8_t* __restrict__ rows_out,
+             const int32_t* __restrict__ off, int E, int rows, MxItem* __restrict__ items) {
+  const int tid = threadIdx.x;
+  if (blockIdx.x == 0) {
+    __shared__ int s_off[kMaxExperts + 1], s_first[kMaxExperts + 1];
+    __shared__ int s_wave[kPrThreads / kWave];
+    for (int i = tid; i <= E; i += kPrThreads) s_off[i] = off[i];
+    __syncthreads();
+    constexpr int kPer = kMaxExperts / kPrThreads;   // consecutive experts a thread counts
+    int n[kPer], sum = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int e = kPer * tid + j;
+      n[j] = e < E ? (s_off[e + 1] - s_off[e] + rows - 1) / rows : 0;
+      sum += n[j];
     }
+    int inc = sum;
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+      const int o = __shfl_up(inc, d, kWave);
+      if (tid % kWave >= d) inc += o;
+    }
+    if (tid % kWave == kWave - 1) s_wave[tid / kWave] = inc;
+    __syncthreads();
+    int first = inc - sum;
+    for (int w = 0; w < tid / kWave; ++w) first += s_wave[w];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int e = kPer * tid + j;
+      if (e < E) s_first[e] = first;
+      first += n[j];
+      if (e == E - 1) s_first[E] = first;
+    }
+    __syncthreads();
+    const int total = s_first[E];
+    if (tid == 0) items[0] = MxItem{total, 0, 0, 0};
+    for (int i = tid; i < total; i += kPrThreads) {
+      int lo = 0, hi = E;   // the last expert whose first pass is at or before i: it has passes
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (s_first[mid] <= i) lo = mid;
+        else hi = mid;
+      }
+      const int m = s_off[lo + 1] - s_off[lo], passes = s_first[lo + 1] - s_first[lo];
+      const int per = (m + passes - 1) / passes, p = i - s_first[lo];
+      items[1 + i] = MxItem{lo, s_off[lo] + p * per, max(0, min(per, m - p * per)), 0};
+    }
+    return;
   }
+  const int64_t i = (int64_t)(blockIdx.x - 1) * kPrThreads + tid;
+  float v[8] = {};
+  const int64_t row = (i / 4) / nbp;
+  const int b = (int)(i / 4 - row * nbp);
+  if (i < n8 && b < nb) mx_load8(x + (row * nb + b) * kMxBlock + 8 * (i & 3), v);
+  int s;
+  const uint32_t c = mx_quant8(v, s);   // n8 is a multiple of 4: a block's four lanes are all in or all out
+  if (i >= n8) return;
+  uint8_t* o = rows_out + row * row_bytes;
+  *reinterpret_cast<uint32_t*>(o + 16 * b + 4 * (i & 3)) = c;
+  if ((i & 3) == 0) o[16 * nbp + b] = (uint8_t)(b < nb ? s : 127);
 }
 
 // out[t, h .. h + 3] = sum_j w[t, j] y[pos[t k + j], h .. h + 3], slot order
-__global__ void __launch_bounds__(kMgThreads)
+__global__ void __launch_bounds__(kPrThreads)
 k_mx_combine(const float* __restrict__ y, int H, int k, const float* __restrict__ tw, const int32_t* __restrict__ pos,
              float* __restrict__ out) {
   const int64_t t = blockIdx.x;
-  const int h = 4 * (blockIdx.y * kMgThreads + threadIdx.x);
+  const int h = 4 * (blockIdx.y * kPrThreads + threadIdx.x);
   if (h >= H) return;
   f32x4 o = {0.f, 0.f, 0.f, 0.f};
   for (int j = 0; j < k; ++j) {
@@ -311,48 +520,91 @@ k_mx_combine(const float* __restrict__ y, int H, int k, const float* __restrict_
 
 }  // namespace
 
-template <bool GU, typename AT>
-static hipError_t mx_grouped(MxArgs a, int64_t P, int64_t rows, float* out0, AT* out1, hipStream_t st) {
-  // rows per pass by the average expert: passes of 32 rows while experts hold a
-  // dozen pairs, of 160 (a prefill expert's 128 on average, with its spread) for many
-  const int mt = P <= 16 * (int64_t)a.E ? 1 : P <= 40 * (int64_t)a.E ? 2 : 5;
-  a.ntiles = cdiv(a.R, kMgRows);
-  a.xq_n = (uint32_t)(rows * cdiv(a.nb, kStB) * 128);
+// How a product of rows of K is run: the passes' rows and the kernel
+struct MxPlan {
+  int nb, nbp, row_bytes, mt;
+  bool stream;
+  MxPlan(int K, int64_t P, int E) {
+    nb = K / kMxBlock;
+    nbp = cdiv(nb, kStB) * kStB;
+    row_bytes = (cdiv(17 * nbp, 16) | 1) * 16;   // an odd number of 16-byte pieces: 16 rows meet all LDS banks
+    // rows per pass by the average expert: 32 while experts hold a dozen pairs
+    // (a verify batch), up to 128 for many, as far as the rows fit LDS
+    const int want = P <= 16 * (int64_t)E ? 1 : P <= 40 * (int64_t)E ? 2 : 4;
+    const int fit = kSmX / (32 * row_bytes);
+    stream = fit >= 1 && (nb <= kSmGroup || nb % 4 == 0);
+    mt = stream ? (want <= fit ? want : fit >= 2 ? 2 : 1) : kRgMt;
+  }
   // every non-empty expert has at most one pass that is not full
-  const int64_t items = P / (32 * mt) + (P < a.E ? P : a.E);
-  const int64_t grid = (items + kXcds - 1) / kXcds * kXcds * a.ntiles;
-  if (grid >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
-  a.items = (int)items;
-  const bool tail = a.nb % kStB != 0;
-  const unsigned g = (unsigned)grid;
-#define I8H_MX(M, PD)                                                            \
-  do {                                                                           \
-    if (tail) k_mx_grouped<GU, M, true, PD><<<g, kMgThreads, 0, st>>>(a, out0, out1);  \
-    else k_mx_grouped<GU, M, false, PD><<<g, kMgThreads, 0, st>>>(a, out0, out1);      \
-  } while (0)
-  if (mt == 1) I8H_MX(1, 2);
-  else if (mt == 2) I8H_MX(2, 2);
-  else I8H_MX(5, 2);
+  int64_t passes(int64_t P, int E) const { return P / (32 * mt) + (P < E ? P : E); }
+};
+
+MxWorkspace::MxWorkspace(int64_t rows, int K, int64_t P, int E) {
+  const auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+  const MxPlan plan(K, P, E);
+  items = up((size_t)rows * plan.row_bytes + 16);   // reads of a row's scales run up to 8 bytes past it
+  total = items + up((size_t)(1 + plan.passes(P, E)) * sizeof(MxItem));
+}
+
+template <bool GU, typename XT, typename AT>
+static hipError_t mx_grouped(const XT* x, int64_t rows, int K, int64_t P, const uint8_t* codes, const uint8_t* scales,
+                             int E, int R, int topk, const int32_t* expert_off, const int32_t* sorted_pairs,
+                             uint8_t* ws, float* out0, AT* out1, hipStream_t st) {
+  const MxWorkspace lay(rows, K, P, E);
+  const MxPlan plan(K, P, E);
+  const int64_t n8 = rows * plan.nbp * 4, qgrid = 1 + (n8 + kPrThreads - 1) / kPrThreads;
+  const int ntiles = R / 32;
+  const int64_t rgrid = plan.passes(P, E) * cdiv(ntiles, kRgWaves);
+  if (qgrid >= ((int64_t)1 << 31) || (!plan.stream && rgrid >= ((int64_t)1 << 31))) return hipErrorInvalidValue;
+  MxItem* items = reinterpret_cast<MxItem*>(ws + lay.items);
+  k_mx_prepare<<<(unsigned)qgrid, kPrThreads, 0, st>>>(x, n8, plan.nb, plan.nbp, plan.row_bytes, ws, expert_off, E,
+                                                       32 * plan.mt, items);
+  const hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return err;
+  const MxArgs a = {ws, codes, scales, (uint32_t)(rows * plan.row_bytes + 16), plan.row_bytes, E, R, plan.nb, topk,
+                    ntiles, items, sorted_pairs};
+#define I8H_MX(M, D, S) k_mx_stream<GU, M, D, MxSc::S><<<kSmBlocks, kSmThreads, 0, st>>>(a, out0, out1)
+  if (!plan.stream) {
+    k_mx_ring<GU><<<(unsigned)rgrid, kRgThreads, 0, st>>>(a, out0, out1);
+  } else if (plan.nb <= kSmGroup) {
+    // short rows (up to 4 stages) would fill half of an 8-deep prefetch
+    if (plan.mt == 1 && plan.nb > 4 * kStB) I8H_MX(1, 8, kRun);
+    else if (plan.mt == 1) I8H_MX(1, 4, kRun);
+    else if (plan.mt == 2) I8H_MX(2, 4, kRun);
+    else I8H_MX(4, 4, kRun);
+  } else if (plan.nb % 16 == 0) {
+    if (plan.mt == 1) I8H_MX(1, 8, kPiece);
+    else I8H_MX(2, 4, kPiece);
+  } else {
+    if (plan.mt == 1) I8H_MX(1, 8, kWord);
+    else I8H_MX(2, 4, kWord);
+  }
 #undef I8H_MX
   return hipGetLastError();
 }
 
-hipError_t launch_gateup_mxfp4(const uint8_t* xq, const uint8_t* xs, int T, int K, const uint8_t* codes,
-                               const uint8_t* scales, int E, int N, int k, const int32_t* expert_off,
-                               const int32_t* sorted_pairs, float* gu, void* act, bool act_bf16, hipStream_t st) {
-  const MxArgs a = {xq, xs, codes, scales, 0, E, N, K / kMxBlock, k, 0, 0, expert_off, sorted_pairs};
+hipError_t launch_gateup_mxfp4(const uint16_t* x, int T, int K, const uint8_t* codes, const uint8_t* scales, int E,
+                               int N, int k, const int32_t* expert_off, const int32_t* sorted_pairs, float* gu,
+                               void* act, bool act_bf16, uint8_t* ws, hipStream_t st) {
   const int64_t P = (int64_t)T * k;
-  return act_bf16 ? mx_grouped<true>(a, P, T, gu, static_cast<uint16_t*>(act), st)
-                  : mx_grouped<true>(a, P, T, gu, static_cast<float*>(act), st);
+  return act_bf16 ? mx_grouped<true>(x, T, K, P, codes, scales, E, N, k, expert_off, sorted_pairs, ws, gu,
+                                     static_cast<uint16_t*>(act), st)
+                  : mx_grouped<true>(x, T, K, P, codes, scales, E, N, k, expert_off, sorted_pairs, ws, gu,
+                                     static_cast<float*>(act), st);
 }
 
-hipError_t launch_down_mxfp4(const uint8_t* aq, const uint8_t* as, int T, int I, const uint8_t* codes,
+hipError_t launch_down_mxfp4(const void* act, bool act_bf16, int T, int I, const uint8_t* codes,
                              const uint8_t* scales, int E, int H, int k, const float* tw, const int32_t* expert_off,
-                             const int32_t* pos, float* y, float* out, hipStream_t st) {
-  const MxArgs a = {aq, as, codes, scales, 0, E, H, I / kMxBlock, k, 0, 0, expert_off, nullptr};
-  const hipError_t err = mx_grouped<false>(a, (int64_t)T * k, (int64_t)T * k, y, static_cast<float*>(nullptr), st);
+                             const int32_t* pos, uint8_t* ws, float* y, float* out, hipStream_t st) {
+  const int64_t P = (int64_t)T * k;
+  float* const none = nullptr;
+  const hipError_t err =
+      act_bf16 ? mx_grouped<false>(static_cast<const uint16_t*>(act), P, I, P, codes, scales, E, H, k, expert_off,
+                                   nullptr, ws, y, none, st)
+               : mx_grouped<false>(static_cast<const float*>(act), P, I, P, codes, scales, E, H, k, expert_off,
+                                   nullptr, ws, y, none, st);
   if (err != hipSuccess) return err;
-  k_mx_combine<<<dim3(T, cdiv(H / 4, kMgThreads)), kMgThreads, 0, st>>>(y, H, k, tw, pos, out);
+  k_mx_combine<<<dim3(T, cdiv(H / 4, kPrThreads)), kPrThreads, 0, st>>>(y, H, k, tw, pos, out);
   return hipGetLastError();
 }
 

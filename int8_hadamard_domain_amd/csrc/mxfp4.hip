@@ -15,31 +15,18 @@ namespace {
 
 constexpr int kMxThreads = 256;
 
-// PAD: rows of nb blocks go to rows of nbp blocks (whole stages of the grouped
-// products); the blocks behind a row hold zero codes with scale 1.
-template <bool PAD, typename XT>
+template <typename XT>
 __global__ void __launch_bounds__(kMxThreads)
-k_mxfp4_quantize(const XT* __restrict__ x, int64_t n8, int nb, int nbp, uint32_t* __restrict__ codes,
-                 uint8_t* __restrict__ scales) {
-  // without padding rows are whole blocks, so the matrix is one run of blocks
+k_mxfp4_quantize(const XT* __restrict__ x, int64_t n8, uint32_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+  // rows are whole blocks, so the matrix is one run of blocks
   const int64_t i = (int64_t)blockIdx.x * kMxThreads + threadIdx.x;
   float v[8] = {};
-  bool fill = false;
-  if (i < n8) {   // n8 is a multiple of 4: a block's lanes are all in or all out
-    if constexpr (PAD) {
-      const int64_t row = (i / 4) / nbp;
-      const int b = (int)(i / 4 - row * nbp);
-      fill = b >= nb;
-      if (!fill) mx_load8(x + (row * nb + b) * kMxBlock + 8 * (threadIdx.x & 3), v);
-    } else {
-      mx_load8(x + 8 * i, v);
-    }
-  }
+  if (i < n8) mx_load8(x + 8 * i, v);   // n8 is a multiple of 4: a block's lanes are all in or all out
   int s;
   const uint32_t c = mx_quant8(v, s);
   if (i >= n8) return;
   codes[i] = c;
-  if ((threadIdx.x & 3) == 0) scales[i / 4] = (uint8_t)(fill ? 127 : s);
+  if ((threadIdx.x & 3) == 0) scales[i / 4] = (uint8_t)s;
 }
 
 // E2M1 code -> float: codes 0..7 are 0, 0.5, 1, 1.5, 2, 3, 4, 6
@@ -82,20 +69,15 @@ k_mxfp4_dequantize(const uint32_t* __restrict__ codes, const uint8_t* __restrict
 
 }  // namespace
 
-hipError_t launch_mxfp4_quantize(const void* x, bool bf16, int64_t rows, int K, int Kp, uint8_t* codes,
-                                 uint8_t* scales, hipStream_t st) {
-  const int64_t n8 = rows * (Kp / 8), grid = (n8 + kMxThreads - 1) / kMxThreads;
+hipError_t launch_mxfp4_quantize(const void* x, bool bf16, int64_t values, uint8_t* codes, uint8_t* scales,
+                                 hipStream_t st) {
+  const int64_t n8 = values / 8, grid = (n8 + kMxThreads - 1) / kMxThreads;
   if (grid >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
-  const int nb = K / kMxBlock, nbp = Kp / kMxBlock;
   uint32_t* c = reinterpret_cast<uint32_t*>(codes);
-  auto go = [&](auto* p) {
-    if (nb == nbp)
-      k_mxfp4_quantize<false><<<(unsigned)grid, kMxThreads, 0, st>>>(p, n8, nb, nbp, c, scales);
-    else
-      k_mxfp4_quantize<true><<<(unsigned)grid, kMxThreads, 0, st>>>(p, n8, nb, nbp, c, scales);
-  };
-  if (bf16) go(static_cast<const uint16_t*>(x));
-  else go(static_cast<const float*>(x));
+  if (bf16)
+    k_mxfp4_quantize<<<(unsigned)grid, kMxThreads, 0, st>>>(static_cast<const uint16_t*>(x), n8, c, scales);
+  else
+    k_mxfp4_quantize<<<(unsigned)grid, kMxThreads, 0, st>>>(static_cast<const float*>(x), n8, c, scales);
   return hipGetLastError();
 }
 
