@@ -117,6 +117,11 @@ def _dev(t, name, dtype, ndim=None, shape=None, device=None):
     """Check one tensor handed to the library: a torch.Tensor on the GPU (on
     `device` when given), of `dtype`, contiguous, with `ndim` dimensions or
     exactly `shape`. Raises TypeError / ValueError before anything is launched."""
+    # the fitting tensor in one test (a call's checks are part of its latency);
+    # the tests behind it only find what to say
+    if type(t) is torch.Tensor and t.dtype is dtype and t.is_cuda and (shape is None or t.shape == shape) \
+            and (ndim is None or t.dim() == ndim) and (device is None or t.device == device) and t.is_contiguous():
+        return t
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device.type != "cuda":
@@ -160,11 +165,12 @@ def _routing_outputs(out, T, E, topk, device):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    # the handle itself: building torch.cuda.current_stream()'s Stream object takes 2 us a call
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def moe_route_permute(logits, topk, out=None):
@@ -509,9 +515,22 @@ def _mx_weights(codes, scales, K, dev):
     return E, R
 
 
-def _rows(n):
-    if n >= 1 << 31:
-        raise ValueError(f"at most {(1 << 31) - 1} rows (got {n})")
+def _mx_out(t, name, shape, dtype, x):
+    """A caller's tensor, checked, or a new one beside x."""
+    if t is None:
+        return x.new_empty(shape, dtype=dtype)
+    return _dev(t, name, dtype, shape=shape, device=x.device)
+
+
+def _mx_shape(t, name, unit, per_row):
+    """(leading dimensions, last dimension, rows) of a matrix of whole blocks along its last dimension."""
+    shape = tuple(t.shape)
+    if not shape or shape[-1] == 0 or shape[-1] % unit:
+        raise ValueError(f"{name} must have a last dimension of whole blocks of {unit} (got {shape})")
+    rows = t.numel() // shape[-1]
+    if rows >= 1 << 31:
+        raise ValueError(f"{name} must have fewer than 2^31 rows (got {rows})")
+    return shape[:-1], shape[-1] * per_row, rows
 
 
 def mxfp4_quantize(x, codes=None, scales=None):
@@ -520,16 +539,11 @@ def mxfp4_quantize(x, codes=None, scales=None):
     the low nibble) and an E8M0 scale per 32 values."""
     xt = _type(x, "x")
     _dev(x, "x", x.dtype)
-    if x.dim() == 0 or x.shape[-1] == 0 or x.shape[-1] % 32:
-        raise ValueError(f"x must have a last dimension of whole blocks of 32 (got {tuple(x.shape)})")
-    lead, K = tuple(x.shape[:-1]), x.shape[-1]
-    _rows(x.numel() // K)
-    want = {"codes": lead + (K // 2,), "scales": lead + (K // 32,)}
-    codes, scales = (torch.empty(want[n], dtype=torch.uint8, device=x.device) if t is None
-                     else _dev(t, n, torch.uint8, shape=want[n], device=x.device)
-                     for n, t in (("codes", codes), ("scales", scales)))
+    lead, K, rows = _mx_shape(x, "x", 32, 1)
+    codes = _mx_out(codes, "codes", lead + (K // 2,), torch.uint8, x)
+    scales = _mx_out(scales, "scales", lead + (K // 32,), torch.uint8, x)
     _check("mxfp4_quantize", lib().mxfp4_quantize(
-        _ptr(x), xt, x.numel() // K, K, _ptr(codes), _ptr(scales), _stream(x.device)))
+        x.data_ptr(), xt, rows, K, codes.data_ptr(), scales.data_ptr(), _stream(x.device)))
     return codes, scales
 
 
@@ -537,19 +551,15 @@ def mxfp4_dequantize(codes, scales, dtype=torch.bfloat16, out=None):
     """The values of MXFP4 codes [..., K/2] and scales [..., K/32] (uint8) as
     [..., K] float32 or bfloat16 (dtype, or the dtype of a given out)."""
     _dev(codes, "codes", torch.uint8)
-    if codes.dim() == 0 or codes.shape[-1] == 0 or codes.shape[-1] % 16:
-        raise ValueError(f"codes must have a last dimension of whole blocks of 16 bytes (got {tuple(codes.shape)})")
-    lead, K = tuple(codes.shape[:-1]), 2 * codes.shape[-1]
-    _rows(codes.numel() * 2 // K)
+    lead, K, rows = _mx_shape(codes, "codes", 16, 2)
     _dev(scales, "scales", torch.uint8, shape=lead + (K // 32,), device=codes.device)
-    if out is None:
-        if dtype not in TYPES:
-            raise TypeError(f"dtype must be float32 or bfloat16 (got {dtype})")
-        out = torch.empty(lead + (K,), dtype=dtype, device=codes.device)
-    ot = _type(out, "out")
-    _dev(out, "out", out.dtype, shape=lead + (K,), device=codes.device)
+    if out is not None:
+        dtype = out.dtype if isinstance(out, torch.Tensor) else None
+    if dtype not in TYPES:
+        raise TypeError(f"dtype must be float32 or bfloat16 (got {dtype})")
+    out = _mx_out(out, "out", lead + (K,), dtype, codes)
     _check("mxfp4_dequantize", lib().mxfp4_dequantize(
-        _ptr(codes), _ptr(scales), codes.numel() * 2 // K, K, _ptr(out), ot, _stream(codes.device)))
+        codes.data_ptr(), scales.data_ptr(), rows, K, out.data_ptr(), TYPES[dtype], _stream(codes.device)))
     return out
 
 
