@@ -112,7 +112,7 @@ int moe_down_mxfp4_combine(const void* act, int act_type, int T, int I, const ui
 
 size_t draft_verify_workspace_size(int B, int V) {
   if (B <= 0 || V <= 0) return 0;
-  return round_up((size_t)B * i8h::draft_chunks(V) * 2 * sizeof(double), 256);
+  return round_up(i8h::draft_workspace_bytes(B, V), 256);
 }
 
 int draft_verify(const void* target_probs, const void* draft_probs, int prob_type, const int32_t* drafted,
@@ -129,7 +129,7 @@ int draft_verify(const void* target_probs, const void* draft_probs, int prob_typ
   if (!workspace || workspace_bytes < draft_verify_workspace_size(B, V) || !aligned(workspace, 256))
     return I8H_EINVAL;
   return from_hip(i8h::launch_draft_verify(target_probs, draft_probs, prob_type == I8H_BF16, drafted, draft_len, u,
-                                           u_next, B, D, V, static_cast<double*>(workspace), tokens, accepted,
+                                           u_next, B, D, V, workspace, tokens, accepted,
                                            as_stream(stream)));
 }
 

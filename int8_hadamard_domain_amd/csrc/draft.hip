@@ -10,8 +10,8 @@
 // cut into chunks, a workgroup each (k_draft_sums: the chunk's sum in float64,
 // fixed order, no atomics on floats), and one workgroup a sequence then finds
 // the chunk that the draw falls into and reads only that one again
-// (k_draft_pick). Which row it is costs a handful of loads, so every workgroup
-// finds it for itself.
+// (k_draft_pick). Which row it is costs two dependent loads, so every workgroup
+// of the first kernel finds it for itself; the second is told.
 //
 // Sums are float64: a token is right only if the draw falls on the right side
 // of a running sum, and float32 sums over 2^18 entries would be off by more
@@ -25,11 +25,35 @@ namespace i8h {
 namespace {
 
 constexpr int kDrThreads = 256;
-constexpr int kDrPer = 16;                          // entries a thread takes of a chunk
-constexpr int kDrChunk = kDrThreads * kDrPer;
+constexpr int kDrWaves = kDrThreads / kWave;
 
-__device__ __forceinline__ float prob(const float* p, int64_t i) { return p[i]; }
-__device__ __forceinline__ float prob(const uint16_t* p, int64_t i) { return bf16_to_f32(p[i]); }
+__device__ __forceinline__ float prob(const float* p) { return *p; }
+__device__ __forceinline__ float prob(const uint16_t* p) { return bf16_to_f32(*p); }
+
+// entries v .. v + 3 of a row of V (zero past its end); vec: rows are aligned for one load
+__device__ __forceinline__ void prob4(const float* p, int64_t v, int V, bool vec, float (&o)[4]) {
+  if (vec && v + 4 <= V) {
+    const f32x4 a = *reinterpret_cast<const f32x4*>(p + v);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = a[j];
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = v + j < V ? p[v + j] : 0.0f;
+  }
+}
+__device__ __forceinline__ void prob4(const uint16_t* p, int64_t v, int V, bool vec, float (&o)[4]) {
+  if (vec && v + 4 <= V) {
+    const u32x2 a = *reinterpret_cast<const u32x2*>(p + v);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      o[2 * j] = bf16_lo(a[j]);
+      o[2 * j + 1] = bf16_hi(a[j]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = v + j < V ? bf16_to_f32(p[v + j]) : 0.0f;
+  }
+}
 
 struct DraftArgs {
   const int32_t* drafted;
@@ -37,26 +61,30 @@ struct DraftArgs {
   const float* u;
   const float* u_next;
   int D, V;
+  bool vec;
 };
 
-// the sequence's drafted length and the number of tokens that stay (wave-uniform)
+__device__ __forceinline__ int draft_length(const DraftArgs& a, int b) {
+  return a.draft_len ? min(max(a.draft_len[b], 0), a.D) : a.D;
+}
+
+// the number of tokens that stay (wave-uniform). A position's loads do not wait
+// for the sequence's length, which only ends the count.
 template <typename PT>
-__device__ __forceinline__ int draft_kept(const DraftArgs& a, const PT* p, const PT* q, int b, int& len) {
+__device__ __forceinline__ int draft_kept(const DraftArgs& a, const PT* p, const PT* q, int b, int len) {
   const int lane = threadIdx.x % kWave;
-  len = a.draft_len ? min(max(a.draft_len[b], 0), a.D) : a.D;
-  for (int i0 = 0; i0 < len; i0 += kWave) {
+  for (int i0 = 0; i0 < a.D; i0 += kWave) {
     const int i = i0 + lane;
-    bool stop = false;
-    if (i < len) {
+    bool stop = true;
+    if (i < a.D) {
       const int x = a.drafted[(int64_t)b * a.D + i];
-      stop = true;
       if (x >= 0 && x < a.V) {
-        const double pv = prob(p, ((int64_t)b * (a.D + 1) + i) * a.V + x);
-        const double qv = q ? (double)prob(q, ((int64_t)b * a.D + i) * a.V + x) : 1.0;
+        const double pv = prob(p + ((int64_t)b * (a.D + 1) + i) * a.V + x);
+        const double qv = q ? (double)prob(q + ((int64_t)b * a.D + i) * a.V + x) : 1.0;
         stop = !((double)a.u[(int64_t)b * a.D + i] * qv < pv);
       }
     }
-    const uint64_t m = __ballot(stop);
+    const uint64_t m = __ballot(stop || i >= len);
     if (m != 0) return i0 + __ffsll((unsigned long long)m) - 1;
   }
   return len;
@@ -80,37 +108,55 @@ struct DraftRow {
       else skip = a.drafted[(int64_t)b * a.D + n];
     }
   }
-  __device__ __forceinline__ void at(int v, double& rest, double& all) const {
-    const double pv = prob(p, v);
-    all = positive(pv);
-    rest = v == skip ? 0.0 : q ? positive(pv - (double)prob(q, v)) : all;
-  }
 };
 
-__device__ __forceinline__ double shfl_xor_f64(double v, int m) { return __shfl_xor(v, m, kWave); }
+// rest and p's own positive part of entries v0 + 4 i stride .. +3, i < N
+template <int N, typename PT>
+__device__ __forceinline__ void draft_entries(const DraftArgs& a, const DraftRow<PT>& row, int64_t v0, int stride,
+                                              double (&rest)[4 * N], double (&all)[4 * N]) {
+  float pv[N][4], qv[N][4];
+#pragma unroll
+  for (int i = 0; i < N; ++i) prob4(row.p, v0 + (int64_t)4 * i * stride, a.V, a.vec, pv[i]);
+  if (row.q) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) prob4(row.q, v0 + (int64_t)4 * i * stride, a.V, a.vec, qv[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) qv[i][j] = 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const double d = pv[i][j];
+      all[4 * i + j] = positive(d);
+      rest[4 * i + j] = v0 + (int64_t)4 * i * stride + j == row.skip ? 0.0 : positive(d - (double)qv[i][j]);
+    }
+}
 
-template <typename PT>
+// N: groups of four entries a thread takes of a chunk of kDrThreads * 4 N
+template <int N, typename PT>
 __global__ void __launch_bounds__(kDrThreads)
-k_draft_sums(const DraftArgs a, const PT* __restrict__ p, const PT* __restrict__ q, double* __restrict__ sums) {
-  __shared__ double part[2][kDrThreads / kWave];
+k_draft_sums(const DraftArgs a, const PT* __restrict__ p, const PT* __restrict__ q, double* __restrict__ sums,
+             int32_t* __restrict__ kept) {
+  __shared__ double part[2][kDrWaves];
   const int b = blockIdx.y, c = blockIdx.x;
-  int len;
+  const int len = draft_length(a, b);
   const int n = draft_kept(a, p, q, b, len);
   const DraftRow<PT> row(a, p, q, b, n, len);
+  double r[4 * N], w[4 * N];
+  draft_entries<N>(a, row, (int64_t)c * (kDrThreads * 4 * N) + 4 * threadIdx.x, kDrThreads, r, w);
   double rest = 0.0, all = 0.0;
 #pragma unroll
-  for (int i = 0; i < kDrPer; ++i) {
-    const int64_t v = (int64_t)c * kDrChunk + i * kDrThreads + threadIdx.x;
-    if (v < a.V) {
-      double r, w;
-      row.at((int)v, r, w);
-      rest += r;
-      all += w;
-    }
+  for (int i = 0; i < 4 * N; ++i) {
+    rest += r[i];
+    all += w[i];
   }
   for (int m = 32; m >= 1; m >>= 1) {
-    rest += shfl_xor_f64(rest, m);
-    all += shfl_xor_f64(all, m);
+    rest += __shfl_xor(rest, m, kWave);
+    all += __shfl_xor(all, m, kWave);
   }
   if (threadIdx.x % kWave == 0) {
     part[0][threadIdx.x / kWave] = rest;
@@ -121,6 +167,7 @@ k_draft_sums(const DraftArgs a, const PT* __restrict__ p, const PT* __restrict__
     double* o = sums + 2 * ((int64_t)b * gridDim.x + c);
     o[0] = (part[0][0] + part[0][1]) + (part[0][2] + part[0][3]);
     o[1] = (part[1][0] + part[1][1]) + (part[1][2] + part[1][3]);
+    if (c == 0) kept[b] = n;
   }
 }
 
@@ -137,7 +184,7 @@ __device__ __forceinline__ double block_scan(double v, double* wave_sum, double&
   __syncthreads();
   double base = 0.0;
   total = 0.0;
-  for (int w = 0; w < kDrThreads / kWave; ++w) {
+  for (int w = 0; w < kDrWaves; ++w) {
     if (w < wave) base += wave_sum[w];
     total += wave_sum[w];
   }
@@ -146,103 +193,101 @@ __device__ __forceinline__ double block_scan(double v, double* wave_sum, double&
   return base + ex;
 }
 
-template <typename PT>
+template <int N, typename PT>
 __global__ void __launch_bounds__(kDrThreads)
 k_draft_pick(const DraftArgs a, const PT* __restrict__ p, const PT* __restrict__ q, const double* __restrict__ sums,
-             int nchunks, int32_t* __restrict__ tokens, int32_t* __restrict__ accepted) {
-  __shared__ double wave_sum[kDrThreads / kWave];
+             int nchunks, const int32_t* __restrict__ kept, int32_t* __restrict__ tokens,
+             int32_t* __restrict__ accepted) {
+  constexpr int kPer = 4 * N;
+  __shared__ double wave_sum[kDrWaves];
   __shared__ double s_base;
   __shared__ int s_first, s_last;
   const int b = blockIdx.x, tid = threadIdx.x;
-  int len;
-  const int n = draft_kept(a, p, q, b, len);
-  const DraftRow<PT> row(a, p, q, b, n, len);
   const double* sb = sums + 2 * (int64_t)b * nchunks;
-
-  // the sums' total, and whether anything is left of rest
-  double rest = 0.0, all = 0.0;
-  for (int c = tid; c < nchunks; c += kDrThreads) {
-    rest += sb[2 * c];
-    all += sb[2 * c + 1];
-  }
-  double rt, at;
-  block_scan(rest, wave_sum, rt);
-  block_scan(all, wave_sum, at);
-  const int kind = rt > 0.0 ? 0 : 1;
-  const double total = kind == 0 ? rt : at;
-  const double target = (double)a.u_next[b] * total;
+  const int n = kept[b], len = draft_length(a, b);
+  const DraftRow<PT> row(a, p, q, b, n, len);
+  const double un = a.u_next[b];
 
   // the first chunk whose running sum passes the target (the last one that
-  // holds anything, if rounding leaves none), and the sum before it
+  // holds anything, if rounding leaves none), and the sum before it. Nearly
+  // always the row's chunks fit one tile of 256.
+  double total, chunk_sum = tid < nchunks ? sb[2 * tid] : 0.0, ex = block_scan(chunk_sum, wave_sum, total);
+  int kind = 0;
+  if (nchunks > kDrThreads) {
+    double more = 0.0, rest;
+    for (int c = kDrThreads + tid; c < nchunks; c += kDrThreads) more += sb[2 * c];
+    block_scan(more, wave_sum, rest);
+    total += rest;
+  }
+  if (!(total > 0.0)) {   // nothing is left of rest: p itself
+    kind = 1;
+    double all = 0.0;
+    for (int c = tid; c < nchunks; c += kDrThreads) all += sb[2 * c + 1];
+    block_scan(all, wave_sum, total);
+    chunk_sum = tid < nchunks ? sb[2 * tid + 1] : 0.0;
+    double unused;
+    ex = block_scan(chunk_sum, wave_sum, unused);
+  }
+  const double target = un * total;
   if (tid == 0) {
     s_first = nchunks;
     s_last = -1;
   }
+  __syncthreads();
   double before = 0.0;
   int chunk = -1;
   for (int c0 = 0; c0 < nchunks; c0 += kDrThreads) {
     const int c = c0 + tid;
-    const double v = c < nchunks ? sb[2 * c + kind] : 0.0;
-    double tile;
-    const double ex = before + block_scan(v, wave_sum, tile);
-    if (c < nchunks && ex + v > target) atomicMin(&s_first, c);
-    if (v > 0.0) atomicMax(&s_last, c);
+    if (c0 > 0) {
+      double tile;
+      chunk_sum = c < nchunks ? sb[2 * c + kind] : 0.0;
+      ex = before + block_scan(chunk_sum, wave_sum, tile);
+    }
+    if (c < nchunks && ex + chunk_sum > target) atomicMin(&s_first, c);
+    if (chunk_sum > 0.0) atomicMax(&s_last, c);
+    if (tid == kDrThreads - 1) s_base = ex + chunk_sum;   // the running sum behind this tile
     __syncthreads();
-    const int hit = s_first < nchunks ? s_first : c0 + kDrThreads >= nchunks ? s_last : -1;
-    // the sum before the chosen chunk, if it is in this tile of chunks
-    if (c < nchunks && c == hit) s_base = ex;
+    before = s_base;
+    const int first = s_first;
     __syncthreads();
-    if (s_first < nchunks) {
-      chunk = s_first;
+    if (first < nchunks) {
+      if (c == first) s_base = ex;
+      chunk = first;
       break;
     }
-    before += tile;
   }
-  int next = a.V - 1;
-  if (chunk < 0) {
-    // no running sum passes (the target rounds up to the total): the last entry
-    // that holds anything; with an empty row the last of all
-    chunk = s_last;
-    if (chunk >= 0) {
-      __syncthreads();
-      if (tid == 0) s_base = __builtin_inf();
-    }
-  }
+  // no running sum passes (the target rounds up to the total): the last entry
+  // that holds anything; with an empty row the last of all
+  const bool last_one = chunk < 0;
+  if (last_one) chunk = s_last;
   __syncthreads();
+  int next = a.V - 1;
   if (chunk >= 0) {
-    const double base = s_base;
-    double v[kDrPer], sum = 0.0;
+    double rest[kPer], all[kPer], sum = 0.0;
+    const int64_t v0 = (int64_t)chunk * (kDrThreads * kPer) + tid * kPer;
+    draft_entries<N>(a, row, v0, 1, rest, all);
+    double run = s_base;
     int last = -1;
-    const int64_t v0 = (int64_t)chunk * kDrChunk + tid * kDrPer;
 #pragma unroll
-    for (int i = 0; i < kDrPer; ++i) {
-      v[i] = 0.0;
-      if (v0 + i < a.V) {
-        double r, w;
-        row.at((int)(v0 + i), r, w);
-        v[i] = kind == 0 ? r : w;
-        if (v[i] > 0.0) last = (int)(v0 + i);
-      }
-      sum += v[i];
+    for (int i = 0; i < kPer; ++i) {
+      if (kind == 1) rest[i] = all[i];
+      if (rest[i] > 0.0) last = (int)(v0 + i);
+      sum += rest[i];
     }
     double unused;
-    double run = block_scan(sum, wave_sum, unused);
+    run += block_scan(sum, wave_sum, unused);
     if (tid == 0) {
       s_first = a.V;
       s_last = -1;
     }
     __syncthreads();
-    // base is infinite where the last entry is wanted: then nothing counts as passed
-    if (base < __builtin_inf()) {
-      run += base;
-      int first = a.V;
+    int first = a.V;
 #pragma unroll
-      for (int i = 0; i < kDrPer; ++i) {
-        run += v[i];
-        if (first == a.V && v[i] > 0.0 && run > target) first = (int)(v0 + i);
-      }
-      if (first < a.V) atomicMin(&s_first, first);
+    for (int i = 0; i < kPer; ++i) {
+      run += rest[i];
+      if (first == a.V && rest[i] > 0.0 && run > target && !last_one) first = (int)(v0 + i);
     }
+    if (first < a.V) atomicMin(&s_first, first);
     if (last >= 0) atomicMax(&s_last, last);
     __syncthreads();
     next = s_first < a.V ? s_first : s_last >= 0 ? s_last : a.V - 1;
@@ -252,29 +297,52 @@ k_draft_pick(const DraftArgs a, const PT* __restrict__ p, const PT* __restrict__
   if (tid == 0) accepted[b] = n;
 }
 
+// Groups of four entries a thread takes: chunks of 1024 entries while they do
+// not make more workgroups than run at once (8 a CU; one sequence of 2^18
+// entries then fills the chip), of 4096 beyond, where each workgroup's search
+// for its row would cost more than the parallelism gives.
+int draft_groups(int B, int V) { return (int64_t)B * ((V + 1023) / 1024) <= 2048 ? 1 : 4; }
+
 template <typename PT>
-hipError_t draft(const DraftArgs& a, const void* pv, const void* qv, int B, double* sums, int32_t* tokens,
+hipError_t draft(const DraftArgs& a, const void* pv, const void* qv, int B, void* ws, int32_t* tokens,
                  int32_t* accepted, hipStream_t st) {
   const PT* p = static_cast<const PT*>(pv);
   const PT* q = a.D > 0 ? static_cast<const PT*>(qv) : nullptr;
-  const int nchunks = draft_chunks(a.V);
-  k_draft_sums<PT><<<dim3(nchunks, B), kDrThreads, 0, st>>>(a, p, q, sums);
+  const int nchunks = draft_chunks(B, a.V);
+  double* sums = static_cast<double*>(ws);
+  int32_t* kept = reinterpret_cast<int32_t*>(sums + (int64_t)2 * B * nchunks);
+  const dim3 grid(nchunks, B);
+  const bool small = draft_groups(B, a.V) == 1;
+  if (small) k_draft_sums<1, PT><<<grid, kDrThreads, 0, st>>>(a, p, q, sums, kept);
+  else k_draft_sums<4, PT><<<grid, kDrThreads, 0, st>>>(a, p, q, sums, kept);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  k_draft_pick<PT><<<B, kDrThreads, 0, st>>>(a, p, q, sums, nchunks, tokens, accepted);
+  if (small) k_draft_pick<1, PT><<<B, kDrThreads, 0, st>>>(a, p, q, sums, nchunks, kept, tokens, accepted);
+  else k_draft_pick<4, PT><<<B, kDrThreads, 0, st>>>(a, p, q, sums, nchunks, kept, tokens, accepted);
   return hipGetLastError();
 }
 
 }  // namespace
 
-int draft_chunks(int V) { return (int)(((int64_t)V + kDrChunk - 1) / kDrChunk); }
+int draft_chunks(int B, int V) {
+  const int64_t chunk = (int64_t)kDrThreads * 4 * draft_groups(B, V);
+  return (int)((V + chunk - 1) / chunk);
+}
+
+// the chunks' sums, two doubles each, then the sequences' counts
+size_t draft_workspace_bytes(int B, int V) {
+  return (size_t)B * draft_chunks(B, V) * 2 * sizeof(double) + (size_t)B * sizeof(int32_t);
+}
 
 hipError_t launch_draft_verify(const void* p, const void* q, bool bf16, const int32_t* drafted,
                                const int32_t* draft_len, const float* u, const float* u_next, int B, int D, int V,
-                               double* sums, int32_t* tokens, int32_t* accepted, hipStream_t st) {
-  const DraftArgs a = {drafted, draft_len, u, u_next, D, V};
-  return bf16 ? draft<uint16_t>(a, p, q, B, sums, tokens, accepted, st)
-              : draft<float>(a, p, q, B, sums, tokens, accepted, st);
+                               void* ws, int32_t* tokens, int32_t* accepted, hipStream_t st) {
+  // one load of four entries where every row starts at its alignment
+  const uintptr_t align = bf16 ? 8 : 16;
+  const bool vec = V % 4 == 0 && (reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(q)) % align == 0;
+  const DraftArgs a = {drafted, draft_len, u, u_next, D, V, vec};
+  return bf16 ? draft<uint16_t>(a, p, q, B, ws, tokens, accepted, st)
+              : draft<float>(a, p, q, B, ws, tokens, accepted, st);
 }
 
 }  // namespace i8h

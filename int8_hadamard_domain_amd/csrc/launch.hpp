@@ -108,10 +108,11 @@ hipError_t launch_down_mxfp4(const void* act, bool act_bf16, int T, int I, const
                              const uint8_t* scales, int E, int H, int k, const float* tw, const int32_t* expert_off,
                              const int32_t* pos, uint8_t* ws, float* y, float* out, hipStream_t st);
 
-// verification of drafted tokens (draft.hip): sums holds 2 doubles per chunk of each sequence's row
-int draft_chunks(int V);
+// verification of drafted tokens (draft.hip)
+int draft_chunks(int B, int V);
+size_t draft_workspace_bytes(int B, int V);
 hipError_t launch_draft_verify(const void* p, const void* q, bool bf16, const int32_t* drafted,
                                const int32_t* draft_len, const float* u, const float* u_next, int B, int D, int V,
-                               double* sums, int32_t* tokens, int32_t* accepted, hipStream_t st);
+                               void* ws, int32_t* tokens, int32_t* accepted, hipStream_t st);
 
 }  // namespace i8h
