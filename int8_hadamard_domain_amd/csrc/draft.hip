@@ -33,7 +33,7 @@ __device__ __forceinline__ float prob(const uint16_t* p) { return bf16_to_f32(*p
 // entries v .. v + 3 of a row of V (zero past its end); vec: rows are aligned for one load
 __device__ __forceinline__ void prob4(const float* p, int64_t v, int V, bool vec, float (&o)[4]) {
   if (vec && v + 4 <= V) {
-    const f32x4 a = *reinterpret_cast<const f32x4*>(p + v);
+    const f32x4 a = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p + v));
 #pragma unroll
     for (int j = 0; j < 4; ++j) o[j] = a[j];
   } else {
@@ -43,7 +43,7 @@ __device__ __forceinline__ void prob4(const float* p, int64_t v, int V, bool vec
 }
 __device__ __forceinline__ void prob4(const uint16_t* p, int64_t v, int V, bool vec, float (&o)[4]) {
   if (vec && v + 4 <= V) {
-    const u32x2 a = *reinterpret_cast<const u32x2*>(p + v);
+    const u32x2 a = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p + v));
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       o[2 * j] = bf16_lo(a[j]);
@@ -110,11 +110,10 @@ struct DraftRow {
   }
 };
 
-// rest and p's own positive part of entries v0 + 4 i stride .. +3, i < N
+// entries v0 + 4 i stride .. +3 of the row's p and q, i < N
 template <int N, typename PT>
-__device__ __forceinline__ void draft_entries(const DraftArgs& a, const DraftRow<PT>& row, int64_t v0, int stride,
-                                              double (&rest)[4 * N], double (&all)[4 * N]) {
-  float pv[N][4], qv[N][4];
+__device__ __forceinline__ void draft_load(const DraftArgs& a, const DraftRow<PT>& row, int64_t v0, int stride,
+                                           float (&pv)[N][4], float (&qv)[N][4]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) prob4(row.p, v0 + (int64_t)4 * i * stride, a.V, a.vec, pv[i]);
   if (row.q) {
@@ -126,14 +125,31 @@ __device__ __forceinline__ void draft_entries(const DraftArgs& a, const DraftRow
 #pragma unroll
       for (int j = 0; j < 4; ++j) qv[i][j] = 0.0f;
   }
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const double d = pv[i][j];
-      all[4 * i + j] = positive(d);
-      rest[4 * i + j] = v0 + (int64_t)4 * i * stride + j == row.skip ? 0.0 : positive(d - (double)qv[i][j]);
-    }
+}
+template <typename PT>
+__device__ __forceinline__ double draft_rest(const DraftRow<PT>& row, int64_t v, float p, float q) {
+  return v == row.skip ? 0.0 : positive((double)p - (double)q);
+}
+
+// Sum over the lanes up to this one, in lane order within rows of 16 and then
+// over rows: data-parallel-primitive moves on the vector ALU (a scan through LDS
+// shuffles costs their latency twelve times).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_f64(double v) {
+  const u32x2 w = __builtin_bit_cast(u32x2, v);
+  u32x2 o;
+  o[0] = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)w[0], CTRL, ROWS, 0xF, true);
+  o[1] = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)w[1], CTRL, ROWS, 0xF, true);
+  return __builtin_bit_cast(double, o);   // 0.0 where no lane gives one
+}
+__device__ __forceinline__ double wave_scan(double v) {
+  v += dpp_f64<0x111, 0xF>(v);   // row_shr 1, 2, 4, 8
+  v += dpp_f64<0x112, 0xF>(v);
+  v += dpp_f64<0x114, 0xF>(v);
+  v += dpp_f64<0x118, 0xF>(v);
+  v += dpp_f64<0x142, 0xA>(v);   // row_bcast 15: lane 15 of rows 0, 2 to rows 1, 3
+  v += dpp_f64<0x143, 0xC>(v);   // row_bcast 31: lane 31 to rows 2, 3
+  return v;
 }
 
 // N: groups of four entries a thread takes of a chunk of kDrThreads * 4 N
@@ -146,19 +162,20 @@ k_draft_sums(const DraftArgs a, const PT* __restrict__ p, const PT* __restrict__
   const int len = draft_length(a, b);
   const int n = draft_kept(a, p, q, b, len);
   const DraftRow<PT> row(a, p, q, b, n, len);
-  double r[4 * N], w[4 * N];
-  draft_entries<N>(a, row, (int64_t)c * (kDrThreads * 4 * N) + 4 * threadIdx.x, kDrThreads, r, w);
+  const int64_t v0 = (int64_t)c * (kDrThreads * 4 * N) + 4 * threadIdx.x;
+  float pv[N][4], qv[N][4];
+  draft_load<N>(a, row, v0, kDrThreads, pv, qv);
   double rest = 0.0, all = 0.0;
 #pragma unroll
-  for (int i = 0; i < 4 * N; ++i) {
-    rest += r[i];
-    all += w[i];
-  }
-  for (int m = 32; m >= 1; m >>= 1) {
-    rest += __shfl_xor(rest, m, kWave);
-    all += __shfl_xor(all, m, kWave);
-  }
-  if (threadIdx.x % kWave == 0) {
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      all += positive(pv[i][j]);
+      rest += draft_rest(row, v0 + (int64_t)4 * i * kDrThreads + j, pv[i][j], qv[i][j]);
+    }
+  rest = wave_scan(rest);
+  all = wave_scan(all);
+  if (threadIdx.x % kWave == kWave - 1) {
     part[0][threadIdx.x / kWave] = rest;
     part[1][threadIdx.x / kWave] = all;
   }
@@ -174,23 +191,38 @@ k_draft_sums(const DraftArgs a, const PT* __restrict__ p, const PT* __restrict__
 // sum of v over the threads below this one; total over the workgroup
 __device__ __forceinline__ double block_scan(double v, double* wave_sum, double& total) {
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-  double inc = v;
-  for (int d = 1; d < kWave; d <<= 1) {
-    const double o = __shfl_up(inc, d, kWave);
-    if (lane >= d) inc += o;
-  }
+  const double inc = wave_scan(v);
   __syncthreads();
   if (lane == kWave - 1) wave_sum[wave] = inc;
   __syncthreads();
   double base = 0.0;
   total = 0.0;
+#pragma unroll
   for (int w = 0; w < kDrWaves; ++w) {
-    if (w < wave) base += wave_sum[w];
-    total += wave_sum[w];
+    const double s = wave_sum[w];
+    if (w < wave) base += s;
+    total += s;
   }
-  double ex = __shfl_up(inc, 1, kWave);
-  if (lane == 0) ex = 0.0;
-  return base + ex;
+  return base + dpp_f64<0x138, 0xF>(inc);   // wave_shr 1
+}
+
+// the lowest thread index at which `hit` holds, and the highest at which `any`
+// does (-1: none), over the workgroup
+__device__ __forceinline__ void block_find(bool hit, bool any, int (*found)[2], int& first, int& last) {
+  const int wave = threadIdx.x / kWave;
+  const uint64_t h = __ballot(hit), a = __ballot(any);
+  __syncthreads();
+  if (threadIdx.x % kWave == 0) {
+    found[wave][0] = h ? wave * kWave + __ffsll((unsigned long long)h) - 1 : -1;
+    found[wave][1] = a ? wave * kWave + 63 - __clzll((long long)a) : -1;
+  }
+  __syncthreads();
+  first = last = -1;
+#pragma unroll
+  for (int w = 0; w < kDrWaves; ++w) {
+    if (first < 0) first = found[w][0];
+    if (found[w][1] >= 0) last = found[w][1];
+  }
 }
 
 template <int N, typename PT>
@@ -201,7 +233,8 @@ k_draft_pick(const DraftArgs a, const PT* __restrict__ p, const PT* __restrict__
   constexpr int kPer = 4 * N;
   __shared__ double wave_sum[kDrWaves];
   __shared__ double s_base;
-  __shared__ int s_first, s_last;
+  __shared__ int s_next;
+  __shared__ int found[kDrWaves][2];
   const int b = blockIdx.x, tid = threadIdx.x;
   const double* sb = sums + 2 * (int64_t)b * nchunks;
   const int n = kept[b], len = draft_length(a, b);
@@ -229,69 +262,59 @@ k_draft_pick(const DraftArgs a, const PT* __restrict__ p, const PT* __restrict__
     ex = block_scan(chunk_sum, wave_sum, unused);
   }
   const double target = un * total;
-  if (tid == 0) {
-    s_first = nchunks;
-    s_last = -1;
-  }
-  __syncthreads();
-  double before = 0.0;
-  int chunk = -1;
-  for (int c0 = 0; c0 < nchunks; c0 += kDrThreads) {
-    const int c = c0 + tid;
-    if (c0 > 0) {
-      double tile;
-      chunk_sum = c < nchunks ? sb[2 * c + kind] : 0.0;
-      ex = before + block_scan(chunk_sum, wave_sum, tile);
-    }
-    if (c < nchunks && ex + chunk_sum > target) atomicMin(&s_first, c);
-    if (chunk_sum > 0.0) atomicMax(&s_last, c);
-    if (tid == kDrThreads - 1) s_base = ex + chunk_sum;   // the running sum behind this tile
-    __syncthreads();
-    before = s_base;
-    const int first = s_first;
-    __syncthreads();
-    if (first < nchunks) {
-      if (c == first) s_base = ex;
-      chunk = first;
+  int chunk = -1, last_chunk = -1;
+  for (int c0 = 0;;) {
+    int first, last;
+    block_find(ex + chunk_sum > target, chunk_sum > 0.0, found, first, last);
+    if (last >= 0) last_chunk = c0 + last;
+    if (first >= 0) {
+      chunk = c0 + first;
+      if (tid == first) s_base = ex;
       break;
     }
+    c0 += kDrThreads;
+    if (c0 >= nchunks) break;
+    if (tid == kDrThreads - 1) s_base = ex + chunk_sum;   // the running sum so far
+    __syncthreads();
+    const double before = s_base;
+    const int c = c0 + tid;
+    double tile;
+    chunk_sum = c < nchunks ? sb[2 * c + kind] : 0.0;
+    ex = before + block_scan(chunk_sum, wave_sum, tile);
   }
   // no running sum passes (the target rounds up to the total): the last entry
   // that holds anything; with an empty row the last of all
   const bool last_one = chunk < 0;
-  if (last_one) chunk = s_last;
+  if (last_one) chunk = last_chunk;
+  if (tid == 0) s_next = a.V - 1;
   __syncthreads();
-  int next = a.V - 1;
   if (chunk >= 0) {
-    double rest[kPer], all[kPer], sum = 0.0;
+    float pv[N][4], qv[N][4];
     const int64_t v0 = (int64_t)chunk * (kDrThreads * kPer) + tid * kPer;
-    draft_entries<N>(a, row, v0, 1, rest, all);
-    double run = s_base;
-    int last = -1;
+    draft_load<N>(a, row, v0, 1, pv, qv);
+    double rest[kPer], sum = 0.0;
+    int mine = -1;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      if (kind == 1) rest[i] = all[i];
-      if (rest[i] > 0.0) last = (int)(v0 + i);
+      const float pi = pv[i / 4][i % 4], qi = qv[i / 4][i % 4];
+      rest[i] = kind == 1 ? positive(pi) : draft_rest(row, v0 + i, pi, qi);
+      if (rest[i] > 0.0) mine = i;
       sum += rest[i];
     }
-    double unused;
-    run += block_scan(sum, wave_sum, unused);
-    if (tid == 0) {
-      s_first = a.V;
-      s_last = -1;
-    }
-    __syncthreads();
-    int first = a.V;
+    double unused, run = s_base + block_scan(sum, wave_sum, unused);
+    const bool any = mine >= 0;
+    int hit = -1;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       run += rest[i];
-      if (first == a.V && rest[i] > 0.0 && run > target && !last_one) first = (int)(v0 + i);
+      if (hit < 0 && rest[i] > 0.0 && run > target && !last_one) hit = i;
     }
-    if (first < a.V) atomicMin(&s_first, first);
-    if (last >= 0) atomicMax(&s_last, last);
+    int first, last;
+    block_find(hit >= 0, any, found, first, last);
+    if (first >= 0 ? tid == first : tid == last) s_next = (int)(v0 + (first >= 0 ? hit : mine));
     __syncthreads();
-    next = s_first < a.V ? s_first : s_last >= 0 ? s_last : a.V - 1;
   }
+  const int next = s_next;
   for (int i = tid; i <= a.D; i += kDrThreads)
     tokens[(int64_t)b * (a.D + 1) + i] = i < n ? a.drafted[(int64_t)b * a.D + i] : i == n ? next : -1;
   if (tid == 0) accepted[b] = n;

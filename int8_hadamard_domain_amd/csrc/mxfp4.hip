@@ -14,19 +14,29 @@ namespace i8h {
 namespace {
 
 constexpr int kMxThreads = 256;
+constexpr int kMxGroups = 2;   // groups of eight values a thread takes
 
 template <typename XT>
 __global__ void __launch_bounds__(kMxThreads)
 k_mxfp4_quantize(const XT* __restrict__ x, int64_t n8, uint32_t* __restrict__ codes, uint8_t* __restrict__ scales) {
   // rows are whole blocks, so the matrix is one run of blocks
-  const int64_t i = (int64_t)blockIdx.x * kMxThreads + threadIdx.x;
-  float v[8] = {};
-  if (i < n8) mx_load8(x + 8 * i, v);   // n8 is a multiple of 4: a block's lanes are all in or all out
-  int s;
-  const uint32_t c = mx_quant8(v, s);
-  if (i >= n8) return;
-  codes[i] = c;
-  if ((threadIdx.x & 3) == 0) scales[i / 4] = (uint8_t)s;
+  const int64_t i0 = (int64_t)blockIdx.x * (kMxGroups * kMxThreads) + threadIdx.x;
+  float v[kMxGroups][8] = {};
+#pragma unroll
+  for (int g = 0; g < kMxGroups; ++g) {
+    const int64_t i = i0 + g * kMxThreads;
+    if (i < n8) mx_load8(x + 8 * i, v[g]);   // n8 is a multiple of 4: a block's lanes are all in or all out
+  }
+#pragma unroll
+  for (int g = 0; g < kMxGroups; ++g) {
+    const int64_t i = i0 + g * kMxThreads;
+    int s;
+    const uint32_t c = mx_quant8(v[g], s);
+    if (i < n8) {
+      codes[i] = c;
+      if ((threadIdx.x & 3) == 0) scales[i / 4] = (uint8_t)s;
+    }
+  }
 }
 
 // E2M1 code -> float: codes 0..7 are 0, 0.5, 1, 1.5, 2, 3, 4, 6
@@ -71,7 +81,7 @@ k_mxfp4_dequantize(const uint32_t* __restrict__ codes, const uint8_t* __restrict
 
 hipError_t launch_mxfp4_quantize(const void* x, bool bf16, int64_t values, uint8_t* codes, uint8_t* scales,
                                  hipStream_t st) {
-  const int64_t n8 = values / 8, grid = (n8 + kMxThreads - 1) / kMxThreads;
+  const int64_t n8 = values / 8, per = kMxGroups * kMxThreads, grid = (n8 + per - 1) / per;
   if (grid >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
   uint32_t* c = reinterpret_cast<uint32_t*>(codes);
   if (bf16)

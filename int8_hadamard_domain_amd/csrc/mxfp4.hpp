@@ -36,7 +36,8 @@ __device__ __forceinline__ uint32_t mx_quant8(const float (&v)[8], int& s) {
 }
 
 __device__ __forceinline__ void mx_load8(const float* p, float (&v)[8]) {
-  const f32x4 a = reinterpret_cast<const f32x4*>(p)[0], b = reinterpret_cast<const f32x4*>(p)[1];
+  const f32x4 a = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p));
+  const f32x4 b = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p) + 1);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     v[i] = a[i];
@@ -44,7 +45,7 @@ __device__ __forceinline__ void mx_load8(const float* p, float (&v)[8]) {
   }
 }
 __device__ __forceinline__ void mx_load8(const uint16_t* p, float (&v)[8]) {
-  const u32x4 a = *reinterpret_cast<const u32x4*>(p);
+  const u32x4 a = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     v[2 * i] = bf16_lo(a[i]);
