@@ -55,8 +55,9 @@ int mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int T, int K, 
  * 2^32 (else I8H_EUNSUPPORTED). gate_up float32 [T*topk, N] or NULL; act [T*topk, N/2]
  * of act_type (bf16: each value rounded to nearest even from the float32
  * one) or NULL; both 16-B aligned. workspace: at least
- * moe_gateup_mxfp4_workspace_size(T, K, E, topk) bytes, 256-B aligned; what it
- * holds after the call is unspecified. */
+ * moe_gateup_mxfp4_workspace_size(T, K, E, topk) bytes, 256-B aligned
+ * (may be NULL when that size is 0: a few tokens take one launch that needs
+ * none); what it holds after the call is unspecified. */
 size_t moe_gateup_mxfp4_workspace_size(int T, int K, int E, int topk);
 int moe_gateup_mxfp4_grouped(const uint16_t* x, int T, int K, const uint8_t* codes, const uint8_t* scales,
                              int E, int N, int topk, const int32_t* expert_off, const int32_t* sorted_pairs,
@@ -73,7 +74,8 @@ int moe_gateup_mxfp4_grouped(const uint16_t* x, int T, int K, const uint8_t* cod
  * T*topk*(I + 256) < 2^32 (else I8H_EUNSUPPORTED). out float32 [T, H],
  * 16-B aligned. topk_ids, topk_w, expert_off, pair_pos: as moe_route_permute
  * writes them. workspace: at least moe_down_mxfp4_workspace_size(T, I, E,
- * H, topk) bytes, 256-B aligned, contents unspecified afterwards. */
+ * H, topk) bytes, 256-B aligned (may be NULL when that size is 0,
+ * as for gate_up), contents unspecified afterwards. */
 size_t moe_down_mxfp4_workspace_size(int T, int I, int E, int H, int topk);
 int moe_down_mxfp4_combine(const void* act, int act_type, int T, int I, const uint8_t* codes,
                            const uint8_t* scales, int E, int H, int topk, const int32_t* topk_ids,

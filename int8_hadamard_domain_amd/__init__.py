@@ -577,13 +577,15 @@ def moe_gateup_mxfp4_grouped(x, codes, scales, topk, expert_off, sorted_pairs,
     E, N = _mx_weights(codes, scales, K, dev)
     _dev(expert_off, "expert_off", torch.int32, shape=(E + 1,), device=dev)
     _dev(sorted_pairs, "sorted_pairs", torch.int32, shape=(T * topk,), device=dev)
-    workspace = _workspace(workspace, "workspace", lib().moe_gateup_mxfp4_workspace_size(T, K, E, topk), dev)
+    need = lib().moe_gateup_mxfp4_workspace_size(T, K, E, topk)
+    if need > 0 or workspace is not None:
+        workspace = _workspace(workspace, "workspace", need, dev)
     gu = _out(gate_up, (T * topk, N), dev)
     adt = _act_dtype(act, act_dtype)
     ac = _out(act, (T * topk, N // 2), dev, adt)
     _check("moe_gateup_mxfp4_grouped", lib().moe_gateup_mxfp4_grouped(
         _ptr(x), T, K, _ptr(codes), _ptr(scales), E, N, topk, _ptr(expert_off), _ptr(sorted_pairs),
-        _ptr(gu), _ptr(ac), TYPES[adt], _ptr(workspace), workspace.numel(), _stream(dev)))
+        _ptr(gu), _ptr(ac), TYPES[adt], _ptr(workspace), need, _stream(dev)))
     return gu, ac
 
 
@@ -604,14 +606,16 @@ def moe_down_mxfp4_combine(act, codes, scales, routing, out=None, workspace=None
     tw = _dev(routing["topk_w"], "topk_w", torch.float32, shape=(T, topk), device=dev)
     off = _dev(routing["expert_off"], "expert_off", torch.int32, shape=(E + 1,), device=dev)
     pos = _dev(routing["pair_pos"], "pair_pos", torch.int32, shape=(P,), device=dev)
-    workspace = _workspace(workspace, "workspace", lib().moe_down_mxfp4_workspace_size(T, I, E, H, topk), dev)
+    need = lib().moe_down_mxfp4_workspace_size(T, I, E, H, topk)
+    if need > 0 or workspace is not None:
+        workspace = _workspace(workspace, "workspace", need, dev)
     if out is None:
         out = torch.empty((T, H), dtype=torch.float32, device=dev)
     else:
         _dev(out, "out", torch.float32, shape=(T, H), device=dev)
     _check("moe_down_mxfp4_combine", lib().moe_down_mxfp4_combine(
         _ptr(act), at, T, I, _ptr(codes), _ptr(scales), E, H, topk, _ptr(ids), _ptr(tw), _ptr(off), _ptr(pos),
-        _ptr(out), _ptr(workspace), workspace.numel(), _stream(dev)))
+        _ptr(out), _ptr(workspace), need, _stream(dev)))
     return out
 
 

@@ -52,7 +52,7 @@ int mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int T, int K, 
 }
 
 size_t moe_gateup_mxfp4_workspace_size(int T, int K, int E, int topk) {
-  if (T <= 0 || K <= 0 || (K % 128) != 0 || E <= 0 || topk <= 0) return 0;
+  if (T <= 0 || K <= 0 || (K % 128) != 0 || E <= 0 || topk <= 0 || i8h::mx_few_gateup(T, K, topk)) return 0;
   return i8h::MxWorkspace(T, K, (int64_t)T * topk, E).total;
 }
 
@@ -72,16 +72,19 @@ int moe_gateup_mxfp4_grouped(const uint16_t* x, int T, int K, const uint8_t* cod
       !aligned(sorted_pairs, 4))
     return I8H_EINVAL;
   if ((gate_up && !aligned(gate_up, 16)) || (act && !aligned(act, 16))) return I8H_EINVAL;
-  if (!workspace || workspace_bytes < moe_gateup_mxfp4_workspace_size(T, K, E, topk) || !aligned(workspace, 256))
-    return I8H_EINVAL;
+  const size_t need = moe_gateup_mxfp4_workspace_size(T, K, E, topk);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return I8H_EINVAL;
   if (!gate_up && !act) return I8H_OK;          // nothing requested
+  if (i8h::mx_few_gateup(T, K, topk))
+    return from_hip(i8h::launch_gateup_mxfp4_few(x, T, K, codes, scales, E, N, topk, expert_off, sorted_pairs, gate_up,
+                                                 act, act_type == I8H_BF16, as_stream(stream)));
   return from_hip(i8h::launch_gateup_mxfp4(x, T, K, codes, scales, E, N, topk, expert_off, sorted_pairs, gate_up, act,
                                            act_type == I8H_BF16, static_cast<uint8_t*>(workspace),
                                            as_stream(stream)));
 }
 
 size_t moe_down_mxfp4_workspace_size(int T, int I, int E, int H, int topk) {
-  if (T <= 0 || I <= 0 || (I % 32) != 0 || E <= 0 || H <= 0 || topk <= 0) return 0;
+  if (T <= 0 || I <= 0 || (I % 32) != 0 || E <= 0 || H <= 0 || topk <= 0 || i8h::mx_few_down(T, I, topk)) return 0;
   const int64_t P = (int64_t)T * topk;
   return i8h::MxWorkspace(P, I, P, E).total + round_up((size_t)P * H * sizeof(float), 256);
 }
@@ -102,8 +105,11 @@ int moe_down_mxfp4_combine(const void* act, int act_type, int T, int I, const ui
   if (!aligned(act, 16) || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(out, 16)) return I8H_EINVAL;
   if (!aligned(topk_ids, 4) || !aligned(topk_w, 4) || !aligned(expert_off, 4) || !aligned(pair_pos, 4))
     return I8H_EINVAL;
-  if (!workspace || workspace_bytes < moe_down_mxfp4_workspace_size(T, I, E, H, topk) || !aligned(workspace, 256))
-    return I8H_EINVAL;
+  const size_t need = moe_down_mxfp4_workspace_size(T, I, E, H, topk);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return I8H_EINVAL;
+  if (i8h::mx_few_down(T, I, topk))
+    return from_hip(i8h::launch_down_mxfp4_few(act, act_type == I8H_BF16, T, I, codes, scales, H, topk, topk_ids,
+                                               topk_w, pair_pos, out, as_stream(stream)));
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   float* y = reinterpret_cast<float*>(ws + i8h::MxWorkspace(P, I, P, E).total);
   return from_hip(i8h::launch_down_mxfp4(act, act_type == I8H_BF16, T, I, codes, scales, E, H, topk, topk_w, expert_off,

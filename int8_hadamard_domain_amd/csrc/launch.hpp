@@ -108,6 +108,16 @@ hipError_t launch_down_mxfp4(const void* act, bool act_bf16, int T, int I, const
                              const uint8_t* scales, int E, int H, int k, const float* tw, const int32_t* expert_off,
                              const int32_t* pos, uint8_t* ws, float* y, float* out, hipStream_t st);
 
+// the same for a few tokens in one launch, no workspace (moe_mx_few.hip)
+bool mx_few_gateup(int T, int K, int topk);
+bool mx_few_down(int T, int I, int topk);
+hipError_t launch_gateup_mxfp4_few(const uint16_t* x, int T, int K, const uint8_t* codes, const uint8_t* scales, int E,
+                                   int N, int k, const int32_t* expert_off, const int32_t* sorted_pairs, float* gu,
+                                   void* act, bool act_bf16, hipStream_t st);
+hipError_t launch_down_mxfp4_few(const void* act, bool act_bf16, int T, int I, const uint8_t* codes,
+                                 const uint8_t* scales, int H, int k, const int32_t* ids, const float* tw,
+                                 const int32_t* pos, float* out, hipStream_t st);
+
 // verification of drafted tokens (draft.hip)
 int draft_chunks(int B, int V);
 size_t draft_workspace_bytes(int B, int V);
