@@ -492,7 +492,7 @@ k_mx_prepare(const XT* __restrict__ x, int64_t n8, int nb, int nbp, int row_byte
   float v[8] = {};
   const int64_t row = (i / 4) / nbp;
   const int b = (int)(i / 4 - row * nbp);
-  if (i < n8 && b < nb) mx_load8(x + (row * nb + b) * kMxBlock + 8 * (i & 3), v);
+  if (i < n8 && b < nb) mx_load8_once(x + (row * nb + b) * kMxBlock + 8 * (i & 3), v);
   int s;
   const uint32_t c = mx_quant8(v, s);   // n8 is a multiple of 4: a block's four lanes are all in or all out
   if (i >= n8) return;

@@ -37,6 +37,7 @@ __device__ __forceinline__ f32x4 mx_mfma16(const u32x4 a, const u32x4 b, f32x4 c
 constexpr int kFgThreads = 256;
 constexpr int kFgWaves = kFgThreads / kWave;
 constexpr int kFgLds = 64 * 1024;    // quantised tokens: rows of codes and scales
+constexpr int kFgAhead = 8;          // groups of eight values a thread loads at once: 8 tokens of K = 2048
 
 // bytes of a token's row in LDS: codes, then scales, padded to an odd number of
 // 16-byte pieces (columns then lie in different banks)
@@ -77,6 +78,7 @@ k_gateup_mx_few(const uint16_t* __restrict__ x, int T, int nb, const uint8_t* __
   const size_t n = (size_t)e * N + ((c & 2) ? I + i0 : i0);
   const uint8_t* wr = wq + n * (16 * nb) + 16 * g;
   const uint8_t* wsr = ws + n * nb;
+  int token = sorted_pairs[r0 + min(c, m - 1)];   // of this lane's column: its pair for now
   const int steps = nb / 4;            // K % 128 == 0
   u32x4 w[kFewSteps];
   uint32_t s[kFewSteps];
@@ -90,33 +92,46 @@ k_gateup_mx_few(const uint16_t* __restrict__ x, int T, int nb, const uint8_t* __
   };
   load(0);
 
-  // every token's row, eight values a thread
-  for (int p0 = 0; p0 < T * (K / 8); p0 += kFgThreads) {
-    const int p = p0 + tid, t = p / (K / 8), k8 = p - t * (K / 8);
-    float v[8] = {};
-    if (t < T) mx_load8(x + (size_t)p * 8, v);   // whole blocks: a block's four lanes are all in or all out
+  // every token's row, eight values a thread and a time, kFgAhead loads at once
+  const int groups = T * (K / 8);
+  auto raw = [&](int p) { return mx_raw8(x + (size_t)min(p, groups - 1) * 8); };
+  u32x4 xv[kFgAhead];
+#pragma unroll
+  for (int i = 0; i < kFgAhead; ++i)
+    if (i * kFgThreads < groups) xv[i] = raw(i * kFgThreads + tid);
+
+  auto quantise = [&](int p, const u32x4 r) {
+    float v[8];
+    mx_floats(r, v);
     int sc;
-    const uint32_t q = mx_quant8(v, sc);
-    if (t < T) {
+    const uint32_t q = mx_quant8(v, sc);   // whole blocks: a block's four lanes are all in or all out
+    if (p < groups) {
+      const int t = p / (K / 8), k8 = p - t * (K / 8);
       *reinterpret_cast<uint32_t*>(&lds[t * row_bytes + 4 * k8]) = q;
       if ((k8 & 3) == 0) lds[t * row_bytes + 16 * nb + k8 / 4] = (uint8_t)sc;
     }
-  }
+  };
+#pragma unroll
+  for (int i = 0; i < kFgAhead; ++i)
+    if (i * kFgThreads < groups) quantise(i * kFgThreads + tid, xv[i]);
+  for (int p0 = kFgAhead * kFgThreads; p0 < groups; p0 += kFgThreads) quantise(p0 + tid, raw(p0 + tid));
+  token /= topk;
   __syncthreads();
   if (!live) return;
 
   for (int c0 = 0; c0 < m; c0 += 16) {
     const int r = r0 + min(c0 + c, m - 1);
-    const uint8_t* xr = lds + (sorted_pairs[r] / topk) * row_bytes;
+    if (c0 > 0) token = sorted_pairs[r] / topk;
+    const uint8_t* xr = lds + token * row_bytes;
     f32x4 acc = {};
     for (int j0 = 0; j0 < steps; j0 += kFewSteps) {
       if (j0 > 0 || (c0 > 0 && steps > kFewSteps)) load(j0);
 #pragma unroll
       for (int j = 0; j < kFewSteps; ++j)
         if (j0 + j < steps) {
-          const u32x4 xv = *reinterpret_cast<const u32x4*>(xr + 64 * (j0 + j) + 16 * g);
+          const u32x4 b = *reinterpret_cast<const u32x4*>(xr + 64 * (j0 + j) + 16 * g);
           const uint32_t xs = *reinterpret_cast<const uint32_t*>(xr + 16 * nb + 4 * (j0 + j));
-          acc = mx_mfma16(w[j], xv, acc, s[j] >> (8 * g), xs >> (8 * g));
+          acc = mx_mfma16(w[j], b, acc, s[j] >> (8 * g), xs >> (8 * g));
         }
     }
     if (c0 + c < m) {
@@ -172,17 +187,25 @@ k_down_mx_few(const XT* __restrict__ act, int nb, const uint8_t* __restrict__ wq
         s[i] = b < nb ? wsr[b] : 127u;
       }
     // the slot's act row, eight values a lane at a time
-    for (int p0 = 0; p0 < 16 * steps; p0 += kWave) {
-      const int p = p0 + lane;
-      float v[8] = {};
-      if (p < 4 * nb) mx_load8(act + r * (nb * kMxBlock) + 8 * p, v);
-      int sc;
-      const uint32_t q = mx_quant8(v, sc);
-      if (p < 16 * steps) {
-        *reinterpret_cast<uint32_t*>(&row[4 * p]) = q;
-        if ((p & 3) == 0) row[kFdMaxI / 2 + p / 4] = (uint8_t)(p < 4 * nb ? sc : 127);
+    constexpr int kPer = kFewSteps * 16 / kWave;
+    decltype(mx_raw8(act)) xv[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (4 * i < steps) xv[i] = mx_raw8(act + r * (nb * kMxBlock) + 8 * min(i * kWave + lane, 4 * nb - 1));
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (4 * i < steps) {
+        const int p = i * kWave + lane;
+        const bool in = p < 4 * nb;
+        float v[8];
+        mx_floats(xv[i], v);
+        int sc;
+        const uint32_t q = mx_quant8(v, sc);   // whole blocks: a block's four lanes are all in or all out
+        if (p < 16 * steps) {
+          *reinterpret_cast<uint32_t*>(&row[4 * p]) = in ? q : 0u;
+          if ((p & 3) == 0) row[kFdMaxI / 2 + p / 4] = (uint8_t)(in ? sc : 127);
+        }
       }
-    }
     f32x4 acc = {};
 #pragma unroll
     for (int i = 0; i < kFewSteps; ++i)

@@ -25,7 +25,7 @@ k_mxfp4_quantize(const XT* __restrict__ x, int64_t n8, uint32_t* __restrict__ co
 #pragma unroll
   for (int g = 0; g < kMxGroups; ++g) {
     const int64_t i = i0 + g * kMxThreads;
-    if (i < n8) mx_load8(x + 8 * i, v[g]);   // n8 is a multiple of 4: a block's lanes are all in or all out
+    if (i < n8) mx_load8_once(x + 8 * i, v[g]);   // n8 is a multiple of 4: a block's lanes are all in or all out
   }
 #pragma unroll
   for (int g = 0; g < kMxGroups; ++g) {

@@ -35,22 +35,40 @@ __device__ __forceinline__ uint32_t mx_quant8(const float (&v)[8], int& s) {
   return e == 255 ? 0u : c;
 }
 
-__device__ __forceinline__ void mx_load8(const float* p, float (&v)[8]) {
-  const f32x4 a = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p));
-  const f32x4 b = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p) + 1);
+// eight values as they lie in memory, and as floats
+struct MxRaw32 {
+  f32x4 a, b;
+};
+__device__ __forceinline__ MxRaw32 mx_raw8(const float* p) {
+  return {reinterpret_cast<const f32x4*>(p)[0], reinterpret_cast<const f32x4*>(p)[1]};
+}
+__device__ __forceinline__ u32x4 mx_raw8(const uint16_t* p) { return *reinterpret_cast<const u32x4*>(p); }
+// the same for data that is read once
+__device__ __forceinline__ MxRaw32 mx_raw8_once(const float* p) {
+  return {__builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p)),
+          __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p) + 1)};
+}
+__device__ __forceinline__ u32x4 mx_raw8_once(const uint16_t* p) {
+  return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+}
+__device__ __forceinline__ void mx_floats(const MxRaw32& r, float (&v)[8]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    v[i] = a[i];
-    v[4 + i] = b[i];
+    v[i] = r.a[i];
+    v[4 + i] = r.b[i];
   }
 }
-__device__ __forceinline__ void mx_load8(const uint16_t* p, float (&v)[8]) {
-  const u32x4 a = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+__device__ __forceinline__ void mx_floats(const u32x4 r, float (&v)[8]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    v[2 * i] = bf16_lo(a[i]);
-    v[2 * i + 1] = bf16_hi(a[i]);
+    v[2 * i] = bf16_lo(r[i]);
+    v[2 * i + 1] = bf16_hi(r[i]);
   }
+}
+
+template <typename T>
+__device__ __forceinline__ void mx_load8_once(const T* p, float (&v)[8]) {
+  mx_floats(mx_raw8_once(p), v);
 }
 
 // 32 x 32 x 64 with both operands E2M1: lane l holds the 32 codes of row (A) or
