@@ -19,12 +19,13 @@
 //
 // k_mx_prepare quantises the activation rows and lists the passes: up to 32 MT
 // sorted rows of one expert each. Then
-//   k_mx_stream  the passes' weight tiles, one after another, are dealt in equal
-//                runs to one workgroup of 8 waves per CU. A workgroup keeps the
-//                pass's activation rows in LDS, whole K, and its waves stream
-//                tiles past them from memory straight into operand registers,
-//                PD stages ahead and on into the next tile: no barrier, no wait
-//                but for the weights themselves.
+//   k_mx_stream  the passes' weight tiles are dealt evenly to one workgroup of 8
+//                waves per CU. A workgroup keeps a pass's activation rows in LDS,
+//                whole K, and its waves stream tiles past them from memory
+//                straight into operand registers, PD stages ahead and on into the
+//                next tile: no barrier, no wait but for the weights themselves.
+//                Passes of one expert start together on neighbouring CUs of an
+//                XCD, so most weights leave memory once.
 //   k_mx_ring    for K too long for that: activation rows in stages through LDS
 
 #include <type_traits>
@@ -163,16 +164,38 @@ k_mx_stream(const MxArgs a, float* __restrict__ out0, AT* __restrict__ out1) {
   const int row_bytes = a.row_bytes, pieces = row_bytes / 16, xsc = S * 128;   // xsc: a row's scales
   const uint32_t wq_n = (uint32_t)R * (16 * nb), ws_n = (uint32_t)R * nb;
 
-  // this workgroup's run of (pass, tile) pairs; neighbouring runs on one XCD
-  const int64_t total = (int64_t)a.items[0].e * a.ntiles;
-  const int rank = blockIdx.x % kXcds * (kSmBlocks / kXcds) + blockIdx.x / kXcds;
-  int64_t u = total * rank / kSmBlocks;
-  const int64_t end = total * (rank + 1) / kSmBlocks;
+  // The deal, lane = workgroup, neighbouring lanes on one XCD: whole passes while
+  // there are as many as lanes; then of each pass left (fewer than lanes) the
+  // first `cut` tiles to a lane of its own, and the tiles behind them in even
+  // runs to the other lanes. A run begins with its pass's activation rows, which
+  // take about the time of four tiles: the cut makes up for a run being several.
+  const int lane_id = blockIdx.x % kXcds * (kSmBlocks / kXcds) + blockIdx.x / kXcds, nt = a.ntiles;
+  const int full = a.items[0].e / kSmBlocks, rest = a.items[0].e % kSmBlocks, others = kSmBlocks - rest;
+  const int64_t even = ((int64_t)rest * nt + kSmBlocks - 1) / kSmBlocks;
+  const int cut = (int)min((int64_t)nt, max(even, ((int64_t)rest * (nt + 4) - 4 * others) / kSmBlocks));
+  int64_t u = 0, end = 0;
+  if (lane_id >= rest) {
+    const int64_t tiles = (int64_t)rest * (nt - cut);
+    u = tiles * (lane_id - rest) / others;
+    end = tiles * (lane_id - rest + 1) / others;
+  }
 
-  while (u < end) {
-    const int64_t idx = u / a.ntiles;
-    const int t0 = (int)(u - idx * a.ntiles), tend = (int)min((int64_t)a.ntiles, t0 + (end - u));
-    u += tend - t0;
+  for (int seg = 0;; ++seg) {
+    int idx, t0 = 0, tend = nt;
+    if (seg < full) {
+      idx = seg * kSmBlocks + lane_id;
+    } else if (lane_id < rest) {
+      if (seg > full) break;
+      idx = full * kSmBlocks + lane_id;
+      tend = cut;
+    } else {
+      if (u >= end) break;
+      const int64_t i = u / (nt - cut);
+      idx = full * kSmBlocks + (int)i;
+      t0 = cut + (int)(u - i * (nt - cut));
+      tend = (int)min((int64_t)nt, t0 + (end - u));
+      u += tend - t0;
+    }
     const MxItem it = a.items[1 + idx];
     const int e = it.e, r0 = it.r0, m = it.m;
     const uint8_t* wq = a.wq + (size_t)e * wq_n;
@@ -256,48 +279,75 @@ k_mx_stream(const MxArgs a, float* __restrict__ out0, AT* __restrict__ out1) {
 
     auto run = [&](auto na_c) __attribute__((always_inline)) {
       constexpr int NA = decltype(na_c)::value;   // live 32-row tiles of the pass
+      // Operands from LDS run one step ahead of the products (two waves a SIMD
+      // do not hide its latency otherwise): the activation codes of step j + 1,
+      // and with a stage's last step the next one's codes and scales, on into
+      // the next tile, whose stages begin with 0 again.
+      u32x4 xv[2][NA];
+      uint32_t xs[NA], xn[NA], sw, sn = 0;
+      auto read_x = [&](int s, int j, u32x4 (&v)[NA]) __attribute__((always_inline)) {
+        const uint8_t* x = &lds_x[col * row_bytes + 128 * s + 64 * half + 16 * j];
+#pragma unroll
+        for (int q = 0; q < NA; ++q) v[q] = *reinterpret_cast<const u32x4*>(x + 32 * q * row_bytes);
+      };
+      auto read_xs = [&](int s, uint32_t (&v)[NA]) __attribute__((always_inline)) {
+        const uint8_t* x = &lds_x[col * row_bytes + xsc + kStB * s + 4 * half];
+#pragma unroll
+        for (int q = 0; q < NA; ++q) v[q] = *reinterpret_cast<const uint32_t*>(x + 32 * q * row_bytes);
+      };
+      // scales of the wave's weight rows, stage s (what is read past the row's last block is masked)
+      auto read_sw = [&](int s) __attribute__((always_inline)) {
+        uint32_t v;
+        if constexpr (SM == MxSc::kRun) {
+          const int o = lsc + kStB * s;   // the four bytes may start anywhere
+          const uint32_t* p = reinterpret_cast<const uint32_t*>(&lds_sc[wave][o & ~3]);
+          v = __builtin_amdgcn_alignbyte(p[1], p[0], o & 3);
+        } else {
+          v = *reinterpret_cast<const uint32_t*>(&lds_sc[wave][lsc + kStB * (s % kStB)]);
+        }
+        return mx_mask_scales(v, nb - kStB * s - 4 * half);
+      };
+      if (t < tend) {
+        read_x(0, 0, xv[0]);
+        read_xs(0, xs);
+      }
       for (; t < tend; t += kSmWaves) {
         f32x16 acc[NA];
 #pragma unroll
         for (int q = 0; q < NA; ++q) acc[q] = f32x16{};
         for (int s0 = 0; s0 < SP; s0 += PD) {
-          if (s0 % kStB == 0) {
+          if (s0 % kStB == 0) {   // this group's scales into LDS, the next one's on their way
             store_sc();
             load_sc(t, s0 / kStB + 1);
+            sn = read_sw(s0);
           }
 #pragma unroll
           for (int d = 0; d < PD; ++d) {
             const int s = s0 + d;
-            // stages past the last one multiply its zero weights with stage 0's codes
-            const int sx = s < S ? s : 0;
-            uint32_t sw;
-            if constexpr (SM == MxSc::kRun) {
-              const int o = lsc + kStB * sx;   // the four bytes may start anywhere
-              const uint32_t* p = reinterpret_cast<const uint32_t*>(&lds_sc[wave][o & ~3]);
-              sw = __builtin_amdgcn_alignbyte(p[1], p[0], o & 3);
-            } else {
-              sw = *reinterpret_cast<const uint32_t*>(&lds_sc[wave][lsc + kStB * (s % kStB)]);
-            }
-            sw = mx_mask_scales(sw, nb - kStB * s - 4 * half);
-            const uint8_t* x = &lds_x[col * row_bytes + 128 * sx + 64 * half];
-            uint32_t xs[NA];
-#pragma unroll
-            for (int q = 0; q < NA; ++q)
-              xs[q] = *reinterpret_cast<const uint32_t*>(&lds_x[(32 * q + col) * row_bytes + xsc + kStB * sx + 4 * half]);
+            // stages past the last one multiply zero weights with the first stage's codes
+            const int sx = s < S ? s : 0, next = s + 1 < S ? s + 1 : 0;
+            sw = sn;
             auto step = [&](auto jc) __attribute__((always_inline)) {
               constexpr int J = decltype(jc)::value;
-#pragma unroll
-              for (int q = 0; q < NA; ++q) {
-                const u32x4 xv = *reinterpret_cast<const u32x4*>(x + 32 * q * row_bytes + 16 * J);
-                acc[q] = mx_mfma32<J, J>(w[d][J], xv, acc[q], sw, xs[q]);
+              if constexpr (J < 3) {
+                read_x(sx, J + 1, xv[(J + 1) % 2]);
+              } else {
+                read_x(next, 0, xv[0]);
+                read_xs(next, xn);
+                sn = read_sw(next);
               }
+              __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+              for (int q = 0; q < NA; ++q) acc[q] = mx_mfma32<J, J>(w[d][J], xv[J % 2][q], acc[q], sw, xs[q]);
+              __builtin_amdgcn_sched_barrier(0);
             };
             step(std::integral_constant<int, 0>{});
             step(std::integral_constant<int, 1>{});
             step(std::integral_constant<int, 2>{});
             step(std::integral_constant<int, 3>{});
-            __builtin_amdgcn_sched_barrier(0);   // the next use of these registers is loaded after their products
-            load_w(t, s + PD, d);
+#pragma unroll
+            for (int q = 0; q < NA; ++q) xs[q] = xn[q];
+            load_w(t, s + PD, d);   // into the registers just used
           }
         }
         mx_store<GU, NA>(acc, t, R, r0, m, out0, out1);
@@ -571,7 +621,7 @@ static hipError_t mx_grouped(const XT* x, int64_t rows, int K, int64_t P, const 
     if (plan.mt == 1 && plan.nb > 4 * kStB) I8H_MX(1, 8, kRun);
     else if (plan.mt == 1) I8H_MX(1, 4, kRun);
     else if (plan.mt == 2) I8H_MX(2, 4, kRun);
-    else I8H_MX(4, 4, kRun);
+    else I8H_MX(4, 2, kRun);   // two stages: what its registers leave
   } else if (plan.nb % 16 == 0) {
     if (plan.mt == 1) I8H_MX(1, 8, kPiece);
     else I8H_MX(2, 4, kPiece);
