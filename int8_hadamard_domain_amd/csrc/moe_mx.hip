@@ -10,9 +10,10 @@
 // (products far below the largest of an instruction are kept, unlike the E4M3
 // forms), so the result is as exact as a float32 sum.
 //
-// The weights are the A operand (tiles of 32 rows: for gate_up 16 gate rows and
-// the matching 16 up rows, so both halves of an output meet in one lane), the
-// activation rows the B operand (32 columns). Within a stage of K = 256, step j
+// The weights are the B operand (tiles of 32 rows, one a lane: for gate_up 16
+// gate rows and the matching 16 up rows), the activation rows the A operand, so
+// that neighbouring lanes hold neighbouring features and stores write whole
+// runs of them. Within a stage of K = 256, step j
 // takes block 4 (lane / 32) + j of both operands, so a lane's four scale bytes
 // are one dword, picked by the instruction's byte select, and its codes 64
 // contiguous bytes of its row.
@@ -63,8 +64,8 @@ struct MxArgs {
 // like all others, under a descriptor of size 0. With no branch around a load
 // the compiler counts those in flight exactly and waits only for what it uses.
 typedef __amdgpu_buffer_rsrc_t mx_rsrc;
-__device__ __forceinline__ mx_rsrc mx_buffer(const uint8_t* p, uint32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, (int)bytes, 0x00020000);   // raw, 32-bit data
+__device__ __forceinline__ mx_rsrc mx_buffer(const void* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);   // raw, 32-bit data
 }
 __device__ __forceinline__ u32x4 mx_get16(mx_rsrc r, uint32_t off) {
   return __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0);
@@ -89,48 +90,51 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-__device__ __forceinline__ void put4(float* p, const f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
-__device__ __forceinline__ void put4(uint16_t* p, const f32x4 v) {
-  *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+// one value at offset off, dropped past the descriptor's end
+__device__ __forceinline__ void mx_put(mx_rsrc r, float, float v, uint32_t off) {
+  __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), r, (int)off, 0, 0);
+}
+__device__ __forceinline__ void mx_put(mx_rsrc r, uint16_t, float v, uint32_t off) {
+  __builtin_amdgcn_raw_buffer_store_b16((uint16_t)pack_bf16x2(v, 0.f), r, (int)off, 0, 0);
 }
 
 // The results of one 32-row weight tile for NA x 32 rows from sorted row r0 (m
 // of them live). GU: out0 = gate_up or NULL, out1 = act or NULL; else out0 = y.
+// A lane holds one weight row's products with 16 sorted rows, so a store writes
+// whole runs of features (down: 128 bytes, a cache line) of two or four rows;
+// rows behind m lie past the descriptor and are dropped.
 template <bool GU, int NA, typename AT>
 __device__ __forceinline__ void mx_store(const f32x16 (&acc)[NA], int tile, int R, int r0, int m, float* out0,
                                          AT* out1) {
   const int lane = threadIdx.x % kWave, half = lane / 32, col = lane % 32, I = R / 2;
-  // uniform bases and 32-bit lane offsets, opaque so that the compiler does not
-  // keep the addresses of every store across the tiles
-  uint32_t og = (uint32_t)(col * R + 4 * half), oa = (uint32_t)(col * I + 4 * half);
-  asm volatile("" : "+v"(og), "+v"(oa));
 #pragma unroll
   for (int q = 0; q < NA; ++q) {
-    if (32 * q + col >= m) continue;
+    const uint32_t live = (uint32_t)min(32, m - 32 * q);
     if constexpr (GU) {
-      float* g_b = out0 ? out0 + (size_t)(r0 + 32 * q) * R + tile * 16 : nullptr;
-      AT* a_b = out1 ? out1 + (size_t)(r0 + 32 * q) * I + tile * 16 : nullptr;
+      // Lanes 0..15 hold gate rows, 16..31 the matching up rows: swapped with
+      // the next register, one register holds the gates of sorted rows j and
+      // j + 1 (lanes 0..15, 16..31), the other their ups.
+      const mx_rsrc g_r = mx_buffer(out0 + (size_t)(r0 + 32 * q) * R, out0 ? live * R * 4 : 0);
+      const mx_rsrc a_r = mx_buffer(out1 + (size_t)(r0 + 32 * q) * I, out1 ? live * I * sizeof(AT) : 0);
+      const int row = 4 * half + col / 16, n = tile * 16 + col % 16;
+      const uint32_t og = 4 * (uint32_t)(row * R + n), oa = sizeof(AT) * (uint32_t)(row * I + n);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        // gate rows 8 h + 4 half .. +3 of the tile in registers 4 h .. +3, their up rows in 8 + 4 h .. +3
-        f32x4 g, u, v;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          g[j] = acc[q][4 * h + j];
-          u[j] = acc[q][8 + 4 * h + j];
-          v[j] = gelu_tanh(g[j]) * u[j];
+      for (int r = 0; r < 16; r += 2) {
+        const uint32_t j = 8 * (r / 4) + r % 4;
+        const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[q][r]), __float_as_uint(acc[q][r + 1]),
+                                                        false, false);
+        const float g = __uint_as_float(s[0]), u = __uint_as_float(s[1]);
+        if (out0) {
+          mx_put(g_r, 0.f, g, og + 4 * j * R);
+          mx_put(g_r, 0.f, u, og + 4 * (I + j * R));
         }
-        if (g_b) {
-          put4(g_b + (og + 8 * h), g);
-          put4(g_b + (og + I + 8 * h), u);
-        }
-        if (a_b) put4(a_b + (oa + 8 * h), v);
+        if (out1) mx_put(a_r, AT{}, gelu_tanh(g) * u, oa + sizeof(AT) * j * I);
       }
     } else {
-      float* y_b = out0 + (size_t)(r0 + 32 * q) * R + tile * 32;
+      const mx_rsrc y_r = mx_buffer(out0 + (size_t)(r0 + 32 * q) * R, live * R * 4);
+      const uint32_t oy = 4 * (uint32_t)(4 * half * R + tile * 32 + col);
 #pragma unroll
-      for (int h = 0; h < 4; ++h)
-        put4(y_b + (og + 8 * h), f32x4{acc[q][4 * h], acc[q][4 * h + 1], acc[q][4 * h + 2], acc[q][4 * h + 3]});
+      for (int r = 0; r < 16; ++r) mx_put(y_r, 0.f, acc[q][r], oy + 4 * (8 * (r / 4) + r % 4) * R);
     }
   }
 }
@@ -338,7 +342,7 @@ k_mx_stream(const MxArgs a, float* __restrict__ out0, AT* __restrict__ out1) {
               }
               __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-              for (int q = 0; q < NA; ++q) acc[q] = mx_mfma32<J, J>(w[d][J], xv[J % 2][q], acc[q], sw, xs[q]);
+              for (int q = 0; q < NA; ++q) acc[q] = mx_mfma32<J, J>(xv[J % 2][q], w[d][J], acc[q], xs[q], sw);
               __builtin_amdgcn_sched_barrier(0);
             };
             step(std::integral_constant<int, 0>{});
@@ -458,7 +462,7 @@ k_mx_ring(const MxArgs a, float* __restrict__ out0, AT* __restrict__ out1) {
 #pragma unroll
           for (int q = 0; q < NA; ++q) {
             const u32x4 xv = *reinterpret_cast<const u32x4*>(x + 32 * q * kRgTile + 16 * J);
-            acc[q] = mx_mfma32<J, J>(w[d][J], xv, acc[q], wsc[d], xs[q]);
+            acc[q] = mx_mfma32<J, J>(xv, w[d][J], acc[q], xs[q], wsc[d]);
           }
         };
         step(std::integral_constant<int, 0>{});
