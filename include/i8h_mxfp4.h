@@ -35,7 +35,8 @@ enum { I8H_F32 = 0, I8H_BF16 = 1 };
  *   code = E2M1(x * 2^(127 - s))                (nearest, ties to the even
  *          code, magnitudes above 6 become 6, the sign of zero is kept)
  * which is the conversion that the MX specification gives for E2M1. A block
- * with an infinity or NaN gets s = 255 and codes 0. */
+ * with an infinity or NaN gets s = 255 and codes 0. T*K above 2^35 - 2048:
+ * I8H_EUNSUPPORTED (for both calls). */
 int mxfp4_quantize(const void* x, int x_type, int T, int K, uint8_t* codes, uint8_t* scales, void* stream);
 
 /* The values that codes and scales stand for: out [T, K] (out_type, 16-B
@@ -70,8 +71,8 @@ int moe_gateup_mxfp4_grouped(const uint16_t* x, int T, int K, const uint8_t* cod
  *   y[r, h]   = sum_b 2^(sw[e,h,b] + sa[r,b] - 254) sum_{i in b} qw[e,h,i] qa[r,i]
  *   out[t, h] = sum_j topk_w[t, j] * y[pair_pos[t*topk + j], h]   (slot order)
  * codes [E, H, I/2] 16-B aligned, scales [E, H, I/32] 4-B aligned; H % 32 ==
- * 0 (H % 8 != 0: I8H_EINVAL, else I8H_EUNSUPPORTED), H*I < 2^32 and
- * T*topk*(I + 256) < 2^32 (else I8H_EUNSUPPORTED). out float32 [T, H],
+ * 0 (H % 8 != 0: I8H_EINVAL, else I8H_EUNSUPPORTED), H < 2^25, H*I <
+ * 2^32 and T*topk*(I + 256) < 2^32 (else I8H_EUNSUPPORTED). out float32 [T, H],
  * 16-B aligned. topk_ids, topk_w, expert_off, pair_pos: as moe_route_permute
  * writes them. workspace: at least moe_down_mxfp4_workspace_size(T, I, E,
  * H, topk) bytes, 256-B aligned (may be NULL when that size is 0,

@@ -499,6 +499,15 @@ def i8g_workspace_views(workspace, T, K):
     return qx, sx
 
 
+def _call(fn, device, *args):
+    """Call the library's fn(*args, stream) on `device`'s current stream, with
+    `device` current: kernels launch on the current device only."""
+    if torch._C._cuda_getDevice() != device.index:
+        with torch.cuda.device(device):
+            return _call(fn, device, *args)
+    _check(fn, getattr(lib(), fn)(*args, _stream(device)))
+
+
 def _type(t, name):
     """The library's element type of a float32 or bfloat16 tensor."""
     if not isinstance(t, torch.Tensor) or t.dtype not in TYPES:
@@ -542,8 +551,7 @@ def mxfp4_quantize(x, codes=None, scales=None):
     lead, K, rows = _mx_shape(x, "x", 32, 1)
     codes = _mx_out(codes, "codes", lead + (K // 2,), torch.uint8, x)
     scales = _mx_out(scales, "scales", lead + (K // 32,), torch.uint8, x)
-    _check("mxfp4_quantize", lib().mxfp4_quantize(
-        x.data_ptr(), xt, rows, K, codes.data_ptr(), scales.data_ptr(), _stream(x.device)))
+    _call("mxfp4_quantize", x.device, x.data_ptr(), xt, rows, K, codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
@@ -558,8 +566,8 @@ def mxfp4_dequantize(codes, scales, dtype=torch.bfloat16, out=None):
     if dtype not in TYPES:
         raise TypeError(f"dtype must be float32 or bfloat16 (got {dtype})")
     out = _mx_out(out, "out", lead + (K,), dtype, codes)
-    _check("mxfp4_dequantize", lib().mxfp4_dequantize(
-        codes.data_ptr(), scales.data_ptr(), rows, K, out.data_ptr(), TYPES[dtype], _stream(codes.device)))
+    _call("mxfp4_dequantize", codes.device, codes.data_ptr(), scales.data_ptr(), rows, K, out.data_ptr(),
+          TYPES[dtype])
     return out
 
 
@@ -583,9 +591,8 @@ def moe_gateup_mxfp4_grouped(x, codes, scales, topk, expert_off, sorted_pairs,
     gu = _out(gate_up, (T * topk, N), dev)
     adt = _act_dtype(act, act_dtype)
     ac = _out(act, (T * topk, N // 2), dev, adt)
-    _check("moe_gateup_mxfp4_grouped", lib().moe_gateup_mxfp4_grouped(
-        _ptr(x), T, K, _ptr(codes), _ptr(scales), E, N, topk, _ptr(expert_off), _ptr(sorted_pairs),
-        _ptr(gu), _ptr(ac), TYPES[adt], _ptr(workspace), need, _stream(dev)))
+    _call("moe_gateup_mxfp4_grouped", dev, _ptr(x), T, K, _ptr(codes), _ptr(scales), E, N, topk, _ptr(expert_off),
+          _ptr(sorted_pairs), _ptr(gu), _ptr(ac), TYPES[adt], _ptr(workspace), need)
     return gu, ac
 
 
@@ -613,9 +620,8 @@ def moe_down_mxfp4_combine(act, codes, scales, routing, out=None, workspace=None
         out = torch.empty((T, H), dtype=torch.float32, device=dev)
     else:
         _dev(out, "out", torch.float32, shape=(T, H), device=dev)
-    _check("moe_down_mxfp4_combine", lib().moe_down_mxfp4_combine(
-        _ptr(act), at, T, I, _ptr(codes), _ptr(scales), E, H, topk, _ptr(ids), _ptr(tw), _ptr(off), _ptr(pos),
-        _ptr(out), _ptr(workspace), need, _stream(dev)))
+    _call("moe_down_mxfp4_combine", dev, _ptr(act), at, T, I, _ptr(codes), _ptr(scales), E, H, topk, _ptr(ids),
+          _ptr(tw), _ptr(off), _ptr(pos), _ptr(out), _ptr(workspace), need)
     return out
 
 
@@ -649,7 +655,6 @@ def draft_verify(target_probs, draft_probs, drafted, u, u_next, draft_len=None, 
     accepted = (torch.empty((B,), dtype=torch.int32, device=dev) if accepted is None
                 else _dev(accepted, "accepted", torch.int32, shape=(B,), device=dev))
     workspace = _workspace(workspace, "workspace", lib().draft_verify_workspace_size(B, V), dev)
-    _check("draft_verify", lib().draft_verify(
-        _ptr(target_probs), _ptr(draft_probs), pt, _ptr(drafted), _ptr(draft_len), _ptr(u), _ptr(u_next), B, D, V,
-        _ptr(tokens), _ptr(accepted), _ptr(workspace), workspace.numel(), _stream(dev)))
+    _call("draft_verify", dev, _ptr(target_probs), _ptr(draft_probs), pt, _ptr(drafted), _ptr(draft_len), _ptr(u),
+          _ptr(u_next), B, D, V, _ptr(tokens), _ptr(accepted), _ptr(workspace), workspace.numel())
     return tokens, accepted

@@ -25,8 +25,8 @@ inline bool is_type(int t) { return t == I8H_F32 || t == I8H_BF16; }
 // the products address the quantised rows with 32-bit offsets (144 bytes a stage of 256)
 inline bool rows_fit(int64_t rows, int K) { return rows * ((int64_t)K + i8h::kMxStage) < ((int64_t)1 << 32); }
 
-// a kernel per 8 values, 256 threads a workgroup
-inline bool quant_fits(int64_t rows, int K) { return rows * (K / 8) < ((int64_t)1 << 38); }
+// a thread per 8 values: a launch holds fewer than 2^32 threads, in workgroups of 256
+inline bool quant_fits(int64_t rows, int K) { return rows * (K / 8) <= ((int64_t)1 << 32) - 256; }
 
 }  // namespace
 
@@ -96,7 +96,8 @@ int moe_down_mxfp4_combine(const void* act, int act_type, int T, int I, const ui
   if (!is_type(act_type) || T < 0 || I <= 0 || (I % 32) != 0 || H <= 0 || (H % 8) != 0 || E <= 0 || topk <= 0)
     return I8H_EINVAL;
   if (E > kMaxExperts || topk > kMaxTopk || topk > E) return I8H_EUNSUPPORTED;
-  if ((H % 32) != 0 || (int64_t)H * I >= (int64_t)1 << 32) return I8H_EUNSUPPORTED;
+  // 32-bit offsets in an expert, and in 32 rows of y
+  if ((H % 32) != 0 || (int64_t)H * I >= (int64_t)1 << 32 || H >= 1 << 25) return I8H_EUNSUPPORTED;
   const int64_t P = (int64_t)T * topk;
   if (P >= (int64_t)1 << 31) return I8H_EUNSUPPORTED;
   if (!rows_fit(P, I)) return I8H_EUNSUPPORTED;

@@ -609,7 +609,6 @@ static hipError_t mx_grouped(const XT* x, int64_t rows, int K, int64_t P, const 
   const int64_t n8 = rows * plan.nbp * 4, qgrid = 1 + (n8 + kPrThreads - 1) / kPrThreads;
   const int ntiles = R / 32;
   const int64_t rgrid = plan.passes(P, E) * cdiv(ntiles, kRgWaves);
-  if (qgrid >= ((int64_t)1 << 31) || (!plan.stream && rgrid >= ((int64_t)1 << 31))) return hipErrorInvalidValue;
   MxItem* items = reinterpret_cast<MxItem*>(ws + lay.items);
   k_mx_prepare<<<(unsigned)qgrid, kPrThreads, 0, st>>>(x, n8, plan.nb, plan.nbp, plan.row_bytes, ws, expert_off, E,
                                                        32 * plan.mt, items);

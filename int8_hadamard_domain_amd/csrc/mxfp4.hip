@@ -82,7 +82,6 @@ k_mxfp4_dequantize(const uint32_t* __restrict__ codes, const uint8_t* __restrict
 hipError_t launch_mxfp4_quantize(const void* x, bool bf16, int64_t values, uint8_t* codes, uint8_t* scales,
                                  hipStream_t st) {
   const int64_t n8 = values / 8, per = kMxGroups * kMxThreads, grid = (n8 + per - 1) / per;
-  if (grid >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
   uint32_t* c = reinterpret_cast<uint32_t*>(codes);
   if (bf16)
     k_mxfp4_quantize<<<(unsigned)grid, kMxThreads, 0, st>>>(static_cast<const uint16_t*>(x), n8, c, scales);
@@ -94,7 +93,6 @@ hipError_t launch_mxfp4_quantize(const void* x, bool bf16, int64_t values, uint8
 hipError_t launch_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t values, void* out, bool bf16,
                                    hipStream_t st) {
   const int64_t n8 = values / 8, grid = (n8 + kMxThreads - 1) / kMxThreads;
-  if (grid >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
   const uint32_t* c = reinterpret_cast<const uint32_t*>(codes);
   if (bf16)
     k_mxfp4_dequantize<<<(unsigned)grid, kMxThreads, 0, st>>>(c, scales, n8, static_cast<uint16_t*>(out));

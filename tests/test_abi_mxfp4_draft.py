@@ -50,7 +50,8 @@ def test_quantiser_validation(L, name):
     assert call(T=-1) == EINVAL and call(K=0) == EINVAL and call(K=48) == EINVAL and call(K=-32) == EINVAL
     assert call(x=None) == EINVAL and call(c=None) == EINVAL and call(s=None) == EINVAL
     assert call(x=EIGHT) == EINVAL and call(c=EIGHT) == EINVAL
-    assert call(T=(1 << 31) - 1, K=2048) == EUNSUP          # more workgroups than a launch takes
+    assert call(T=(1 << 31) - 1, K=2048) == EUNSUP          # more threads than a launch takes
+    assert call(T=1 << 24, K=2048) == EUNSUP and call(T=1 << 30, K=32) == EUNSUP
     assert call(T=0) == OK and call(T=0, x=None, c=None, s=None) == OK
 
 
@@ -85,7 +86,8 @@ def test_down_validation(L):
                 dict(out=None), dict(a=EIGHT), dict(c=EIGHT), dict(s=ODD), dict(ids=ODD), dict(w=ODD), dict(off=ODD),
                 dict(pos=ODD), dict(out=EIGHT), dict(ws=None), dict(ws=EIGHT), dict(wsb=need - 1)):
         assert call(**bad) == EINVAL, bad
-    for bad in (dict(H=72), dict(E=1025), dict(k=5), dict(E=64, k=33), dict(T=1 << 28, k=32, E=64), dict(T=1 << 25)):
+    for bad in (dict(H=72), dict(E=1025), dict(k=5), dict(E=64, k=33), dict(T=1 << 28, k=32, E=64), dict(T=1 << 25),
+                dict(H=1 << 25, I=32), dict(H=1 << 25, I=96), dict(H=1 << 24, I=256)):
         assert call(**bad) == EUNSUP, bad
     assert call(T=0) == OK
 
@@ -122,3 +124,31 @@ def test_binding_refuses_what_does_not_fit():
         i8h.moe_down_mxfp4_combine(torch.zeros((2, 32), dtype=torch.float16), None, None, {})
     with pytest.raises(TypeError):
         i8h.draft_verify(torch.zeros((1, 2, 3), dtype=torch.float64), None, None, None, None)
+
+
+def test_calls_run_on_their_tensors_device(monkeypatch):
+    """Tensors of another device than the current one: the call makes theirs current and takes its stream."""
+    current, seen = [0], []
+
+    class Guard:
+        def __init__(self, device):
+            self.index = device.index
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.index
+
+        def __exit__(self, *exc):
+            current[0] = self.before
+
+    class Lib:
+        def draft_verify(self, *args):
+            seen.append((current[0], args))
+            return OK
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0])
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 1000 + index)
+    monkeypatch.setattr(torch.cuda, "device", Guard)
+    monkeypatch.setattr(i8h, "lib", lambda: Lib())
+    i8h._call("draft_verify", torch.device("cuda", 0), 7)
+    i8h._call("draft_verify", torch.device("cuda", 3), 8)
+    assert seen == [(0, (7, 1000)), (3, (8, 1003))] and current == [0]
