@@ -140,3 +140,81 @@ def test_no_sequences(gpu_available):
     e = lambda *s, dt=torch.float32: torch.empty(s, dtype=dt, device="cuda")  # noqa: E731
     t, n = i8h.draft_verify(e(0, 4, 9), e(0, 3, 9), e(0, 3, dt=torch.int32), e(0, 3), e(0))
     assert t.shape == (0, 4) and n.shape == (0,)
+
+
+# ------------------------------------------------------------------------------------- many chunks, large tensors
+
+def _running(P, Q, x, length, u, un):
+    """One sequence against extended-precision running sums."""
+    n = 0
+    while n < length and float(u[n]) * (1.0 if Q is None else Q[n, x[n]]) < P[n, x[n]]:
+        n += 1
+    rest = P[n].copy()
+    if n < length:
+        if Q is None:
+            rest[x[n]] = 0
+        else:
+            rest = np.maximum(rest - Q[n], 0)
+    cum = np.cumsum(rest.astype(np.longdouble))
+    target = np.longdouble(un) * cum[-1]
+    assert np.abs(cum - target).min() > len(rest) * 2.0 ** -50 * cum[-1]
+    return n, int((cum <= target).sum())
+
+
+@pytest.mark.parametrize("B,V,dtype", [(1, 1 << 20, torch.float32), (2, 1100003, torch.float32),
+                                       (2, 1100004, torch.bfloat16), (90, 40000, torch.bfloat16),
+                                       (300, 8192, torch.float32), (300, 8191, torch.bfloat16)])
+@pytest.mark.parametrize("greedy", [False, True])
+def test_many_chunks(gpu_available, B, V, dtype, greedy):
+    """Rows of more chunks than a workgroup has threads, and batches that take the larger chunks."""
+    print(f"draft_verify B={B} V={V} {dtype} greedy={greedy}", flush=True)
+    D = 2
+    p, q, x, length, u, un = _case(B, D, V, V + B, greedy, dtype)
+    un[0] = 0.999
+    got_t, got_n = _gpu(p, q, x, length, u, un)
+    P, Q = _np(p), _np(q)
+    for b in range(0, B, max(1, B // 12)):
+        n, nxt = _running(P[b], None if Q is None else Q[b], x[b], length[b], u[b], un[b])
+        assert got_n[b] == n and got_t[b].tolist() == x[b, :n].tolist() + [nxt] + [-1] * (D - n)
+
+
+def test_probabilities_past_2_31_elements(gpu_available):
+    """A row that starts past 2^31 elements is found, kept and drawn from."""
+    B, D, V = 2, 1023, (1 << 20) + 5
+    p = torch.zeros((B, D + 1, V), dtype=torch.bfloat16, device="cuda")
+    print("draft_verify past 2^31 elements", flush=True)
+    assert p.numel() > 1 << 31
+    x = torch.randint(0, V, (B, D), generator=torch.Generator().manual_seed(1)).int()
+    x[1, 1000] = 77
+    for b in range(B):
+        p[b, torch.arange(D, device="cuda"), x[b].long().cuda()] = 1.0
+    p[1, 1000, 77] = 0.0                            # refused there
+    p[1, 1000, V - 3] = 0.5
+    p[0, D, 123456] = 0.25
+    p[0, D, 654321] = 0.75
+    u, un = np.full((B, D), 0.5, np.float32), np.array([0.3, 0.9], np.float32)
+    c = lambda a: torch.from_numpy(a).cuda()  # noqa: E731
+    tokens, accepted = i8h.draft_verify(p, None, x.cuda(), c(u), c(un))
+    assert accepted.tolist() == [D, 1000]
+    want = torch.cat([x[0], torch.tensor([654321], dtype=torch.int32)])
+    assert torch.equal(tokens[0].cpu(), want)
+    assert tokens[1].tolist() == x[1, :1000].tolist() + [V - 3] + [-1] * 23
+
+
+def test_unaligned_rows_and_outputs(gpu_available):
+    """Rows at every alignment of their element, outputs inside larger buffers."""
+    B, D, V = 3, 2, 1027
+    for dtype in (torch.float32, torch.bfloat16):
+        print(f"draft_verify unaligned {dtype}", flush=True)
+        p, q, x, length, u, un = _case(B, D, V, 31, False, dtype)
+        want = draft.verify_batch(_np(p), _np(q), x, length, u, un)
+        for shift in (1, 2, 3):
+            pb = torch.empty(p.numel() + shift, dtype=dtype, device="cuda")[shift:].view(p.shape)
+            pb.copy_(p)
+            qb = torch.empty(q.numel() + 4 - shift, dtype=dtype, device="cuda")[4 - shift:].view(q.shape)
+            qb.copy_(q)
+            tok = torch.full((B + 2, D + 1), 9, dtype=torch.int32, device="cuda")
+            acc = torch.full((B + 2,), 9, dtype=torch.int32, device="cuda")
+            t, n = _gpu(pb, qb, x, length, u, un, tokens=tok[1:-1], accepted=acc[1:-1])
+            assert np.array_equal(n, want[1]) and np.array_equal(t, want[0])
+            assert (tok[0] == 9).all() and (tok[-1] == 9).all() and acc[0] == 9 and acc[-1] == 9
