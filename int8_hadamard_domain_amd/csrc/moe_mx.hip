@@ -121,6 +121,7 @@ __device__ __forceinline__ void mx_store(const f32x16 (&acc)[NA], int tile, int 
 #pragma unroll
       for (int r = 0; r < 16; r += 2) {
         const uint32_t j = 8 * (r / 4) + r % 4;
+        if (8 * (r / 4) >= live) break;
         const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[q][r]), __float_as_uint(acc[q][r + 1]),
                                                         false, false);
         const float g = __uint_as_float(s[0]), u = __uint_as_float(s[1]);
@@ -134,7 +135,10 @@ __device__ __forceinline__ void mx_store(const f32x16 (&acc)[NA], int tile, int 
       const mx_rsrc y_r = mx_buffer(out0 + (size_t)(r0 + 32 * q) * R, live * R * 4);
       const uint32_t oy = 4 * (uint32_t)(4 * half * R + tile * 32 + col);
 #pragma unroll
-      for (int r = 0; r < 16; ++r) mx_put(y_r, 0.f, acc[q][r], oy + 4 * (8 * (r / 4) + r % 4) * R);
+      for (int r = 0; r < 16; ++r) {
+        if (8 * (r / 4) >= live) break;
+        mx_put(y_r, 0.f, acc[q][r], oy + 4 * (8 * (r / 4) + r % 4) * R);
+      }
     }
   }
 }
