@@ -74,6 +74,11 @@ __device__ __forceinline__ uint32_t mx_get4(mx_rsrc r, uint32_t off) {
   return __builtin_amdgcn_raw_buffer_load_b32(r, (int)off, 0, 0);
 }
 
+// the same 16 bytes to LDS, lane l's at p + 16 l, with no register between
+__device__ __forceinline__ void mx_get16_lds(mx_rsrc r, uint8_t* p, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)p, 16, (int)off, 0, 0, 0);
+}
+
 // The four scale bytes v of a lane's blocks, of which the row has `left` from
 // there on: what is read past a row's last block meets activation codes of
 // zero, and the scale 1 keeps another row's NaN scale out.
@@ -88,6 +93,58 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// A stage of weights as the matrix unit wants it (lane: its row's four pieces of
+// 16 bytes, one a register) from how it is loaded (register k: piece lane % 4 of
+// the lane's quad's row k). A quad's four lanes then read 64 contiguous bytes,
+// which the load path takes at 52 bytes a clock and CU; each lane reading its
+// own row's, it takes 15. Two rounds of exchanges between neighbours: a and b
+// are registers k and k + HOP, lanes with bit HOP of k set keep b and fetch b of
+// the lane HOP below into a, the others keep a and fetch a into b. One
+// instruction a word: a select whose one side comes from another lane, which the
+// compiler does not form by itself. The blocks wait out the two cycles between
+// a vector write and a lane move's, or a matrix instruction's, read.
+#define I8H_SEL(D, MOVED, KEPT) "v_cndmask_b32_dpp " D ", " MOVED ", " KEPT ", vcc " I8H_PERM "\n"
+#define I8H_EXCHANGE                                                                                              \
+  "s_nop 1\n"                                                                                                     \
+  "s_mov_b64 vcc, %[set]\n" /* b of the lanes whose bit is not set comes from a */                                \
+  I8H_SEL("%[t0]", "%[a0]", "%[b0]") I8H_SEL("%[t1]", "%[a1]", "%[b1]")                                           \
+  I8H_SEL("%[t2]", "%[a2]", "%[b2]") I8H_SEL("%[t3]", "%[a3]", "%[b3]")                                           \
+  "s_not_b64 vcc, vcc\n" /* a of the others from b */                                                             \
+  I8H_SEL("%[a0]", "%[b0]", "%[a0]") I8H_SEL("%[a1]", "%[b1]", "%[a1]")                                           \
+  I8H_SEL("%[a2]", "%[b2]", "%[a2]") I8H_SEL("%[a3]", "%[b3]", "%[a3]")                                           \
+  "s_nop 1"
+template <int HOP>
+__device__ __forceinline__ void mx_exchange(u32x4& a, u32x4& b) {
+  uint32_t t0, t1, t2, t3, a0 = a[0], a1 = a[1], a2 = a[2], a3 = a[3];
+#define I8H_REGS                                                                                                  \
+  : [t0] "=&v"(t0), [t1] "=&v"(t1), [t2] "=&v"(t2), [t3] "=&v"(t3), [a0] "+v"(a0), [a1] "+v"(a1), [a2] "+v"(a2),   \
+    [a3] "+v"(a3)                                                                                                 \
+  : [b0] "v"(b[0]), [b1] "v"(b[1]), [b2] "v"(b[2]), [b3] "v"(b[3]), [set] "s"(lanes)                              \
+  : "vcc", "scc"
+  if constexpr (HOP == 1) {
+    const uint64_t lanes = 0xaaaaaaaaaaaaaaaaull;
+#define I8H_PERM "quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf"
+    asm(I8H_EXCHANGE I8H_REGS);
+#undef I8H_PERM
+  } else {
+    const uint64_t lanes = 0xccccccccccccccccull;
+#define I8H_PERM "quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf"
+    asm(I8H_EXCHANGE I8H_REGS);
+#undef I8H_PERM
+  }
+#undef I8H_REGS
+  a = u32x4{a0, a1, a2, a3};
+  b = u32x4{t0, t1, t2, t3};
+}
+#undef I8H_EXCHANGE
+#undef I8H_SEL
+__device__ __forceinline__ void mx_transpose(u32x4 (&w)[4]) {
+  mx_exchange<1>(w[0], w[1]);
+  mx_exchange<1>(w[2], w[3]);
+  mx_exchange<2>(w[0], w[2]);
+  mx_exchange<2>(w[1], w[3]);
 }
 
 // one value at offset off, dropped past the descriptor's end
@@ -211,7 +268,8 @@ k_mx_stream(const MxArgs a, float* __restrict__ out0, AT* __restrict__ out1) {
     // offsets of the lane's row of tile 0; tstep rows further on for each tile
     const int n0 = GU ? (col < 16 ? col : I + col - 16) : col;
     constexpr int tstep = GU ? 16 : 32;
-    const uint32_t qo = (uint32_t)n0 * (16 * nb) + 64 * half;
+    // a lane loads piece lane % 4 of its quad's four rows (mx_transpose)
+    const uint32_t qo = (uint32_t)(n0 - col % 4) * (16 * nb) + 64 * half + 16 * (lane % 4);
 
     // stage s of the wave's tile t, or past SP of its next one
     u32x4 w[PD][4];
@@ -223,7 +281,7 @@ k_mx_stream(const MxArgs a, float* __restrict__ out0, AT* __restrict__ out1) {
       const mx_rsrc q = mx_buffer(wq, s < S && t < tend ? wq_n : 0);
       const uint32_t o = qo + ((uint32_t)(t * tstep) * (16 * nb) + 128 * s);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w[d][j] = mx_get16(q, o + 16 * j);
+      for (int j = 0; j < 4; ++j) w[d][j] = mx_get16(q, o + (uint32_t)(j * 16 * nb));
     };
     // scales of tile t, blocks 64 g and on (g past the last group: of the next tile)
     const int groups = SM == MxSc::kRun ? 1 : (nb + kSmGroup - 1) / kSmGroup;
@@ -266,22 +324,13 @@ k_mx_stream(const MxArgs a, float* __restrict__ out0, AT* __restrict__ out1) {
     if (tid < m) lds_row[tid] = (uint32_t)(GU ? a.sorted_pairs[r0 + tid] / a.topk : r0 + tid) * (uint32_t)row_bytes;
     lds_barrier();
     {
-      constexpr int U = 4;
       const int n = m * pieces;
       const mx_rsrc x = mx_buffer(a.x, a.x_n);
-      for (int p0 = tid; p0 < n; p0 += U * kSmThreads) {
-        u32x4 v[U];
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-          const int p = min(p0 + i * kSmThreads, n - 1), row = p / pieces;
-          v[i] = mx_get16(x, lds_row[row] + 16 * (p - row * pieces));
-        }
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-          const int p = min(p0 + i * kSmThreads, n - 1);
-          *reinterpret_cast<u32x4*>(&lds_x[16 * p]) = v[i];
-        }
+      for (int p0 = wave * kWave; p0 < n; p0 += kSmThreads) {
+        const int p = p0 + lane, row = p / pieces;
+        if (p < n) mx_get16_lds(x, &lds_x[16 * p0], lds_row[row] + 16 * (p - row * pieces));
       }
+      __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt(0)
     }
     lds_barrier();
 
@@ -335,6 +384,7 @@ k_mx_stream(const MxArgs a, float* __restrict__ out0, AT* __restrict__ out1) {
             // stages past the last one multiply zero weights with the first stage's codes
             const int sx = s < S ? s : 0, next = s + 1 < S ? s + 1 : 0;
             sw = sn;
+            mx_transpose(w[d]);
             auto step = [&](auto jc) __attribute__((always_inline)) {
               constexpr int J = decltype(jc)::value;
               if constexpr (J < 3) {
@@ -624,17 +674,20 @@ static hipError_t mx_grouped(const XT* x, int64_t rows, int K, int64_t P, const 
   if (!plan.stream) {
     k_mx_ring<GU><<<(unsigned)rgrid, kRgThreads, 0, st>>>(a, out0, out1);
   } else if (plan.nb <= kSmGroup) {
-    // short rows (up to 4 stages) would fill half of an 8-deep prefetch
-    if (plan.mt == 1 && plan.nb > 4 * kStB) I8H_MX(1, 8, kRun);
-    else if (plan.mt == 1) I8H_MX(1, 4, kRun);
+    // Depth of the prefetch: what the registers leave, and for short rows no more
+    // than a tile's stages, since those past the last are products of zeros
+    if (plan.mt == 1 && plan.nb <= 3 * kStB) I8H_MX(1, 3, kRun);
+    else if (plan.mt == 1 && plan.nb <= 4 * kStB) I8H_MX(1, 4, kRun);
+    else if (plan.mt == 1) I8H_MX(1, 8, kRun);
     else if (plan.mt == 2) I8H_MX(2, 4, kRun);
-    else I8H_MX(4, 2, kRun);   // two stages: what its registers leave
+    else if (plan.nb <= 3 * kStB) I8H_MX(4, 3, kRun);   // K = 768, 2048 tokens: 84 us, two deep 87; K = 2048: 85, 81
+    else I8H_MX(4, 2, kRun);
   } else if (plan.nb % 16 == 0) {
     if (plan.mt == 1) I8H_MX(1, 8, kPiece);
-    else I8H_MX(2, 4, kPiece);
+    else I8H_MX(2, 2, kPiece);
   } else {
     if (plan.mt == 1) I8H_MX(1, 8, kWord);
-    else I8H_MX(2, 4, kWord);
+    else I8H_MX(2, 2, kWord);
   }
 #undef I8H_MX
   return hipGetLastError();
