@@ -52,14 +52,15 @@ k_gateup_mx_few(const uint16_t* __restrict__ x, int T, int nb, const uint8_t* __
   const int tid = threadIdx.x, lane = tid % kWave, g = lane / 16, c = lane % 16;
   const int I = N / 2, K = nb * kMxBlock, row_bytes = few_row_bytes(nb);
 
-  // the expert whose first sorted row is this slot, from one batch of loads a
-  // 64 experts; a slot that is not an expert's first row has nothing to do
-  const int slot = blockIdx.y;
-  int e = 0, r0 = 0, m = 0;
+  // the y-th expert that has pairs, from one batch of loads a 64 experts; the
+  // workgroups past the last such expert come last in the grid
+  int e = 0, r0 = 0, m = 0, seen = 0;
   for (int e0 = 0; e0 < E; e0 += kWave) {
     const int i = e0 + lane;
     const int lo = i < E ? off[i] : 0, hi = i < E ? off[i + 1] : 0;
-    const uint64_t here = __ballot(lo <= slot && slot < hi);
+    const uint64_t some = __ballot(lo < hi);
+    const int rank = seen + __popcll(some & ((1ull << lane) - 1));
+    const uint64_t here = __ballot(lo < hi && rank == (int)blockIdx.y);
     if (here != 0) {
       const int src = __ffsll((unsigned long long)here) - 1;
       e = __builtin_amdgcn_readfirstlane(e0 + src);
@@ -67,8 +68,9 @@ k_gateup_mx_few(const uint16_t* __restrict__ x, int T, int nb, const uint8_t* __
       m = __builtin_amdgcn_readfirstlane(__shfl(hi, src, kWave)) - r0;
       break;
     }
+    seen += __popcll(some);
   }
-  if (m == 0 || r0 != slot) return;
+  if (m == 0) return;
 
   // weight row of this lane: rows 4 G, 4 G + 1 of a tile are gate rows 2 G, 2 G + 1,
   // rows 4 G + 2, 4 G + 3 the matching up rows
@@ -237,7 +239,7 @@ hipError_t launch_gateup_mxfp4_few(const uint16_t* x, int T, int K, const uint8_
                                    int N, int k, const int32_t* expert_off, const int32_t* sorted_pairs, float* gu,
                                    void* act, bool act_bf16, hipStream_t st) {
   const int nb = K / kMxBlock;
-  const dim3 grid(cdiv(N / 16, kFgWaves), T * k);
+  const dim3 grid(cdiv(N / 16, kFgWaves), T * k < E ? T * k : E);
   const size_t lds = (size_t)T * few_row_bytes(nb);
   if (act_bf16)
     k_gateup_mx_few<<<grid, kFgThreads, lds, st>>>(x, T, nb, codes, scales, E, N, k, expert_off, sorted_pairs, gu,
