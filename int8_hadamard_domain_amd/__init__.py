@@ -650,9 +650,9 @@ def draft_verify(target_probs, draft_probs, drafted, u, u_next, draft_len=None, 
     _dev(u_next, "u_next", torch.float32, shape=(B,), device=dev)
     if draft_len is not None:
         _dev(draft_len, "draft_len", torch.int32, shape=(B,), device=dev)
-    tokens = (torch.empty((B, D + 1), dtype=torch.int32, device=dev) if tokens is None
+    tokens = (drafted.new_empty((B, D + 1)) if tokens is None
               else _dev(tokens, "tokens", torch.int32, shape=(B, D + 1), device=dev))
-    accepted = (torch.empty((B,), dtype=torch.int32, device=dev) if accepted is None
+    accepted = (drafted.new_empty(B) if accepted is None
                 else _dev(accepted, "accepted", torch.int32, shape=(B,), device=dev))
     workspace = _workspace(workspace, "workspace", lib().draft_verify_workspace_size(B, V), dev)
     _call("draft_verify", dev, _ptr(target_probs), _ptr(draft_probs), pt, _ptr(drafted), _ptr(draft_len), _ptr(u),
