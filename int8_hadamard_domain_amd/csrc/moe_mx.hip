@@ -55,7 +55,9 @@ struct MxArgs {
   uint32_t x_n;        // bytes of x, rounded up so that 16-byte reads of scales end inside
   int row_bytes;
   int E, R, nb, topk, ntiles;
-  const MxItem* items;
+  const MxItem* items;           // NULL where the kernel finds passes and quantises rows itself, from:
+  const void* raw;               // [rows, 32 nb] float32 or bf16
+  const int32_t* off;
   const int32_t* sorted_pairs;   // gate_up: activation row of sorted row r is sorted_pairs[r] / topk
 };
 
@@ -217,12 +219,17 @@ enum class MxSc {
   kWord     // the same, 4 bytes a load (nb % 4 == 0)
 };
 
-template <bool GU, int MT, int PD, MxSc SM, typename AT>
+// XT: element type of the rows that the kernel quantises itself, or void for
+// rows and passes that k_mx_prepare made.
+template <bool GU, int MT, int PD, MxSc SM, typename XT, typename AT>
 __global__ void __launch_bounds__(kSmThreads, 2)
 k_mx_stream(const MxArgs a, float* __restrict__ out0, AT* __restrict__ out1) {
+  constexpr bool kOwn = !std::is_void_v<XT>;
   __shared__ __attribute__((aligned(16))) uint8_t lds_x[kSmX];
   __shared__ __attribute__((aligned(16))) uint8_t lds_sc[kSmWaves][kSmSc];
   __shared__ uint32_t lds_row[32 * MT];
+  __shared__ MxItem lds_item[2];
+  __shared__ int lds_wave[kSmWaves];
   const int tid = threadIdx.x, lane = tid % kWave, half = lane / 32, col = lane % 32;
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int R = a.R, I = R / 2, nb = a.nb, S = (nb + kStB - 1) / kStB, SP = (S + PD - 1) / PD * PD;
@@ -235,34 +242,75 @@ k_mx_stream(const MxArgs a, float* __restrict__ out0, AT* __restrict__ out1) {
   // runs to the other lanes. A run begins with its pass's activation rows, which
   // take about the time of four tiles: the cut makes up for a run being several.
   const int lane_id = blockIdx.x % kXcds * (kSmBlocks / kXcds) + blockIdx.x / kXcds, nt = a.ntiles;
-  const int full = a.items[0].e / kSmBlocks, rest = a.items[0].e % kSmBlocks, others = kSmBlocks - rest;
-  const int64_t even = ((int64_t)rest * nt + kSmBlocks - 1) / kSmBlocks;
-  const int cut = (int)min((int64_t)nt, max(even, ((int64_t)rest * (nt + 4) - 4 * others) / kSmBlocks));
-  int64_t u = 0, end = 0;
+  // kOwn: this thread's two experts' rows and first pass, as k_mx_prepare lists them
+  static_assert(kMaxExperts == 2 * kSmThreads);
+  int r_lo = 0, m_0 = 0, m_1 = 0, first = 0, passes;
+  if constexpr (kOwn) {
+    r_lo = a.off[min(2 * tid, a.E)];
+    const int mid = a.off[min(2 * tid + 1, a.E)];
+    m_0 = mid - r_lo;
+    m_1 = a.off[min(2 * tid + 2, a.E)] - mid;
+    int sum = cdiv(m_0, 32 * MT) + cdiv(m_1, 32 * MT);
+    first = -sum;
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+      const int o = __shfl_up(sum, d, kWave);
+      if (lane >= d) sum += o;
+    }
+    if (lane == kWave - 1) lds_wave[wave] = sum;
+    lds_barrier();
+    first += sum;
+    passes = 0;
+#pragma unroll
+    for (int i = 0; i < kSmWaves; ++i) {
+      if (i < wave) first += lds_wave[i];
+      passes += lds_wave[i];
+    }
+    passes = __builtin_amdgcn_readfirstlane(passes);
+  } else {
+    passes = a.items[0].e;
+  }
+  // pass idx into lds_item: by the thread that has its expert
+  auto find = [&](int idx, MxItem* out) __attribute__((always_inline)) {
+    const int n0 = cdiv(m_0, 32 * MT), n1 = cdiv(m_1, 32 * MT), i = idx - first;
+    if (i < 0 || i >= n0 + n1) return;
+    const bool second = i >= n0;
+    const int m = second ? m_1 : m_0, per = cdiv(m, second ? n1 : n0), r = (second ? i - n0 : i) * per;
+    *out = MxItem{2 * tid + second, (second ? r_lo + m_0 : r_lo) + r, max(0, min(per, m - r)), 0};
+  };
+
+  const int full = passes / kSmBlocks, rest = passes % kSmBlocks, others = kSmBlocks - rest;
+  const int even = (rest * nt + kSmBlocks - 1) / kSmBlocks;   // nt < 2^20
+  const int cut = min(nt, max(even, (rest * (nt + 4) - 4 * others) / kSmBlocks));
+  int u = 0, end = 0;
   if (lane_id >= rest) {
     const int64_t tiles = (int64_t)rest * (nt - cut);
-    u = tiles * (lane_id - rest) / others;
-    end = tiles * (lane_id - rest + 1) / others;
+    u = (int)(tiles * (lane_id - rest) / others);
+    end = (int)(tiles * (lane_id - rest + 1) / others);
   }
+  struct Run {
+    int idx, t0, tend;   // tiles t0 .. tend - 1 of a pass; idx < 0: no more
+  };
+  auto next_run = [&](int seg) __attribute__((always_inline)) -> Run {
+    if (seg < full) return {seg * kSmBlocks + lane_id, 0, nt};
+    if (lane_id < rest) return {seg == full ? full * kSmBlocks + lane_id : -1, 0, cut};
+    if (u >= end) return {-1, 0, 0};
+    const int i = u / (nt - cut), t0 = cut + (u - i * (nt - cut)), tend = min(nt, t0 + (end - u));
+    u += tend - t0;
+    return {full * kSmBlocks + i, t0, tend};
+  };
 
-  for (int seg = 0;; ++seg) {
-    int idx, t0 = 0, tend = nt;
-    if (seg < full) {
-      idx = seg * kSmBlocks + lane_id;
-    } else if (lane_id < rest) {
-      if (seg > full) break;
-      idx = full * kSmBlocks + lane_id;
-      tend = cut;
-    } else {
-      if (u >= end) break;
-      const int64_t i = u / (nt - cut);
-      idx = full * kSmBlocks + (int)i;
-      t0 = cut + (int)(u - i * (nt - cut));
-      tend = (int)min((int64_t)nt, t0 + (end - u));
-      u += tend - t0;
-    }
-    const MxItem it = a.items[1 + idx];
-    const int e = it.e, r0 = it.r0, m = it.m;
+  Run next = next_run(0);
+  if constexpr (kOwn) {
+    find(next.idx, &lds_item[0]);
+    lds_barrier();
+  }
+  for (int seg = 0; next.idx >= 0; ++seg) {
+    const int idx = next.idx, t0 = next.t0, tend = next.tend;
+    next = next_run(seg + 1);
+    const MxItem it = kOwn ? lds_item[seg & 1] : a.items[1 + idx];
+    const int e = __builtin_amdgcn_readfirstlane(it.e), r0 = __builtin_amdgcn_readfirstlane(it.r0),
+              m = __builtin_amdgcn_readfirstlane(it.m);
     const uint8_t* wq = a.wq + (size_t)e * wq_n;
     const uint8_t* ws = a.ws + (size_t)e * ws_n;
     // offsets of the lane's row of tile 0; tstep rows further on for each tile
@@ -315,15 +363,65 @@ k_mx_stream(const MxArgs a, float* __restrict__ out0, AT* __restrict__ out1) {
     const int lsc = col * (SM == MxSc::kRun ? nb : kSmGroup) + 4 * half;
 
     int t = t0 + wave;
+    if constexpr (kOwn) {
+      // Rows quantised by the workgroup, eight values a thread and kAhead times
+      // at once. The first ones' loads go out between the weights' stages 1 and 2
+      // and the stages from 4 on only behind them: with all of them first, the
+      // rows arrived after 13 us of weights (128 tokens: 48.5 us; so 47.0).
+      // Blocks behind a row: zero codes, scale 1.
+      constexpr int kAhead = sizeof(XT) == 4 ? 4 : 8, kFirst = 2, kThen = PD < 4 ? PD : 4;
+      const XT* x = static_cast<const XT*>(a.raw);
+      const int per = 4 * kStB * S, n = m * per;   // a multiple of 4: a block's four lanes are all in or all out
+      decltype(mx_raw8(x)) v[kAhead];
+      auto load_x = [&](int p0) __attribute__((always_inline)) {
+        int row[kAhead];
 #pragma unroll
-    for (int d = 0; d < PD; ++d) load_w(t, d, d);
-    load_sc(t, 0);
+        for (int i = 0; i < kAhead; ++i) {
+          row[i] = r0 + min(p0 + i * kSmThreads, n - 1) / per;
+          if constexpr (GU) row[i] = a.sorted_pairs[row[i]];
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const int p = min(p0 + i * kSmThreads, n - 1), g = min(p % per, 4 * nb - 1);
+          v[i] = mx_raw8(x + (size_t)(GU ? row[i] / a.topk : row[i]) * (nb * kMxBlock) + 8 * g);
+        }
+      };
+#pragma unroll
+      for (int d = 0; d < kFirst; ++d) load_w(t, d, d);
+      load_sc(t, 0);
+      load_x(tid);
+#pragma unroll
+      for (int d = kFirst; d < kThen; ++d) load_w(t, d, d);
+      lds_barrier();   // no wave still reads the last pass's
+      find(next.idx, &lds_item[(seg + 1) & 1]);
+      for (int p0 = tid; p0 < n; p0 += kAhead * kSmThreads) {
+        if (p0 != tid) load_x(p0);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const int p = p0 + i * kSmThreads, row = p / per, g = p - row * per;
+          const bool in = g < 4 * nb;
+          float f[8];
+          mx_floats(v[i], f);
+          int sc;
+          const uint32_t c = mx_quant8(f, sc);
+          if (p < n) {
+            uint8_t* o = &lds_x[row * row_bytes];
+            *reinterpret_cast<uint32_t*>(o + 4 * g) = in ? c : 0u;
+            if ((g & 3) == 0) o[xsc + g / 4] = (uint8_t)(in ? sc : 127);
+          }
+        }
+      }
+#pragma unroll
+      for (int d = kThen; d < PD; ++d) load_w(t, d, d);
+    } else {
+#pragma unroll
+      for (int d = 0; d < PD; ++d) load_w(t, d, d);
+      load_sc(t, 0);
 
-    // the pass's activation rows
-    lds_barrier();   // no wave still reads the last pass's
-    if (tid < m) lds_row[tid] = (uint32_t)(GU ? a.sorted_pairs[r0 + tid] / a.topk : r0 + tid) * (uint32_t)row_bytes;
-    lds_barrier();
-    {
+      // the pass's activation rows
+      lds_barrier();   // no wave still reads the last pass's
+      if (tid < m) lds_row[tid] = (uint32_t)(GU ? a.sorted_pairs[r0 + tid] / a.topk : r0 + tid) * (uint32_t)row_bytes;
+      lds_barrier();
       const int n = m * pieces;
       const mx_rsrc x = mx_buffer(a.x, a.x_n);
       for (int p0 = wave * kWave; p0 < n; p0 += kSmThreads) {
@@ -631,7 +729,7 @@ k_mx_combine(const float* __restrict__ y, int H, int k, const float* __restrict_
 // How a product of rows of K is run: the passes' rows and the kernel
 struct MxPlan {
   int nb, nbp, row_bytes, mt;
-  bool stream;
+  bool stream, own;   // own: the stream kernel finds the passes and quantises the rows itself
   MxPlan(int K, int64_t P, int E) {
     nb = K / kMxBlock;
     nbp = cdiv(nb, kStB) * kStB;
@@ -642,6 +740,7 @@ struct MxPlan {
     const int fit = kSmX / (32 * row_bytes);
     stream = fit >= 1 && (nb <= kSmGroup || nb % 4 == 0);
     mt = stream ? (want <= fit ? want : fit >= 2 ? 2 : 1) : kRgMt;
+    own = stream && mt == 1 && nb <= kSmGroup;
   }
   // every non-empty expert has at most one pass that is not full
   int64_t passes(int64_t P, int E) const { return P / (32 * mt) + (P < E ? P : E); }
@@ -650,6 +749,8 @@ struct MxPlan {
 MxWorkspace::MxWorkspace(int64_t rows, int K, int64_t P, int E) {
   const auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   const MxPlan plan(K, P, E);
+  items = total = 0;
+  if (plan.own) return;
   items = up((size_t)rows * plan.row_bytes + 16);   // reads of a row's scales run up to 8 bytes past it
   total = items + up((size_t)(1 + plan.passes(P, E)) * sizeof(MxItem));
 }
@@ -663,31 +764,36 @@ static hipError_t mx_grouped(const XT* x, int64_t rows, int K, int64_t P, const 
   const int64_t n8 = rows * plan.nbp * 4, qgrid = 1 + (n8 + kPrThreads - 1) / kPrThreads;
   const int ntiles = R / 32;
   const int64_t rgrid = plan.passes(P, E) * cdiv(ntiles, kRgWaves);
+#define I8H_MX(M, D, S, X) k_mx_stream<GU, M, D, MxSc::S, X><<<kSmBlocks, kSmThreads, 0, st>>>(a, out0, out1)
+  if (plan.own) {
+    const MxArgs a = {nullptr, codes, scales, 0, plan.row_bytes, E, R, plan.nb, topk, ntiles, nullptr, x, expert_off,
+                      sorted_pairs};
+    // Depth of the prefetch: what the registers leave, and for short rows no more
+    // than a tile's stages, since those past the last are products of zeros
+    if (plan.nb <= 3 * kStB) I8H_MX(1, 3, kRun, XT);
+    else if (plan.nb <= 4 * kStB) I8H_MX(1, 4, kRun, XT);
+    else I8H_MX(1, 8, kRun, XT);
+    return hipGetLastError();
+  }
   MxItem* items = reinterpret_cast<MxItem*>(ws + lay.items);
   k_mx_prepare<<<(unsigned)qgrid, kPrThreads, 0, st>>>(x, n8, plan.nb, plan.nbp, plan.row_bytes, ws, expert_off, E,
                                                        32 * plan.mt, items);
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   const MxArgs a = {ws, codes, scales, (uint32_t)(rows * plan.row_bytes + 16), plan.row_bytes, E, R, plan.nb, topk,
-                    ntiles, items, sorted_pairs};
-#define I8H_MX(M, D, S) k_mx_stream<GU, M, D, MxSc::S><<<kSmBlocks, kSmThreads, 0, st>>>(a, out0, out1)
+                    ntiles, items, nullptr, nullptr, sorted_pairs};
   if (!plan.stream) {
     k_mx_ring<GU><<<(unsigned)rgrid, kRgThreads, 0, st>>>(a, out0, out1);
   } else if (plan.nb <= kSmGroup) {
-    // Depth of the prefetch: what the registers leave, and for short rows no more
-    // than a tile's stages, since those past the last are products of zeros
-    if (plan.mt == 1 && plan.nb <= 3 * kStB) I8H_MX(1, 3, kRun);
-    else if (plan.mt == 1 && plan.nb <= 4 * kStB) I8H_MX(1, 4, kRun);
-    else if (plan.mt == 1) I8H_MX(1, 8, kRun);
-    else if (plan.mt == 2) I8H_MX(2, 4, kRun);
-    else if (plan.nb <= 3 * kStB) I8H_MX(4, 3, kRun);   // K = 768, 2048 tokens: 84 us, two deep 87; K = 2048: 85, 81
-    else I8H_MX(4, 2, kRun);
+    if (plan.mt == 2) I8H_MX(2, 4, kRun, void);
+    else if (plan.nb <= 3 * kStB) I8H_MX(4, 3, kRun, void);   // K = 768, 2048 tokens: 84 us, two deep 87; K = 2048: 85, 81
+    else I8H_MX(4, 2, kRun, void);
   } else if (plan.nb % 16 == 0) {
-    if (plan.mt == 1) I8H_MX(1, 8, kPiece);
-    else I8H_MX(2, 2, kPiece);
+    if (plan.mt == 1) I8H_MX(1, 8, kPiece, void);
+    else I8H_MX(2, 2, kPiece, void);
   } else {
-    if (plan.mt == 1) I8H_MX(1, 8, kWord);
-    else I8H_MX(2, 2, kWord);
+    if (plan.mt == 1) I8H_MX(1, 8, kWord, void);
+    else I8H_MX(2, 2, kWord, void);
   }
 #undef I8H_MX
   return hipGetLastError();

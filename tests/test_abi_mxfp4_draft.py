@@ -57,11 +57,13 @@ def test_quantiser_validation(L, name):
 
 def test_gateup_validation(L):
     assert L.moe_gateup_mxfp4_workspace_size(8, 256, 4, 2) == 0        # one launch, no workspace
-    need = L.moe_gateup_mxfp4_workspace_size(9, 256, 4, 2)
-    assert need > 9 * 256 * 17 // 32 and need % 256 == 0      # the quantised rows and a list
-    assert L.moe_gateup_mxfp4_workspace_size(0, 256, 4, 2) == 0 and L.moe_gateup_mxfp4_workspace_size(9, 100, 4, 2) == 0
+    assert L.moe_gateup_mxfp4_workspace_size(32, 256, 4, 2) == 0
+    need = L.moe_gateup_mxfp4_workspace_size(99, 256, 4, 2)
+    assert need > 99 * 256 * 17 // 32 and need % 256 == 0      # the quantised rows and a list
+    assert L.moe_gateup_mxfp4_workspace_size(0, 256, 4, 2) == 0
+    assert L.moe_gateup_mxfp4_workspace_size(99, 100, 4, 2) == 0
 
-    def call(x=A, T=9, K=256, c=A, s=A, E=4, N=128, k=2, off=A, sp=A, gu=A, act=A, t=0, ws=A, wsb=need):
+    def call(x=A, T=99, K=256, c=A, s=A, E=4, N=128, k=2, off=A, sp=A, gu=A, act=A, t=0, ws=A, wsb=need):
         return L.moe_gateup_mxfp4_grouped(x, T, K, c, s, E, N, k, off, sp, gu, act, t, ws, wsb, None)
     for bad in (dict(T=-1), dict(K=0), dict(K=96), dict(E=0), dict(N=0), dict(N=127), dict(k=0), dict(t=2),
                 dict(x=None), dict(c=None), dict(s=None), dict(off=None), dict(sp=None), dict(x=EIGHT), dict(c=EIGHT),
@@ -75,11 +77,14 @@ def test_gateup_validation(L):
 
 def test_down_validation(L):
     assert L.moe_down_mxfp4_workspace_size(8, 96, 4, 64, 2) == 0
-    need = L.moe_down_mxfp4_workspace_size(9, 96, 4, 64, 2)
-    assert need > 18 * 96 * 17 // 32 + 18 * 64 * 4 and need % 256 == 0      # quantised rows, y and a list
-    assert L.moe_down_mxfp4_workspace_size(0, 96, 4, 64, 2) == 0 and L.moe_down_mxfp4_workspace_size(9, 100, 4, 64, 2) == 0
+    small = L.moe_down_mxfp4_workspace_size(9, 96, 4, 64, 2)
+    assert small >= 18 * 64 * 4 and small % 256 == 0          # y
+    need = L.moe_down_mxfp4_workspace_size(99, 96, 4, 64, 2)
+    assert need > 198 * 96 * 17 // 32 + 198 * 64 * 4 and need % 256 == 0      # quantised rows, y and a list
+    assert L.moe_down_mxfp4_workspace_size(0, 96, 4, 64, 2) == 0
+    assert L.moe_down_mxfp4_workspace_size(99, 100, 4, 64, 2) == 0
 
-    def call(a=A, t=0, T=9, I=96, c=A, s=A, E=4, H=64, k=2, ids=A, w=A, off=A, pos=A, out=A, ws=A, wsb=need):
+    def call(a=A, t=0, T=99, I=96, c=A, s=A, E=4, H=64, k=2, ids=A, w=A, off=A, pos=A, out=A, ws=A, wsb=need):
         return L.moe_down_mxfp4_combine(a, t, T, I, c, s, E, H, k, ids, w, off, pos, out, ws, wsb, None)
     for bad in (dict(T=-1), dict(I=0), dict(I=48), dict(E=0), dict(H=0), dict(H=36), dict(k=0), dict(t=2),
                 dict(a=None), dict(c=None), dict(s=None), dict(ids=None), dict(w=None), dict(off=None), dict(pos=None),

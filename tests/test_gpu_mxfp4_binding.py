@@ -9,7 +9,7 @@ import int8_hadamard_domain_amd as i8h
 
 pytestmark = pytest.mark.gpu
 
-T, K, E, N, H, k = 9, 256, 8, 128, 64, 2
+T, K, E, N, H, k = 99, 256, 8, 128, 64, 2
 
 
 def u8(*s):
