@@ -320,11 +320,13 @@ k_draft_pick(const DraftArgs a, const PT* __restrict__ p, const PT* __restrict__
   if (tid == 0) accepted[b] = n;
 }
 
-// Groups of four entries a thread takes: chunks of 1024 entries while they do
-// not make more workgroups than run at once (8 a CU; one sequence of 2^18
-// entries then fills the chip), of 4096 beyond, where each workgroup's search
-// for its row would cost more than the parallelism gives.
-int draft_groups(int B, int V) { return (int64_t)B * ((V + 1023) / 1024) <= 2048 ? 1 : 4; }
+// Groups of four entries a thread takes: chunks of 1024 entries, so that one
+// sequence of 2^18 entries fills the chip, while they make up to four times the
+// workgroups that run at once; chunks of 4096 beyond, where each workgroup's
+// search for its row costs more than the parallelism gives. Both, of 1024 and of
+// 4096 entries: 1 sequence of 2^18 7.4 and 11.9 us, 32 of 2^17 15.4 and 17.2, 64
+// (8192 workgroups) 23.4 and 23.3, 128 34.4 and 27.5, 256 58 and 40.
+int draft_groups(int B, int V) { return (int64_t)B * ((V + 1023) / 1024) <= 8192 ? 1 : 4; }
 
 template <typename PT>
 hipError_t draft(const DraftArgs& a, const void* pv, const void* qv, int B, void* ws, int32_t* tokens,

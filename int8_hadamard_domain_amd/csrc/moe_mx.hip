@@ -734,9 +734,14 @@ struct MxPlan {
     nb = K / kMxBlock;
     nbp = cdiv(nb, kStB) * kStB;
     row_bytes = (cdiv(17 * nbp, 16) | 1) * 16;   // an odd number of 16-byte pieces: 16 rows meet all LDS banks
-    // rows per pass by the average expert: 32 while experts hold a dozen pairs
-    // (a verify batch), up to 128 for many, as far as the rows fit LDS
-    const int want = P <= 16 * (int64_t)E ? 1 : P <= 40 * (int64_t)E ? 2 : 4;
+    // Rows per pass: 32, quantised by the kernel itself (no second launch), while
+    // an expert has eight on average; up to 128, as far as they fit LDS, for more.
+    // Both at K = 2048, N = 1536, 32 and 128 rows: 128 experts, 4 pairs each 40.5
+    // and 41.0 us, 8 each 46.9 and 47.5, 16 each 57.6 and 50.7, 32 each 73 and 55;
+    // 8 experts, 8 pairs each 13.5 and 11.9 (the launch not counted), 16 each 18.5
+    // and 12.4. 64 rows are within 1 us of 128 up to 20 pairs an expert and 7 us
+    // behind at 64.
+    const int want = P <= 8 * (int64_t)E ? 1 : 4;
     const int fit = kSmX / (32 * row_bytes);
     stream = fit >= 1 && (nb <= kSmGroup || nb % 4 == 0);
     mt = stream ? (want <= fit ? want : fit >= 2 ? 2 : 1) : kRgMt;
@@ -785,8 +790,7 @@ static hipError_t mx_grouped(const XT* x, int64_t rows, int K, int64_t P, const 
   if (!plan.stream) {
     k_mx_ring<GU><<<(unsigned)rgrid, kRgThreads, 0, st>>>(a, out0, out1);
   } else if (plan.nb <= kSmGroup) {
-    if (plan.mt == 2) I8H_MX(2, 4, kRun, void);
-    else if (plan.nb <= 3 * kStB) I8H_MX(4, 3, kRun, void);   // K = 768, 2048 tokens: 84 us, two deep 87; K = 2048: 85, 81
+    if (plan.nb <= 3 * kStB) I8H_MX(4, 3, kRun, void);   // K = 768, 2048 tokens: 84 us, two deep 87; K = 2048: 85, 81
     else I8H_MX(4, 2, kRun, void);
   } else if (plan.nb % 16 == 0) {
     if (plan.mt == 1) I8H_MX(1, 8, kPiece, void);

@@ -169,10 +169,10 @@ k_down_mx_few(const XT* __restrict__ act, int nb, const uint8_t* __restrict__ wq
   __shared__ __attribute__((aligned(16))) uint8_t rows[kFdWaves][kFdRow];
   __shared__ float part[kMaxTopk][16];
   const int tid = threadIdx.x, lane = tid % kWave, g = lane / 16, c = lane % 16, wave = tid / kWave;
-  const int t = blockIdx.y, h0 = 16 * blockIdx.x;
+  const int t = blockIdx.y, h0 = 16 * blockIdx.x, waves = blockDim.x / kWave;
   const int steps = (nb + 3) / 4;      // the last one may hold fewer than four blocks
   uint8_t* row = rows[wave];
-  for (int j = wave; j < k; j += kFdWaves) {
+  for (int j = wave; j < k; j += waves) {
     const int e = ids[t * k + j];
     const int64_t r = pos[t * k + j];
     const size_t n = (size_t)e * H + h0 + c;
@@ -229,11 +229,15 @@ k_down_mx_few(const XT* __restrict__ act, int nb, const uint8_t* __restrict__ wq
 
 }  // namespace
 
-// Up to 8 tokens and 64 pairs, the tokens' rows within LDS
+// Up to 8 tokens and 32 pairs, the tokens' rows within LDS. Both ways, this form
+// and k_mx_stream, 128 experts, top 8: gate_up (K = 2048, N = 1536) one token 8.3
+// and 11.0 us, 2 12.9 and 14.5, 4 17.8 and 21.1, 8 26.6 and 25.3; down (I = 768,
+// H = 2048) 6.6 and 10.5, 7.3 and 12.7, 12.7 and 15.8, 22.3 and 18.9.
+static bool mx_few(int T, int topk) { return T <= 8 && T * topk <= 32; }
 bool mx_few_gateup(int T, int K, int topk) {
-  return T <= 8 && T * topk <= 64 && T * few_row_bytes(K / kMxBlock) <= kFgLds;
+  return mx_few(T, topk) && T * few_row_bytes(K / kMxBlock) <= kFgLds;
 }
-bool mx_few_down(int T, int I, int topk) { return T <= 8 && T * topk <= 64 && I <= kFdMaxI; }
+bool mx_few_down(int T, int I, int topk) { return mx_few(T, topk) && I <= kFdMaxI; }
 
 hipError_t launch_gateup_mxfp4_few(const uint16_t* x, int T, int K, const uint8_t* codes, const uint8_t* scales, int E,
                                    int N, int k, const int32_t* expert_off, const int32_t* sorted_pairs, float* gu,
@@ -254,12 +258,13 @@ hipError_t launch_down_mxfp4_few(const void* act, bool act_bf16, int T, int I, c
                                  const uint8_t* scales, int H, int k, const int32_t* ids, const float* tw,
                                  const int32_t* pos, float* out, hipStream_t st) {
   const dim3 grid(H / 16, T);
+  const int threads = kWave * (k < kFdWaves ? k : kFdWaves);
   const int nb = I / kMxBlock;
   if (act_bf16)
-    k_down_mx_few<<<grid, kFdThreads, 0, st>>>(static_cast<const uint16_t*>(act), nb, codes, scales, H, k, ids, tw, pos,
+    k_down_mx_few<<<grid, threads, 0, st>>>(static_cast<const uint16_t*>(act), nb, codes, scales, H, k, ids, tw, pos,
                                                out);
   else
-    k_down_mx_few<<<grid, kFdThreads, 0, st>>>(static_cast<const float*>(act), nb, codes, scales, H, k, ids, tw, pos,
+    k_down_mx_few<<<grid, threads, 0, st>>>(static_cast<const float*>(act), nb, codes, scales, H, k, ids, tw, pos,
                                                out);
   return hipGetLastError();
 }

@@ -32,8 +32,9 @@ def test_gate_up_long_rows(gpu_available, T, K, E, topk, N):
     _check_gateup(T, K, E, topk, N, seed=T + K + E + N)
 
 
-# few tokens / many: T = 8, 9 and 64, 65.. pairs; 16, 17 and 40, 41 pairs an expert
-BORDERS = [(8, 8, 8), (8, 9, 16), (9, 1, 4), (4, 16, 16), (2, 32, 32), (3, 22, 32), (32, 2, 4), (33, 2, 4), (34, 2, 4),
+# few tokens / many: T = 8, 9 and 32, 33.. pairs; passes of 32 and of 128 rows: 8 and more pairs an expert
+BORDERS = [(8, 4, 8), (8, 5, 16), (8, 8, 8), (8, 9, 16), (9, 1, 4), (4, 8, 16), (3, 11, 32), (1, 32, 32), (2, 32, 32),
+           (3, 22, 32), (16, 2, 4), (17, 2, 4), (32, 2, 4), (33, 2, 4), (34, 2, 4),
            (80, 2, 4), (81, 2, 4)]
 
 
