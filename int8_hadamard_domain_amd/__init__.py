@@ -517,9 +517,10 @@ def _type(t, name):
 
 def _mx_weights(codes, scales, K, dev):
     """Check MXFP4 weights of K columns: codes [E, R, K/2], scales [E, R, K/32]. Returns (E, R)."""
-    _dev(codes, "codes", torch.uint8, 3, device=dev)
+    if not isinstance(codes, torch.Tensor) or codes.dim() != 3:
+        _dev(codes, "codes", torch.uint8, 3, device=dev)
     E, R, _ = codes.shape
-    _dev(codes, "codes", torch.uint8, shape=(E, R, K // 2))
+    _dev(codes, "codes", torch.uint8, shape=(E, R, K // 2), device=dev)
     _dev(scales, "scales", torch.uint8, shape=(E, R, K // 32), device=dev)
     return E, R
 
