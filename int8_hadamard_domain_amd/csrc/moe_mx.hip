@@ -210,7 +210,10 @@ constexpr int kSmWaves = kSmThreads / kWave;
 constexpr int kSmBlocks = 256;                    // one workgroup a CU
 constexpr int kSmX = 128 * 1104;                  // LDS for activation rows: 128 of K = 2048
 constexpr int kSmGroup = 64;                      // blocks of a row whose scales a wave holds at a time
-constexpr int kSmSc = 32 * kSmGroup + 16;         // LDS for a wave's scales: a tile's 32 rows
+// LDS for a wave's scales: a tile's 32 rows, 16 bytes unused behind every 64, or
+// the rows of K = 2048 would all begin in the same four banks
+constexpr int kSmSc = 32 * kSmGroup / 4 * 5 + 16;
+__device__ __forceinline__ int mx_sc_at(int o) { return o + o / 64 * 16; }
 
 // how a wave copies its tile's scales to LDS
 enum class MxSc {
@@ -358,7 +361,7 @@ k_mx_stream(const MxArgs a, float* __restrict__ out0, AT* __restrict__ out1) {
     };
     auto store_sc = [&]() __attribute__((always_inline)) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) *reinterpret_cast<u32x4*>(&lds_sc[wave][16 * (lane + i * kWave)]) = sr[i];
+      for (int i = 0; i < 2; ++i) *reinterpret_cast<u32x4*>(&lds_sc[wave][mx_sc_at(16 * (lane + i * kWave))]) = sr[i];
     };
     const int lsc = col * (SM == MxSc::kRun ? nb : kSmGroup) + 4 * half;
 
@@ -455,10 +458,11 @@ k_mx_stream(const MxArgs a, float* __restrict__ out0, AT* __restrict__ out1) {
         uint32_t v;
         if constexpr (SM == MxSc::kRun) {
           const int o = lsc + kStB * s;   // the four bytes may start anywhere
-          const uint32_t* p = reinterpret_cast<const uint32_t*>(&lds_sc[wave][o & ~3]);
-          v = __builtin_amdgcn_alignbyte(p[1], p[0], o & 3);
+          const uint32_t lo = *reinterpret_cast<const uint32_t*>(&lds_sc[wave][mx_sc_at(o & ~3)]);
+          const uint32_t hi = *reinterpret_cast<const uint32_t*>(&lds_sc[wave][mx_sc_at((o & ~3) + 4)]);
+          v = __builtin_amdgcn_alignbyte(hi, lo, o & 3);
         } else {
-          v = *reinterpret_cast<const uint32_t*>(&lds_sc[wave][lsc + kStB * (s % kStB)]);
+          v = *reinterpret_cast<const uint32_t*>(&lds_sc[wave][mx_sc_at(lsc + kStB * (s % kStB))]);
         }
         return mx_mask_scales(v, nb - kStB * s - 4 * half);
       };
