@@ -240,10 +240,20 @@ k_mx_stream(const MxArgs a, float* __restrict__ out0, AT* __restrict__ out1) {
   const uint32_t wq_n = (uint32_t)R * (16 * nb), ws_n = (uint32_t)R * nb;
 
   // The deal, lane = workgroup, neighbouring lanes on one XCD: whole passes while
-  // there are as many as lanes; then of each pass left (fewer than lanes) the
-  // first `cut` tiles to a lane of its own, and the tiles behind them in even
-  // runs to the other lanes. A run begins with its pass's activation rows, which
-  // take about the time of four tiles: the cut makes up for a run being several.
+  // there are as many as lanes; then of each of the `rest` passes left the first
+  // `cut` tiles to a lane of its own, and the tiles behind them to the `others`.
+  // Every run begins with its pass's activation rows, so runs are few:
+  //   as many others as passes or more: `helpers` a pass, equal runs;
+  //   fewer: even runs over all of them, a cut that makes up for a run being
+  //     several (its rows taken as four tiles);
+  //   fewer, gate_up, clearly (rest : others above 9 : 8): a helper takes the
+  //     whole remainder of its passes, a multiple of 8 tiles, as eight waves take
+  //     a tile each in one round; often there is no cut at all.
+  // Measured, even runs always and this deal: gate_up K = 2048, 128 tokens (120
+  // passes) 48.3 and 46.2 us, 1024 (146) 63.1 and 60.3, 2048 (202) 80 and 75, 640
+  // (132, helpers' whole remainders) 56.2 and 58.8; 18 passes 28.5 and 20.8; down
+  // I = 768, 1999 tokens, the whole remainders 88 and 96, for its stores of y keep
+  // all CUs busy to the end.
   const int lane_id = blockIdx.x % kXcds * (kSmBlocks / kXcds) + blockIdx.x / kXcds, nt = a.ntiles;
   // kOwn: this thread's two experts' rows and first pass, as k_mx_prepare lists them
   static_assert(kMaxExperts == 2 * kSmThreads);
@@ -283,24 +293,48 @@ k_mx_stream(const MxArgs a, float* __restrict__ out0, AT* __restrict__ out1) {
   };
 
   const int full = passes / kSmBlocks, rest = passes % kSmBlocks, others = kSmBlocks - rest;
-  const int even = (rest * nt + kSmBlocks - 1) / kSmBlocks;   // nt < 2^20
-  const int cut = min(nt, max(even, (rest * (nt + 4) - 4 * others) / kSmBlocks));
-  int u = 0, end = 0;
-  if (lane_id >= rest) {
-    const int64_t tiles = (int64_t)rest * (nt - cut);
-    u = (int)(tiles * (lane_id - rest) / others);
-    end = (int)(tiles * (lane_id - rest + 1) / others);
+  const int helpers = rest > 0 ? others / rest : 0;
+  int cut = nt, u = 0, end = 0;   // even runs: u .. end - 1 of the tiles behind the cuts
+  bool even = false;
+  if (helpers > 0) {
+    cut = cdiv(nt, helpers + 1);
+  } else if (!GU || 8 * rest < 9 * others) {
+    even = true;
+    cut = min(nt, max(cdiv(rest * nt, kSmBlocks), (rest * (nt + 4) - 4 * others) / kSmBlocks));
+    if (lane_id >= rest) {
+      const int64_t tiles = (int64_t)rest * (nt - cut);
+      u = (int)(tiles * (lane_id - rest) / others);
+      end = (int)(tiles * (lane_id - rest + 1) / others);
+    }
+  } else {
+    // a round, a tile a wave, takes S stages, a pass's rows about six: the
+    // rounds r at which both are alike, rounded either way, or all
+    constexpr int kStart = 6;
+    const int rounds = cdiv(nt, kSmWaves), shared = cdiv(rest, others);
+    auto cost = [&](int r) { return max(r * S + kStart, r < rounds ? shared * ((rounds - r) * S + kStart) : 0); };
+    const int r = (int)(((int64_t)shared * rounds * S + (shared - 1) * kStart) / ((shared + 1) * S));
+    if (min(cost(r), cost(r + 1)) < cost(rounds)) cut = min(nt, (cost(r) < cost(r + 1) ? r : r + 1) * kSmWaves);
   }
   struct Run {
     int idx, t0, tend;   // tiles t0 .. tend - 1 of a pass; idx < 0: no more
   };
   auto next_run = [&](int seg) __attribute__((always_inline)) -> Run {
     if (seg < full) return {seg * kSmBlocks + lane_id, 0, nt};
-    if (lane_id < rest) return {seg == full ? full * kSmBlocks + lane_id : -1, 0, cut};
-    if (u >= end) return {-1, 0, 0};
-    const int i = u / (nt - cut), t0 = cut + (u - i * (nt - cut)), tend = min(nt, t0 + (end - u));
-    u += tend - t0;
-    return {full * kSmBlocks + i, t0, tend};
+    seg -= full;
+    const int j = lane_id - rest;
+    if (j < 0) return {seg == 0 ? full * kSmBlocks + lane_id : -1, 0, cut};
+    if (helpers > 0) {
+      const int i = j / helpers, per = cdiv(nt - cut, helpers), t0 = cut + (j - i * helpers) * per;
+      return {seg == 0 && i < rest && t0 < nt ? full * kSmBlocks + i : -1, t0, min(nt, t0 + per)};
+    }
+    if (even) {
+      if (u >= end) return {-1, 0, 0};
+      const int i = u / (nt - cut), t0 = cut + (u - i * (nt - cut)), tend = min(nt, t0 + (end - u));
+      u += tend - t0;
+      return {full * kSmBlocks + i, t0, tend};
+    }
+    const int i = j * rest / others + seg;
+    return {cut < nt && i < (j + 1) * rest / others ? full * kSmBlocks + i : -1, cut, nt};
   };
 
   Run next = next_run(0);

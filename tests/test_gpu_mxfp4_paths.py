@@ -58,6 +58,48 @@ def test_down_long_rows(gpu_available, T, I, E, topk, H):
     _check_down(T, I, E, topk, H, seed=T + I + H, dtype=torch.float32)
 
 
+# Passes of up to 128 rows (one expert) against 256 workgroups: a helper or more a pass, even runs over the workgroups
+# left, whole remainders, no helper, none left, whole rounds and a few more.
+PASSES = [2, 50, 128, 129, 135, 137, 160, 200, 255, 256, 257, 300, 520]
+
+
+@pytest.mark.parametrize("N", [64, 704, 832])
+@pytest.mark.parametrize("passes", PASSES)
+def test_gate_up_deals(gpu_available, passes, N):
+    T = 128 * passes - 61
+    _check_gateup(T, 128, 1, 1, N, seed=passes + N, rows=np.unique(np.r_[np.arange(0, T, 61), T - 1]))
+
+
+@pytest.mark.parametrize("H", [32, 352, 416])
+@pytest.mark.parametrize("passes", PASSES)
+def test_down_deals(gpu_available, passes, H):
+    T = 128 * passes - 61
+    _check_down(T, 64, 1, 1, H, seed=passes + H, dtype=torch.bfloat16, tokens=np.unique(np.r_[np.arange(0, T, 61), T - 1]))
+
+
+@pytest.mark.parametrize("E,passes", [(16, 3), (128, 120), (200, 190), (256, 256), (300, 300), (700, 600)])
+def test_deals_of_small_passes(gpu_available, E, passes):
+    """Passes of a few rows (quantised by the product's own workgroups): one expert each."""
+    T, topk = passes, 1
+    rng = np.random.default_rng(passes)
+    ids = rng.choice(E, passes, replace=False).reshape(T, topk)
+    r = _routing_of(ids, E)
+    K, N, H = 384, 704, 416
+    x, a = _exact_values(rng, T, K), _exact_values(rng, T, 96)
+    codes, scales = _weights(rng, E, N, K, 2)
+    dc, ds = _weights(rng, E, H, 96, 2)
+    print(f"deals of small passes E={E} passes={passes}", flush=True)
+    gu, _ = i8h.moe_gateup_mxfp4_grouped(x.cuda(), u8(codes), u8(scales), topk, r["expert_off"], r["sorted_pairs"],
+                                         act=False)
+    out = i8h.moe_down_mxfp4_combine(a.cuda(), u8(dc), u8(ds), r)
+    off, order = r["expert_off"].cpu().numpy(), r["sorted_pairs"].cpu().numpy()
+    ref, mag = mxfp4.grouped(mxfp4.dequantize(*mxfp4.quantize(values(x)))[order], codes, scales, off)
+    assert mag.max() < 2.0 ** 24 * 0.25 * 2.0 ** -7 and np.array_equal(values(gu), ref)
+    y, mag = mxfp4.grouped(mxfp4.dequantize(*mxfp4.quantize(values(a))), dc, ds, off)
+    ref, m = mxfp4.combine(y, r["topk_w"].cpu().numpy(), r["pair_pos"].cpu().numpy())
+    assert np.all(np.abs(values(out) - ref) <= 2.0 ** -23 * m)
+
+
 # ------------------------------------------------------------------------------------------------------ routings
 
 def _routing_of(ids, E, seed=0):
