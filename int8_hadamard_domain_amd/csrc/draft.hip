@@ -6,7 +6,9 @@
 //   rest(0) + .. + rest(v) > u_next sum(rest).
 //
 // Only one row of p and q is read whole, so the step is a read of 8 V bytes a
-// sequence, bound by HBM for many sequences and by latency for one. The row is
+// sequence, bound by HBM for many sequences (64 of 2^17 entries: 67 MB in 23 us,
+// 19 of them k_draft_sums, whose read waits for the search for the row) and by
+// latency for one (2^18 entries: 7.6 us, two launches). The row is
 // cut into chunks, a workgroup each (k_draft_sums: the chunk's sum in float64,
 // fixed order, no atomics on floats), and one workgroup a sequence then finds
 // the chunk that the draw falls into and reads only that one again

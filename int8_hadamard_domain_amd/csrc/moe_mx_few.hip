@@ -12,6 +12,10 @@
 // the slots' sums meet in LDS to be merged in slot order: out comes straight
 // from one launch, with no y.
 //
+// Bound by latency more than by HBM (one token, 8 of 128 experts: gate_up 13.4 MB
+// in 8.3 us; down 6.7 MB in 6.6 us): a launch, then the chain offsets, weights,
+// products, sums. 7 tokens of 4 of 60 experts: 33 MB in 12.8 us, 2.6 TB/s.
+//
 // Both use v_mfma_scale_f32_16x16x128_f8f6f4: lane l holds block 4 j + l / 16
 // (of step j, K = 128) of weight row l % 16 (A) and of column l % 16 (B), and
 // results of rows 4 (l / 16) .. +3, column l % 16. An expert's pairs are the
@@ -24,7 +28,10 @@ namespace i8h {
 
 namespace {
 
-constexpr int kFewSteps = 16;        // steps of a chunk held in registers: K = 2048
+// Steps of a chunk held in registers: K = 2048. With all of a row's loads in
+// flight at once gate_up of one token takes 8.3 us; with the activation rows
+// loaded before them 9.4.
+constexpr int kFewSteps = 16;
 
 __device__ __forceinline__ f32x4 mx_mfma16(const u32x4 a, const u32x4 b, f32x4 c, uint32_t sa, uint32_t sb) {
   const i32x8 av = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};

@@ -14,7 +14,10 @@ namespace i8h {
 namespace {
 
 constexpr int kMxThreads = 256;
-constexpr int kMxGroups = 2;   // groups of eight values a thread takes
+// Groups of eight values a thread takes. Bound by HBM: 24576 x 2048 float32 to
+// codes in 43 us (228 MB, 5.3 TB/s; with one group a thread 52.5), back in 35 us
+// (6.5 TB/s); a large copy moves 5.1 TB/s.
+constexpr int kMxGroups = 2;
 
 template <typename XT>
 __global__ void __launch_bounds__(kMxThreads)
