@@ -57,8 +57,8 @@ int mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int T, int K, 
  * of act_type (bf16: each value rounded to nearest even from the float32
  * one) or NULL; both 16-B aligned. workspace: at least
  * moe_gateup_mxfp4_workspace_size(T, K, E, topk) bytes, 256-B aligned
- * (may be NULL when that size is 0: a few tokens take one launch that needs
- * none); what it holds after the call is unspecified. */
+ * (may be NULL when that size is 0: with few rows an expert the call is one
+ * launch that needs none); what it holds after the call is unspecified. */
 size_t moe_gateup_mxfp4_workspace_size(int T, int K, int E, int topk);
 int moe_gateup_mxfp4_grouped(const uint16_t* x, int T, int K, const uint8_t* codes, const uint8_t* scales,
                              int E, int N, int topk, const int32_t* expert_off, const int32_t* sorted_pairs,

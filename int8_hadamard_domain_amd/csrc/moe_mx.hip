@@ -33,11 +33,11 @@
 // Bounds, at 128 experts, top 8, K = 2048, N = 1536 (I = 768, H = 2048):
 //   128 tokens   the weights from HBM: gate_up 216 MB in 46 us, 4.7 TB/s (a large
 //                copy: 5.1), down 111 MB and the y round trip in 32 us.
-//   2048 tokens  gate_up 75 us, 70 of them k_mx_stream: 283 MB of HBM traffic
-//                (weights fetched 1.2 times) at 4.0 TB/s, matrix units a quarter
-//                busy, LDS too; the rest are each pass's start (rows to LDS, 5 to
-//                7 us), its last round of tiles and the epilogue. down 84 us: y,
-//                131 MB, written (k_mx_stream 53) and read again (k_mx_combine 22).
+//   2048 tokens  gate_up 75 us, 71 of them k_mx_stream: 255 MB of HBM traffic
+//                (weights fetched 1.04 times) at 3.6 TB/s, matrix units 30 % busy,
+//                LDS less; the rest are each pass's start (rows to LDS, 5 to 7 us),
+//                whole rounds of tiles and the epilogue. down 84 us: y, 131 MB,
+//                written (k_mx_stream 53) and read again (k_mx_combine 22).
 
 #include <type_traits>
 
