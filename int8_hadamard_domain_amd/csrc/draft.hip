@@ -267,7 +267,10 @@ k_draft_pick(const DraftArgs a, const PT* __restrict__ p, const PT* __restrict__
   int chunk = -1, last_chunk = -1;
   for (int c0 = 0;;) {
     int first, last;
-    block_find(ex + chunk_sum > target, chunk_sum > 0.0, found, first, last);
+    // only a chunk that holds something: ex is rounded in another order than the
+    // sums before it, so an empty chunk's may pass where theirs did not
+    const bool some = chunk_sum > 0.0;
+    block_find(some && ex + chunk_sum > target, some, found, first, last);
     if (last >= 0) last_chunk = c0 + last;
     if (first >= 0) {
       chunk = c0 + first;

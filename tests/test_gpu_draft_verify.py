@@ -218,3 +218,35 @@ def test_unaligned_rows_and_outputs(gpu_available):
             t, n = _gpu(pb, qb, x, length, u, un, tokens=tok[1:-1], accepted=acc[1:-1])
             assert np.array_equal(n, want[1]) and np.array_equal(t, want[0])
             assert (tok[0] == 9).all() and (tok[-1] == 9).all() and acc[0] == 9 and acc[-1] == 9
+
+
+@pytest.mark.parametrize("B,chunks,chunk", [(200, 40, 1024), (27, 300, 1024), (300, 40, 4096)])
+def test_empty_chunks_at_a_border(gpu_available, B, chunks, chunk):
+    """Rows of a few entries (as a top-k filter leaves them), the draw on the border before a run of empty chunks:
+    the token holds probability, and the target lies at one of its ends, off by the sums' rounding at most."""
+    V = chunks * chunk
+    print(f"draft_verify empty chunks B={B} V={V}", flush=True)
+    rng = np.random.default_rng(B + chunks)
+    p = np.zeros((B, 1, V), np.float32)
+
+    def put(b, c, value):       # 48 bits of it, as two entries of a chunk
+        hi = np.float32(value)
+        if float(hi) > value:
+            hi = np.nextafter(hi, np.float32(0))
+        lo = np.float32(value - float(hi))
+        p[b, 0, c * chunk + 5], p[b, 0, c * chunk + 77] = hi, lo
+        return float(hi) + float(lo)
+    for b in range(B):
+        total = 0.0
+        for c in np.sort(rng.choice(chunks - 12, int(rng.integers(3, 12)), replace=False)):
+            total += put(b, c, rng.random() * 2.0 ** -int(rng.integers(0, 30)))
+        put(b, chunks - 3, total)      # as much again behind the empty chunks: u_next = 0.5 is the border
+    un = np.full(B, 0.5, np.float32)
+    tokens, accepted = _gpu(torch.from_numpy(p), None, np.zeros((B, 0), np.int32), None, np.zeros((B, 0), np.float32), un)
+    assert not accepted.any()
+    for b in range(B):
+        row = p[b, 0].astype(np.longdouble)
+        run, t = np.cumsum(row), tokens[b, 0]
+        target, off = 0.5 * run[-1], V * 2.0 ** -50 * run[-1]
+        assert row[t] > 0, (b, t)
+        assert run[t] > target - off and run[t] - row[t] <= target + off, (b, t)
