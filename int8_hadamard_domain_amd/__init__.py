@@ -533,14 +533,15 @@ def _mx_out(t, name, shape, dtype, x):
 
 
 def _mx_shape(t, name, unit, per_row):
-    """(leading dimensions, last dimension, rows) of a matrix of whole blocks along its last dimension."""
+    """(leading dimensions, last dimension, blocks of 32) of a matrix of whole blocks along its last dimension. Its
+    rows lie one behind another, so the library takes it as so many rows of one block: its sizes are 32-bit."""
     shape = tuple(t.shape)
     if not shape or shape[-1] == 0 or shape[-1] % unit:
         raise ValueError(f"{name} must have a last dimension of whole blocks of {unit} (got {shape})")
-    rows = t.numel() // shape[-1]
-    if rows >= 1 << 31:
-        raise ValueError(f"{name} must have fewer than 2^31 rows (got {rows})")
-    return shape[:-1], shape[-1] * per_row, rows
+    blocks = t.numel() // unit
+    if blocks >= 1 << 31:
+        raise ValueError(f"{name} must have fewer than 2^31 blocks (got {blocks})")
+    return shape[:-1], shape[-1] * per_row, blocks
 
 
 def mxfp4_quantize(x, codes=None, scales=None):
@@ -549,10 +550,10 @@ def mxfp4_quantize(x, codes=None, scales=None):
     the low nibble) and an E8M0 scale per 32 values."""
     xt = _type(x, "x")
     _dev(x, "x", x.dtype)
-    lead, K, rows = _mx_shape(x, "x", 32, 1)
+    lead, K, blocks = _mx_shape(x, "x", 32, 1)
     codes = _mx_out(codes, "codes", lead + (K // 2,), torch.uint8, x)
     scales = _mx_out(scales, "scales", lead + (K // 32,), torch.uint8, x)
-    _call("mxfp4_quantize", x.device, x.data_ptr(), xt, rows, K, codes.data_ptr(), scales.data_ptr())
+    _call("mxfp4_quantize", x.device, x.data_ptr(), xt, blocks, 32, codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
@@ -560,14 +561,14 @@ def mxfp4_dequantize(codes, scales, dtype=torch.bfloat16, out=None):
     """The values of MXFP4 codes [..., K/2] and scales [..., K/32] (uint8) as
     [..., K] float32 or bfloat16 (dtype, or the dtype of a given out)."""
     _dev(codes, "codes", torch.uint8)
-    lead, K, rows = _mx_shape(codes, "codes", 16, 2)
+    lead, K, blocks = _mx_shape(codes, "codes", 16, 2)
     _dev(scales, "scales", torch.uint8, shape=lead + (K // 32,), device=codes.device)
     if out is not None:
         dtype = out.dtype if isinstance(out, torch.Tensor) else None
     if dtype not in TYPES:
         raise TypeError(f"dtype must be float32 or bfloat16 (got {dtype})")
     out = _mx_out(out, "out", lead + (K,), dtype, codes)
-    _call("mxfp4_dequantize", codes.device, codes.data_ptr(), scales.data_ptr(), rows, K, out.data_ptr(),
+    _call("mxfp4_dequantize", codes.device, codes.data_ptr(), scales.data_ptr(), blocks, 32, out.data_ptr(),
           TYPES[dtype])
     return out
 

@@ -157,3 +157,40 @@ def test_calls_run_on_their_tensors_device(monkeypatch):
     i8h._call("draft_verify", torch.device("cuda", 0), 7)
     i8h._call("draft_verify", torch.device("cuda", 3), 8)
     assert seen == [(0, (7, 1000)), (3, (8, 1003))] and current == [0]
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The library's calls with their arguments, from tensors that hold no memory."""
+    seen = []
+    monkeypatch.setattr(i8h, "_dev", lambda t, *a, **kw: t)
+    monkeypatch.setattr(i8h, "_call", lambda fn, device, *args: seen.append((fn, args)))
+    return seen
+
+
+def _meta(*shape, dtype=torch.bfloat16):
+    return torch.empty(shape, dtype=dtype, device="meta")
+
+
+@pytest.mark.parametrize("shape", [(32,), (5, 64), (2, 3, 64), ((1 << 31) - 32,), (1 << 31,), ((1 << 32) + 64,),
+                                   (3, (1 << 32) + 32), (1 << 30, 32), (2, 1 << 33)])
+def test_quantiser_takes_rows_of_any_length(calls, shape):
+    """The library's sizes are 32-bit integers: what it is told has to cover the tensor, rows of 2^31 values too."""
+    n = _meta(*shape).numel()
+    codes, scales = i8h.mxfp4_quantize(_meta(*shape))
+    assert codes.shape == shape[:-1] + (shape[-1] // 2,) and scales.shape == shape[:-1] + (shape[-1] // 32,)
+    assert i8h.mxfp4_dequantize(codes, scales).shape == shape
+    (q, (_, _, qt, qk, _, _)), (d, (_, _, dt, dk, _, _)) = calls
+    assert q == "mxfp4_quantize" and d == "mxfp4_dequantize"
+    for rows, K in ((qt, qk), (dt, dk)):
+        assert rows * K == n and rows < 1 << 31 and K < 1 << 31 and K % 32 == 0
+
+
+def test_quantiser_refuses_more_than_its_sizes_hold(calls):
+    for shape in ((1 << 36,), (1 << 31, 32), (7, 1 << 34)):
+        with pytest.raises(ValueError):
+            i8h.mxfp4_quantize(_meta(*shape))
+        with pytest.raises(ValueError):
+            i8h.mxfp4_dequantize(_meta(*shape[:-1], shape[-1] // 2, dtype=torch.uint8),
+                                 _meta(*shape[:-1], shape[-1] // 32, dtype=torch.uint8))
+    assert not calls

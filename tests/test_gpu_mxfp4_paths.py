@@ -348,3 +348,23 @@ def test_calls_at_once_on_two_streams(gpu_available, T):
     for i in range(2):
         for g in got[i]:
             assert all(torch.equal(a, b) for a, b in zip(g, want[i]))
+
+
+def test_quantiser_of_one_row_past_2_32_elements(gpu_available):
+    """A flat tensor: its last dimension does not fit 32 bits."""
+    n = (1 << 32) + 96
+    print("quantise a row past 2^32 elements", flush=True)
+    base = torch.randn(1 << 16, device="cuda").to(torch.bfloat16)
+    x = torch.empty(n, dtype=torch.bfloat16, device="cuda")
+    x[:1 << 32].view(-1, 1 << 16).copy_(base)
+    x[1 << 32:] = base[:96] * 4
+    c0, s0 = i8h.mxfp4_quantize(base)
+    codes, scales = i8h.mxfp4_quantize(x)
+    assert codes.shape == (n // 2,) and scales.shape == (n // 32,)
+    m = 1 << 31
+    assert (codes[:m].view(-1, 1 << 15) == c0).all() and torch.equal(codes[m:], c0[:48])
+    assert (scales[:m // 16].view(-1, 1 << 11) == s0).all() and torch.equal(scales[m // 16:], s0[:3] + 2)
+    del x
+    back = i8h.mxfp4_dequantize(codes, scales)
+    want = i8h.mxfp4_dequantize(c0, s0)
+    assert (back[:1 << 32].view(-1, 1 << 16) == want).all() and torch.equal(back[1 << 32:], want[:96] * 4)
