@@ -42,6 +42,7 @@ I8H_OK, I8H_EINVAL, I8H_EUNSUPPORTED, I8H_EHIP = 0, -1, -2, -3
 PATHS = {"auto": 0, "gemv": 1, "gemm": 2, "tall": 3, "skinny": 4}
 DOWN_PATHS = {"auto": 0, "gemv": 1, "gemm": 2}
 TYPES = {torch.float32: 0, torch.bfloat16: 1}
+INT_MAX = (1 << 31) - 1   # the library's sizes are C ints, to which ctypes cuts a larger one without a word
 
 _lib = None
 
@@ -645,6 +646,8 @@ def draft_verify(target_probs, draft_probs, drafted, u, u_next, draft_len=None, 
     dev = target_probs.device
     if D < 0:
         raise ValueError("target_probs must hold a row for each drafted token and one more")
+    if B > INT_MAX or D > INT_MAX or V > INT_MAX:
+        raise ValueError(f"target_probs must have dimensions below 2^31 (got {tuple(target_probs.shape)})")
     if draft_probs is not None:
         _dev(draft_probs, "draft_probs", target_probs.dtype, shape=(B, D, V), device=dev)
     _dev(drafted, "drafted", torch.int32, shape=(B, D), device=dev)

@@ -194,3 +194,13 @@ def test_quantiser_refuses_more_than_its_sizes_hold(calls):
             i8h.mxfp4_dequantize(_meta(*shape[:-1], shape[-1] // 2, dtype=torch.uint8),
                                  _meta(*shape[:-1], shape[-1] // 32, dtype=torch.uint8))
     assert not calls
+
+
+@pytest.mark.parametrize("B,D,V", [(1, 0, (1 << 32) + 5), (1, 0, 1 << 31), ((1 << 32) + 1, 0, 1), (1 << 31, 0, 1),
+                                   (1, (1 << 32) + 3, 1), (2, 1, (1 << 33) + 7)])
+def test_draft_verify_refuses_sizes_past_32_bits(calls, B, D, V):
+    """A size cut to 32 bits would be a smaller, valid one."""
+    f, i = torch.float32, torch.int32
+    with pytest.raises(ValueError):
+        i8h.draft_verify(_meta(B, D + 1, V), None, _meta(B, D, dtype=i), _meta(B, D, dtype=f), _meta(B, dtype=f))
+    assert not calls
