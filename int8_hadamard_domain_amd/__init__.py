@@ -521,6 +521,8 @@ def _mx_weights(codes, scales, K, dev):
     if not isinstance(codes, torch.Tensor) or codes.dim() != 3:
         _dev(codes, "codes", torch.uint8, 3, device=dev)
     E, R, _ = codes.shape
+    if K > INT_MAX or R > INT_MAX:
+        raise ValueError(f"codes must have fewer than 2^31 rows and columns an expert (got {R} and {K})")
     _dev(codes, "codes", torch.uint8, shape=(E, R, K // 2), device=dev)
     _dev(scales, "scales", torch.uint8, shape=(E, R, K // 32), device=dev)
     return E, R

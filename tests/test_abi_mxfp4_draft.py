@@ -204,3 +204,24 @@ def test_draft_verify_refuses_sizes_past_32_bits(calls, B, D, V):
     with pytest.raises(ValueError):
         i8h.draft_verify(_meta(B, D + 1, V), None, _meta(B, D, dtype=i), _meta(B, D, dtype=f), _meta(B, dtype=f))
     assert not calls
+
+
+def _meta_routing(T, E, topk):
+    i = torch.int32
+    return {"topk_ids": _meta(T, topk, dtype=i), "topk_w": _meta(T, topk, dtype=torch.float32),
+            "expert_off": _meta(E + 1, dtype=i), "sorted_pairs": _meta(T * topk, dtype=i),
+            "pair_pos": _meta(T * topk, dtype=i)}
+
+
+@pytest.mark.parametrize("R,K", [(64, (1 << 32) + 128), (64, 1 << 32), (64, 1 << 31), ((1 << 32) + 64, 128),
+                                 ((1 << 31) + 64, 128)])
+def test_products_refuse_sizes_past_32_bits(L, calls, R, K):
+    """Rows of the weights, and their number: cut to 32 bits they would be smaller, valid ones."""
+    T, E, topk = 2, 3, 1
+    codes, scales = _meta(E, R, K // 2, dtype=torch.uint8), _meta(E, R, K // 32, dtype=torch.uint8)
+    r = _meta_routing(T, E, topk)
+    with pytest.raises(ValueError):
+        i8h.moe_gateup_mxfp4_grouped(_meta(T, K), codes, scales, topk, r["expert_off"], r["sorted_pairs"])
+    with pytest.raises(ValueError):
+        i8h.moe_down_mxfp4_combine(_meta(T * topk, K), codes, scales, r)
+    assert not calls
