@@ -331,7 +331,7 @@ k_draft_pick(const DraftArgs a, const PT* __restrict__ p, const PT* __restrict__
 // search for its row costs more than the parallelism gives. Both, of 1024 and of
 // 4096 entries: 1 sequence of 2^18 7.4 and 11.9 us, 32 of 2^17 15.4 and 17.2, 64
 // (8192 workgroups) 23.4 and 23.3, 128 34.4 and 27.5, 256 58 and 40.
-int draft_groups(int B, int V) { return (int64_t)B * ((V + 1023) / 1024) <= 8192 ? 1 : 4; }
+int draft_groups(int B, int V) { return B * (((int64_t)V + 1023) / 1024) <= 8192 ? 1 : 4; }
 
 template <typename PT>
 hipError_t draft(const DraftArgs& a, const void* pv, const void* qv, int B, void* ws, int32_t* tokens,

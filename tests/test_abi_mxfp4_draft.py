@@ -225,3 +225,11 @@ def test_products_refuse_sizes_past_32_bits(L, calls, R, K):
     with pytest.raises(ValueError):
         i8h.moe_down_mxfp4_combine(_meta(T * topk, K), codes, scales, r)
     assert not calls
+
+
+@pytest.mark.parametrize("B", [1, 3])
+def test_draft_workspace_of_the_largest_vocabularies(L, B):
+    """Two float64 sums a chunk of 4096 entries and a count a sequence, up to V = 2^31 - 1."""
+    for V in ((1 << 31) - 4096, (1 << 31) - 1024, (1 << 31) - 1023, (1 << 31) - 1):
+        chunks = -(-V // 4096)
+        assert L.draft_verify_workspace_size(B, V) == -(-(B * chunks * 16 + B * 4) // 256) * 256, V

@@ -250,3 +250,16 @@ def test_empty_chunks_at_a_border(gpu_available, B, chunks, chunk):
         target, off = 0.5 * run[-1], V * 2.0 ** -50 * run[-1]
         assert row[t] > 0, (b, t)
         assert run[t] > target - off and run[t] - row[t] <= target + off, (b, t)
+
+
+@pytest.mark.parametrize("V", [(1 << 31) - 1, (1 << 31) - 1024])
+def test_the_largest_vocabularies(gpu_available, V):
+    print(f"draft_verify V={V}", flush=True)
+    p = torch.zeros((1, 1, V), dtype=torch.bfloat16, device="cuda")
+    at = [5, 1 << 30, V - 2, V - 1]
+    p[0, 0, torch.tensor(at, device="cuda")] = 0.25
+    none = torch.empty((1, 0), device="cuda")
+    for i, v in enumerate(at):
+        un = torch.tensor([0.25 * i + 0.1], device="cuda")
+        tokens, accepted = i8h.draft_verify(p, None, none.int(), none, un)
+        assert tokens.tolist() == [[v]] and accepted.tolist() == [0]
