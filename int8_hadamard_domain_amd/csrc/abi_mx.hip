@@ -65,7 +65,7 @@ int moe_gateup_mxfp4_grouped(const uint16_t* x, int T, int K, const uint8_t* cod
   if ((N % 2) != 0) return I8H_EINVAL;          // gate and up halves
   if ((N % 64) != 0 || (int64_t)N * K >= (int64_t)1 << 32) return I8H_EUNSUPPORTED;   // 32-bit offsets in an expert
   if ((int64_t)T * topk >= (int64_t)1 << 31) return I8H_EUNSUPPORTED;
-  if (!rows_fit(T, K)) return I8H_EUNSUPPORTED;
+  if (!rows_fit(T, K) || !i8h::mx_launch_fits(K, (int64_t)T * topk, E, N)) return I8H_EUNSUPPORTED;
   if (T == 0) return I8H_OK;
   if (!x || !codes || !scales || !expert_off || !sorted_pairs) return I8H_EINVAL;
   if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(expert_off, 4) ||
@@ -100,7 +100,7 @@ int moe_down_mxfp4_combine(const void* act, int act_type, int T, int I, const ui
   if ((H % 32) != 0 || (int64_t)H * I >= (int64_t)1 << 32 || H >= 1 << 25) return I8H_EUNSUPPORTED;
   const int64_t P = (int64_t)T * topk;
   if (P >= (int64_t)1 << 31) return I8H_EUNSUPPORTED;
-  if (!rows_fit(P, I)) return I8H_EUNSUPPORTED;
+  if (!rows_fit(P, I) || !i8h::mx_launch_fits(I, P, E, H)) return I8H_EUNSUPPORTED;
   if (T == 0) return I8H_OK;
   if (!act || !codes || !scales || !topk_ids || !topk_w || !expert_off || !pair_pos || !out) return I8H_EINVAL;
   if (!aligned(act, 16) || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(out, 16)) return I8H_EINVAL;

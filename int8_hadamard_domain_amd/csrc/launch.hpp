@@ -101,6 +101,7 @@ struct MxWorkspace {
   size_t items, total;
   MxWorkspace(int64_t rows, int K, int64_t P, int E);
 };
+bool mx_launch_fits(int K, int64_t P, int E, int R);   // P rows of K against R weight rows an expert
 hipError_t launch_gateup_mxfp4(const uint16_t* x, int T, int K, const uint8_t* codes, const uint8_t* scales, int E,
                                int N, int k, const int32_t* expert_off, const int32_t* sorted_pairs, float* gu,
                                void* act, bool act_bf16, uint8_t* ws, hipStream_t st);

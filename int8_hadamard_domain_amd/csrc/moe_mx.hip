@@ -809,6 +809,17 @@ MxWorkspace::MxWorkspace(int64_t rows, int K, int64_t P, int E) {
   total = items + up((size_t)(1 + plan.passes(P, E)) * sizeof(MxItem));
 }
 
+// workgroups of k_mx_ring
+static int64_t mx_ring_grid(const MxPlan& plan, int64_t P, int E, int R) {
+  return plan.passes(P, E) * cdiv(R / 32, kRgWaves);
+}
+
+// a launch holds fewer than 2^32 threads; the other kernels' grids stay far below
+bool mx_launch_fits(int K, int64_t P, int E, int R) {
+  const MxPlan plan(K, P, E);
+  return plan.stream || mx_ring_grid(plan, P, E, R) * kRgThreads < (int64_t)1 << 32;
+}
+
 template <bool GU, typename XT, typename AT>
 static hipError_t mx_grouped(const XT* x, int64_t rows, int K, int64_t P, const uint8_t* codes, const uint8_t* scales,
                              int E, int R, int topk, const int32_t* expert_off, const int32_t* sorted_pairs,
@@ -817,7 +828,6 @@ static hipError_t mx_grouped(const XT* x, int64_t rows, int K, int64_t P, const 
   const MxPlan plan(K, P, E);
   const int64_t n8 = rows * plan.nbp * 4, qgrid = 1 + (n8 + kPrThreads - 1) / kPrThreads;
   const int ntiles = R / 32;
-  const int64_t rgrid = plan.passes(P, E) * cdiv(ntiles, kRgWaves);
 #define I8H_MX(M, D, S, X) k_mx_stream<GU, M, D, MxSc::S, X><<<kSmBlocks, kSmThreads, 0, st>>>(a, out0, out1)
   if (plan.own) {
     const MxArgs a = {nullptr, codes, scales, 0, plan.row_bytes, E, R, plan.nb, topk, ntiles, nullptr, x, expert_off,
@@ -837,7 +847,7 @@ static hipError_t mx_grouped(const XT* x, int64_t rows, int K, int64_t P, const 
   const MxArgs a = {ws, codes, scales, (uint32_t)(rows * plan.row_bytes + 16), plan.row_bytes, E, R, plan.nb, topk,
                     ntiles, items, nullptr, nullptr, sorted_pairs};
   if (!plan.stream) {
-    k_mx_ring<GU><<<(unsigned)rgrid, kRgThreads, 0, st>>>(a, out0, out1);
+    k_mx_ring<GU><<<(unsigned)mx_ring_grid(plan, P, E, R), kRgThreads, 0, st>>>(a, out0, out1);
   } else if (plan.nb <= kSmGroup) {
     if (plan.nb <= 3 * kStB) I8H_MX(4, 3, kRun, void);   // K = 768, 2048 tokens: 84 us, two deep 87; K = 2048: 85, 81
     else I8H_MX(4, 2, kRun, void);

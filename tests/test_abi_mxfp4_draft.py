@@ -233,3 +233,12 @@ def test_draft_workspace_of_the_largest_vocabularies(L, B):
     for V in ((1 << 31) - 4096, (1 << 31) - 1024, (1 << 31) - 1023, (1 << 31) - 1):
         chunks = -(-V // 4096)
         assert L.draft_verify_workspace_size(B, V) == -(-(B * chunks * 16 + B * 4) // 256) * 256, V
+
+
+def test_products_refuse_more_threads_than_a_launch_takes(L):
+    """Rows past 8192 columns run as a workgroup per pass and 128 weight rows."""
+    T, K, N = 493000, 8448, 508352
+    need = L.moe_gateup_mxfp4_workspace_size(T, K, 1, 1)
+    assert L.moe_gateup_mxfp4_grouped(A, T, K, A, A, 1, N, 1, A, A, None, A, 1, A, need, None) == EUNSUP
+    need = L.moe_down_mxfp4_workspace_size(T, K, 1, N, 1)
+    assert L.moe_down_mxfp4_combine(A, 1, T, K, A, A, 1, N, 1, A, A, A, A, A, A, need, None) == EUNSUP
