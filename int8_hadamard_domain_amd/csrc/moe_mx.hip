@@ -791,7 +791,7 @@ struct MxPlan {
     // and 12.4. 64 rows are within 1 us of 128 up to 20 pairs an expert and 7 us
     // behind at 64.
     const int want = P <= 8 * (int64_t)E ? 1 : 4;
-    const int fit = kSmX / (32 * row_bytes);
+    const int fit = kSmX / 32 / row_bytes;   // the product overflows for the longest rows
     stream = fit >= 1 && (nb <= kSmGroup || nb % 4 == 0);
     mt = stream ? (want <= fit ? want : fit >= 2 ? 2 : 1) : kRgMt;
     own = stream && mt == 1 && nb <= kSmGroup;

@@ -242,3 +242,13 @@ def test_products_refuse_more_threads_than_a_launch_takes(L):
     assert L.moe_gateup_mxfp4_grouped(A, T, K, A, A, 1, N, 1, A, A, None, A, 1, A, need, None) == EUNSUP
     need = L.moe_down_mxfp4_workspace_size(T, K, 1, N, 1)
     assert L.moe_down_mxfp4_combine(A, 1, T, K, A, A, 1, N, 1, A, A, A, A, A, A, need, None) == EUNSUP
+
+
+@pytest.mark.parametrize("I", [8448, 1 << 27, 252645120, 252645120 + 256, 1 << 30, (1 << 31) - 256])
+def test_workspace_of_the_longest_rows(L, I):
+    """Rows past a workgroup's LDS: codes and scales padded to an odd number of 16-byte pieces, 16 bytes behind the
+    last one, a list entry (16 bytes) for the head and at most each pass of 96 rows and expert, and y."""
+    T, E, H, topk = 33, 4, 64, 1
+    up = lambda v: -(-v // 256) * 256  # noqa: E731
+    row = (-(-17 * (I // 32) // 16) | 1) * 16
+    assert L.moe_down_mxfp4_workspace_size(T, I, E, H, topk) == up(T * row + 16) + up(16 * (1 + T // 96 + E)) + up(T * H * 4)
