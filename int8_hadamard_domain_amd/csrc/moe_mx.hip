@@ -115,8 +115,11 @@ __device__ __forceinline__ void lds_barrier() {
 // are registers k and k + HOP, lanes with bit HOP of k set keep b and fetch b of
 // the lane HOP below into a, the others keep a and fetch a into b. One
 // instruction a word: a select whose one side comes from another lane, which the
-// compiler does not form by itself. The blocks wait out the two cycles between
-// a vector write and a lane move's, or a matrix instruction's, read.
+// compiler does not form by itself (it makes a lane move and a select of the
+// intrinsics: 64 vector instructions a stage instead of 32, times within 1 %). The
+// blocks wait out the two cycles between a vector write and a lane move's, or a
+// matrix instruction's, read, and write every output before the last input is
+// read, so outputs are early-clobber.
 #define I8H_SEL(D, MOVED, KEPT) "v_cndmask_b32_dpp " D ", " MOVED ", " KEPT ", vcc " I8H_PERM "\n"
 #define I8H_EXCHANGE                                                                                              \
   "s_nop 1\n"                                                                                                     \
@@ -131,8 +134,8 @@ template <int HOP>
 __device__ __forceinline__ void mx_exchange(u32x4& a, u32x4& b) {
   uint32_t t0, t1, t2, t3, a0 = a[0], a1 = a[1], a2 = a[2], a3 = a[3];
 #define I8H_REGS                                                                                                  \
-  : [t0] "=&v"(t0), [t1] "=&v"(t1), [t2] "=&v"(t2), [t3] "=&v"(t3), [a0] "+v"(a0), [a1] "+v"(a1), [a2] "+v"(a2),   \
-    [a3] "+v"(a3)                                                                                                 \
+  : [t0] "=&v"(t0), [t1] "=&v"(t1), [t2] "=&v"(t2), [t3] "=&v"(t3), [a0] "+&v"(a0), [a1] "+&v"(a1), [a2] "+&v"(a2), \
+    [a3] "+&v"(a3)                                                                                                \
   : [b0] "v"(b[0]), [b1] "v"(b[1]), [b2] "v"(b[2]), [b3] "v"(b[3]), [set] "s"(lanes)                              \
   : "vcc", "scc"
   if constexpr (HOP == 1) {

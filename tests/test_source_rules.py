@@ -72,3 +72,22 @@ def test_no_hand_written_packed_fp32():
         with open(path) as f:
             text = f.read()
         assert not re.search(r"v_pk_(add|mul|fma)_f32", text), os.path.basename(path)
+
+
+def test_asm_of_several_instructions_keeps_outputs_apart_from_inputs():
+    """An output that an instruction writes while a later one still reads an input may not share a register with that
+    input: in statements of more than one vector instruction every output is early-clobber (&)."""
+    found = 0
+    for path in _sources():
+        with open(path) as f:
+            text = f.read()
+        macros = dict(re.findall(r"#define (I8H_\w+)[ \\\n]+((?:[^\n]*\\\n)*[^\n]*)", text))
+        for stmt in _asm_statements(text):
+            for name in re.findall(r"\bI8H_\w+", stmt):
+                stmt = stmt.replace(name, macros.get(name, name))
+            template, *operands = stmt.split(":")
+            if operands and len(re.findall(r"I8H_SEL\(|\bv_\w+", template)) > 1:
+                for constraint in re.findall(r'"([=+][^"]*)"', operands[0]):
+                    found += 1
+                    assert "&" in constraint, f"{os.path.basename(path)}: output {constraint} without & in {stmt}"
+    assert found > 0
