@@ -523,7 +523,9 @@ k_mx_stream(const MxArgs a, float* __restrict__ out0, AT* __restrict__ out1) {
         for (int q = 0; q < NA; ++q) acc[q] = f32x16{};
         for (int s0 = 0; s0 < SP; s0 += PD) {
           if (s0 % kStB == 0) {   // this group's scales into LDS, the next one's on their way
+            wave_lds_order();   // every lane has read the last group's
             store_sc();
+            wave_lds_order();
             load_sc(t, s0 / kStB + 1);
             sn = read_sw(s0);
           }

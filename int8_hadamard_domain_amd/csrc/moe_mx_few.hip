@@ -201,6 +201,7 @@ k_down_mx_few(const XT* __restrict__ act, int nb, const uint8_t* __restrict__ wq
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
       if (4 * i < steps) xv[i] = mx_raw8(act + r * (nb * kMxBlock) + 8 * min(i * kWave + lane, 4 * nb - 1));
+    wave_lds_order();   // every lane has read the last slot's row
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
       if (4 * i < steps) {
@@ -215,6 +216,7 @@ k_down_mx_few(const XT* __restrict__ act, int nb, const uint8_t* __restrict__ wq
           if ((p & 3) == 0) row[kFdMaxI / 2 + p / 4] = (uint8_t)(in ? sc : 127);
         }
       }
+    wave_lds_order();
     f32x4 acc = {};
 #pragma unroll
     for (int i = 0; i < kFewSteps; ++i)

@@ -91,3 +91,20 @@ def test_asm_of_several_instructions_keeps_outputs_apart_from_inputs():
                     found += 1
                     assert "&" in constraint, f"{os.path.basename(path)}: output {constraint} without & in {stmt}"
     assert found > 0
+
+
+def test_lds_that_lanes_of_a_wave_hand_on_is_ordered():
+    """LDS that a wave's lanes write for its other lanes, without a workgroup barrier: wave_lds_order() stands between
+    the write and the reads, and between the reads and the next write."""
+    with open(os.path.join(CSRC, "moe_mx.hip")) as f:
+        text = f.read()
+    calls = [m.start() for m in re.finditer(r"^\s*store_sc\(\);", text, flags=re.M)]
+    assert calls
+    for at in calls:
+        before, after = text[:at].rstrip().split("\n")[-1], text[at:].strip().split("\n")[1]
+        assert "wave_lds_order();" in before and "wave_lds_order();" in after
+    with open(os.path.join(CSRC, "moe_mx_few.hip")) as f:
+        text = f.read()
+    body = text[text.index("for (int j = wave; j < k; j += waves) {"):text.index("part[j][4 * g + i]")]
+    write, read = body.index("*reinterpret_cast<uint32_t*>(&row["), body.index("reinterpret_cast<const u32x4*>(&row[")
+    assert "wave_lds_order();" in body[:write] and "wave_lds_order();" in body[write:read]
