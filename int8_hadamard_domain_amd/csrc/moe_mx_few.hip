@@ -82,8 +82,7 @@ k_gateup_mx_few(const uint16_t* __restrict__ x, int T, int nb, const uint8_t* __
   // weight row of this lane: rows 4 G, 4 G + 1 of a tile are gate rows 2 G, 2 G + 1,
   // rows 4 G + 2, 4 G + 3 the matching up rows
   const int tile = blockIdx.x * kFgWaves + tid / kWave;
-  const bool live = tile * 8 < I;
-  const int i0 = (live ? tile * 8 : 0) + 2 * (c / 4) + (c & 1);
+  const int i0 = tile * 8 + 2 * (c / 4) + (c & 1);   // N % 64 == 0: the tiles fill the grid's waves
   const size_t n = (size_t)e * N + ((c & 2) ? I + i0 : i0);
   const uint8_t* wr = wq + n * (16 * nb) + 16 * g;
   const uint8_t* wsr = ws + n * nb;
@@ -126,7 +125,6 @@ k_gateup_mx_few(const uint16_t* __restrict__ x, int T, int nb, const uint8_t* __
   for (int p0 = kFgAhead * kFgThreads; p0 < groups; p0 += kFgThreads) quantise(p0 + tid, raw(p0 + tid));
   token /= topk;
   __syncthreads();
-  if (!live) return;
 
   for (int c0 = 0; c0 < m; c0 += 16) {
     const int r = r0 + min(c0 + c, m - 1);
@@ -252,7 +250,7 @@ hipError_t launch_gateup_mxfp4_few(const uint16_t* x, int T, int K, const uint8_
                                    int N, int k, const int32_t* expert_off, const int32_t* sorted_pairs, float* gu,
                                    void* act, bool act_bf16, hipStream_t st) {
   const int nb = K / kMxBlock;
-  const dim3 grid(cdiv(N / 16, kFgWaves), T * k < E ? T * k : E);
+  const dim3 grid(N / (16 * kFgWaves), T * k < E ? T * k : E);
   const size_t lds = (size_t)T * few_row_bytes(nb);
   if (act_bf16)
     k_gateup_mx_few<<<grid, kFgThreads, lds, st>>>(x, T, nb, codes, scales, E, N, k, expert_off, sorted_pairs, gu,
