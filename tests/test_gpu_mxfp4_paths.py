@@ -368,3 +368,47 @@ def test_quantiser_of_one_row_past_2_32_elements(gpu_available):
     back = i8h.mxfp4_dequantize(codes, scales)
     want = i8h.mxfp4_dequantize(c0, s0)
     assert (back[:1 << 32].view(-1, 1 << 16) == want).all() and torch.equal(back[1 << 32:], want[:96] * 4)
+
+
+# --------------------------------------------------------------------------------- each depth of the prefetch, reloads
+
+# at most 8 pairs an expert and past the one-launch form: K to 768, to 1024, to 2048 take prefetches of their own
+@pytest.mark.parametrize("T,K,E,topk,N", [(40, 768, 64, 2, 128), (40, 896, 64, 2, 64), (40, 1024, 64, 2, 128),
+                                          (40, 1152, 64, 2, 64), (40, 1920, 64, 2, 64), (40, 2048, 64, 2, 128)])
+def test_gate_up_small_passes_of_every_depth(gpu_available, T, K, E, topk, N):
+    _check_gateup(T, K, E, topk, N, seed=T + K + E + N)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("I", [768, 800, 1024, 1056, 1536, 2016, 2048])
+def test_down_small_passes_of_every_depth(gpu_available, I, dtype):
+    _check_down(40, I, 64, 2, 96, seed=I, dtype=dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("I", [768, 800, 1536, 2016, 2048, 2080, 2176, 2304, 6272, 8192, 8704])
+def test_down_large_passes_of_every_kind(gpu_available, I, dtype):
+    _check_down(90, I, 3, 2, 64, seed=I, dtype=dtype)
+
+
+@pytest.mark.parametrize("T,k,K", [(8, 4, 2176), (8, 4, 4096), (1, 32, 4096), (5, 6, 6272)])
+def test_one_launch_gate_up_takes_long_rows_for_more_than_sixteen_pairs(gpu_available, T, k, K):
+    """Every slot the same expert: its weights, longer than a chunk, pass again for each sixteen pairs."""
+    E, N = 33, 64
+    r = _routing_of(np.full((T, k), 7), E)
+    rng = np.random.default_rng(T * k + K)
+    x = _exact_values(rng, T, K)
+    codes, scales = _weights(rng, E, N, K, 2)
+    print(f"one-launch gate_up, long rows T={T} k={k} K={K}", flush=True)
+    gu, act = i8h.moe_gateup_mxfp4_grouped(x.cuda(), u8(codes), u8(scales), k, r["expert_off"], r["sorted_pairs"])
+    _, a16 = i8h.moe_gateup_mxfp4_grouped(x.cuda(), u8(codes), u8(scales), k, r["expert_off"], r["sorted_pairs"],
+                                          gate_up=False, act_dtype=torch.bfloat16)
+    qc, qs = mxfp4.quantize(values(x))
+    ref, mag = mxfp4.grouped(mxfp4.dequantize(qc, qs)[r["sorted_pairs"].cpu().numpy() // k], codes, scales,
+                             r["expert_off"].cpu().numpy())
+    assert mag.max() < 2.0 ** 24 * _units(qs, scales)
+    got = values(gu)
+    assert np.array_equal(got, ref)
+    want, z = mxfp4.gelu_tanh_act(got)
+    assert np.all(np.abs(values(act) - want) <= _act_bound(want, z, got[:, :N // 2], got[:, N // 2:]))
+    assert torch.equal(a16, act.to(torch.bfloat16))
