@@ -12,9 +12,11 @@
  * codes [R, K/2] and scales [R, K/32], both uint8, rows contiguous.
  *
  * The products take both operands in MXFP4 (v_mfma_scale_f32_*_f8f6f4), and
- * sum in float32: products of two E2M1 values and their scales are exact,
- * and the matrix unit keeps float32's full significand when it adds them. A
- * NaN scale makes every output NaN whose row or column holds it.
+ * sum in float32: products of two E2M1 values and their scales are exact
+ * multiples of 2^-149 (what lies below is lost), and the matrix unit keeps
+ * float32's full significand when it adds them, subnormals included. Sums past
+ * float32's largest value are infinite. A NaN scale makes every output NaN
+ * whose row or column holds it.
  */
 #ifndef I8H_MXFP4_H
 #define I8H_MXFP4_H

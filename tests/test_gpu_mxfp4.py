@@ -314,3 +314,27 @@ def test_rows_around_the_outputs_are_left_alone(gpu_available):
     torch.cuda.synchronize()
     for n, t in big.items():
         assert (t[0] == 7).all() and (t[-1] == 7).all(), n
+
+
+@pytest.mark.parametrize("T,K", [(4, 256), (40, 256), (600, 256), (20, 2304), (20, 8448)])
+def test_gate_up_at_the_ends_of_float32(gpu_available, T, K):
+    """Terms all alike, 2.25 or 9 times a power of two: their sums are exact down into the subnormals where the terms
+    are multiples of 2^-149, and infinite past float32's range; below, they lose at most themselves."""
+    N = 64
+    r = {"expert_off": _i32([0, T]), "sorted_pairs": _i32(np.arange(T))}
+    for sw in (0, 1, 20, 127, 250, 254):
+        for ex in (-122, -30, -4, 0, 100, 125):
+            for code, value in ((3, 1.5), (7, 6.0)):
+                print(f"gate_up ends of float32 T={T} K={K} scale={sw} x=1.5*2^{ex} weight={value}", flush=True)
+                x = torch.full((T, K), 1.5 * 2.0 ** ex).to(torch.bfloat16).cuda()
+                gu, _ = i8h.moe_gateup_mxfp4_grouped(x, torch.full((1, N, K // 2), 17 * code, dtype=torch.uint8, device="cuda"),
+                                                     torch.full((1, N, K // 32), sw, dtype=torch.uint8, device="cuda"), 1,
+                                                     r["expert_off"], r["sorted_pairs"], act=False)
+                term = 1.5 * value * 2.0 ** (ex + sw - 127)
+                got = values(gu)
+                if term * K >= 2.0 ** 128:
+                    assert np.isinf(got).all() and (got > 0).all()
+                elif term >= 2.0 ** -147:                # 2.25 and 9 are whole multiples of a quarter
+                    assert (got == term * K).all()
+                else:
+                    assert ((got >= 0) & (got <= term * K)).all()
