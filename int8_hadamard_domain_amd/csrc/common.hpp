@@ -58,15 +58,6 @@ __device__ __forceinline__ void put_act(uint16_t* p, size_t i, float v) {
   p[i] = __builtin_bit_cast(uint16_t, (__bf16)v);
 }
 
-// LDS that a wave's lanes write for its other lanes: what stands before is done
-// when what follows begins, in each lane's program (no instruction; the hardware
-// takes a wave's LDS accesses in order)
-__device__ __forceinline__ void wave_lds_order() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
-}
-
 __host__ __device__ constexpr inline int cdiv(int a, int b) { return (a + b - 1) / b; }
 
 }  // namespace i8h

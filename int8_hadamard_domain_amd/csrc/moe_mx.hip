@@ -31,13 +31,13 @@
 //   k_mx_ring    for K too long for that: activation rows in stages through LDS.
 //
 // Bounds, at 128 experts, top 8, K = 2048, N = 1536 (I = 768, H = 2048):
-//   128 tokens   the weights from HBM: gate_up 216 MB in 46 us, 4.7 TB/s (a large
+//   128 tokens   the weights from HBM: gate_up 216 MB in 44 us, 4.9 TB/s (a large
 //                copy: 5.1), down 111 MB and the y round trip in 32 us.
 //   2048 tokens  gate_up 75 us, 71 of them k_mx_stream: 255 MB of HBM traffic
 //                (weights fetched 1.04 times) at 3.6 TB/s, matrix units 30 % busy,
 //                LDS less; the rest are each pass's start (rows to LDS, 5 to 7 us),
-//                whole rounds of tiles and the epilogue. down 84 us: y, 131 MB,
-//                written (k_mx_stream 53) and read again (k_mx_combine 22).
+//                whole rounds of tiles and the epilogue. down 86 us: y, 131 MB,
+//                written (k_mx_stream 53 to 60) and read again (k_mx_combine 22).
 
 #include <type_traits>
 
@@ -261,7 +261,8 @@ k_mx_stream(const MxArgs a, float* __restrict__ out0, AT* __restrict__ out1) {
   //     several (its rows taken as four tiles);
   //   fewer, gate_up, clearly (rest : others above 9 : 8): a helper takes the
   //     whole remainder of its passes, a multiple of 8 tiles, as eight waves take
-  //     a tile each in one round; often there is no cut at all.
+  //     a tile each in one round; often there is no cut at all. The border lies
+  //     between 132 and 146 passes of the sizes below, not measured at others.
   // Measured, even runs always and this deal: gate_up K = 2048, 128 tokens (120
   // passes) 48.3 and 46.2 us, 1024 (146) 63.1 and 60.3, 2048 (202) 80 and 75, 640
   // (132, helpers' whole remainders) 56.2 and 58.8; 18 passes 28.5 and 20.8; down
@@ -796,6 +797,10 @@ struct MxPlan {
     // and 12.4. 64 rows are within 1 us of 128 up to 20 pairs an expert and 7 us
     // behind at 64.
     const int want = P <= 8 * (int64_t)E ? 1 : 4;
+    // Longer rows than 64 blocks: this kernel as far as one pass of 32 rows fits, also
+    // where the other takes passes of 96. Both, 32 experts, top 4, N = 1536: K = 2304,
+    // 128 and 2048 tokens 22.9 and 25.8 us, 53 and 60; 4096 30.6 and 42.8, 76 and 101;
+    // 7168 47 and 69, 163 and 170; 8192 58 and 79, 166 and 190.
     const int fit = kSmX / 32 / row_bytes;   // the product overflows for the longest rows
     stream = fit >= 1 && (nb <= kSmGroup || nb % 4 == 0);
     mt = stream ? (want <= fit ? want : fit >= 2 ? 2 : 1) : kRgMt;
@@ -837,8 +842,9 @@ static hipError_t mx_grouped(const XT* x, int64_t rows, int K, int64_t P, const 
   if (plan.own) {
     const MxArgs a = {nullptr, codes, scales, 0, plan.row_bytes, E, R, plan.nb, topk, ntiles, nullptr, x, expert_off,
                       sorted_pairs};
-    // Depth of the prefetch: what the registers leave, and for short rows no more
-    // than a tile's stages, since those past the last are products of zeros
+    // Depth of the prefetch: what the registers leave, less for short rows, whose
+    // stages are rounded up to it: those past the last are products of zeros (up to
+    // two of three at K <= 256, three of eight at five stages)
     if (plan.nb <= 3 * kStB) I8H_MX(1, 3, kRun, XT);
     else if (plan.nb <= 4 * kStB) I8H_MX(1, 4, kRun, XT);
     else I8H_MX(1, 8, kRun, XT);

@@ -71,6 +71,15 @@ __device__ __forceinline__ void mx_load8_once(const T* p, float (&v)[8]) {
   mx_floats(mx_raw8_once(p), v);
 }
 
+// LDS that a wave's lanes write for its other lanes: what stands before is done
+// when what follows begins, in each lane's program (no instruction; the hardware
+// takes a wave's LDS accesses in order)
+__device__ __forceinline__ void wave_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
 // 32 x 32 x 64 with both operands E2M1: lane l holds the 32 codes of row (A) or
 // column (B) l % 32 for k = 32 (l / 32) .. +31 of the step, and in byte SA / SB
 // of its scale word that block's E8M0 scale; result register r of lane l is
