@@ -29,7 +29,7 @@ extern "C" {
  *
  * draft_probs NULL stands for drafts taken without sampling (q = 1 at x_i, 0
  * elsewhere): token i stays while u < p(x_i), and rest is p without x_n.
- * Products, differences and sums are float64 (the first two exact). Entries of
+ * Products, differences and sums are float64 (products exact). Entries of
  * rest that are not positive and finite count as zero; if none is left, rest is
  * p itself, and if p has none either, next is V - 1. A drafted token outside
  * [0, V) is refused. u and u_next are uniform in [0, 1). Results are the same,
