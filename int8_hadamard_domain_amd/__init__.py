@@ -28,6 +28,11 @@ Functions (same names as the C entry points):
   moe_down_mxfp4_combine     grouped MXFP4 down projection + weighted combine
   draft_verify               which drafted tokens of a verify batch stay, and
                              the token sampled after them
+  moe_route_scored_permute   routing by softmax or sigmoid scores, with a bias
+                             for balance and groups of experts
+  lora_add                   low-rank adapters of many requests beside any
+                             projection's output
+  linear_i8f16_lora          linear_i8f16 with the requests' adapters
 """
 
 import ctypes
@@ -42,6 +47,7 @@ I8H_OK, I8H_EINVAL, I8H_EUNSUPPORTED, I8H_EHIP = 0, -1, -2, -3
 PATHS = {"auto": 0, "gemv": 1, "gemm": 2, "tall": 3, "skinny": 4}
 DOWN_PATHS = {"auto": 0, "gemv": 1, "gemm": 2}
 TYPES = {torch.float32: 0, torch.bfloat16: 1}
+SCORES = {"softmax": 0, "sigmoid": 1}
 INT_MAX = (1 << 31) - 1   # the library's sizes are C ints, to which ctypes cuts a larger one without a word
 
 _lib = None
@@ -63,7 +69,7 @@ def lib():
         raise RuntimeError(f"{LIB_PATH} is missing: build it first "
                            "(python -m int8_hadamard_domain_amd.build_lib)")
     L = ctypes.CDLL(LIB_PATH)
-    P, I, I64, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+    P, I, I64, SZ, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
     sig = {
         "i8h_status_string": (ctypes.c_char_p, [I]),
         "moe_route_permute_workspace_size": (SZ, [I, I, I]),
@@ -98,6 +104,11 @@ def lib():
         "moe_gateup_mxfp4_grouped": (I, [P, I, I, P, P, I, I, I, P, P, P, P, I, P, SZ, P]),
         "moe_down_mxfp4_workspace_size": (SZ, [I, I, I, I, I]),
         "moe_down_mxfp4_combine": (I, [P, I, I, I, P, P, I, I, I, P, P, P, P, P, P, SZ, P]),
+        "moe_route_scored_workspace_size": (SZ, [I, I, I]),
+        "moe_route_scored_permute": (I, [P, I, I, I, I, I, P, I, I, I, I, F, P, P, P, P, P, P, SZ, P]),
+        "lora_workspace_size": (SZ, [I, I]),
+        "lora_add": (I, [P, I, I64, P, I64, I, I, I, P, P, I, I, P, P, P, I64, P, SZ, P]),
+        "linear_i8f16_lora": (I, [P, I, I, P, P, I, P, P, I, I, P, P, P, P, SZ, P]),
         "draft_verify_workspace_size": (SZ, [I, I]),
         "draft_verify": (I, [P, P, I, P, P, P, P, I, I, I, P, P, P, SZ, P]),
     }
@@ -665,3 +676,124 @@ def draft_verify(target_probs, draft_probs, drafted, u, u_next, draft_len=None, 
     _call("draft_verify", dev, _ptr(target_probs), _ptr(draft_probs), pt, _ptr(drafted), _ptr(draft_len), _ptr(u),
           _ptr(u_next), B, D, V, _ptr(tokens), _ptr(accepted), _ptr(workspace), workspace.numel())
     return tokens, accepted
+
+
+def moe_route_scored_permute(logits, topk, score="softmax", bias=None, groups=1, topk_groups=1, group_top=1,
+                             renormalize=True, scale=1.0, out=None):
+    """Routing by scores: logits [T, E] float32 or bfloat16 -> the dict of
+    moe_route_permute.
+
+    score: "softmax" (over all experts) or "sigmoid". The topk experts of
+    largest score + bias (bias [E] float32, or None) are chosen, from the
+    topk_groups of `groups` runs of experts whose group_top (1 or 2) largest
+    values sum highest. topk_w holds their scores, divided by their sum with
+    renormalize, times scale. `out` may hold preallocated tensors, the
+    workspace among them.
+    """
+    lt = _type(logits, "logits")
+    _dev(logits, "logits", logits.dtype, 2)
+    T, E = logits.shape
+    if T > INT_MAX or E > INT_MAX:
+        raise ValueError(f"logits must have dimensions below 2^31 (got {tuple(logits.shape)})")
+    dev = logits.device
+    if score not in SCORES:
+        raise ValueError(f'score must be "softmax" or "sigmoid" (got {score!r})')
+    for name, v in (("topk", topk), ("groups", groups), ("topk_groups", topk_groups), ("group_top", group_top)):
+        if not 0 < v <= INT_MAX:
+            raise ValueError(f"{name} must be positive and below 2^31 (got {v})")
+    if bias is not None:
+        _dev(bias, "bias", torch.float32, shape=(E,), device=dev)
+    o = _routing_outputs(out, T, E, topk, dev)
+    need = lib().moe_route_scored_workspace_size(T, E, topk)
+    if need > 0 or "workspace" in o:
+        o["workspace"] = _workspace(o.get("workspace"), "workspace", need, dev)
+    _call("moe_route_scored_permute", dev, _ptr(logits), lt, T, E, topk, SCORES[score], _ptr(bias), groups,
+          topk_groups, group_top, 1 if renormalize else 0, scale, _ptr(o["topk_ids"]), _ptr(o["topk_w"]),
+          _ptr(o["expert_off"]), _ptr(o["sorted_pairs"]), _ptr(o["pair_pos"]), _ptr(o.get("workspace")), need)
+    return o
+
+
+def _rows(t, name, dtype, shape, device):
+    """Check a matrix of `dtype` whose rows are contiguous and may lie apart. Returns its row stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda or (device is not None and t.device != device):
+        raise ValueError(f"{name} must be on {device or 'the GPU'} (got {t.device})")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must have {'2 dimensions' if shape is None else f'shape {tuple(shape)}'} "
+                         f"(got {tuple(t.shape)})")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if rows <= 1:
+        return -(-cols // 8) * 8      # no second row: any distance will do
+    if t.stride(0) < cols:
+        raise ValueError(f"{name} must have rows that do not overlap")
+    return t.stride(0)
+
+
+def _lora(lora_a, lora_b, adapter, lora_scale, T, K, N, dev):
+    """Check the adapters [L, R, K] and [L, N, R] bf16, the rows' adapters [T] and the scales [L]. Returns (L, R)."""
+    _dev(lora_a, "lora_a", torch.bfloat16, 3, device=dev)
+    L, R, _ = lora_a.shape
+    if max(T, K, N, L, R) > INT_MAX:
+        raise ValueError("sizes must be below 2^31")
+    _dev(lora_a, "lora_a", torch.bfloat16, shape=(L, R, K))
+    _dev(lora_b, "lora_b", torch.bfloat16, shape=(L, N, R), device=dev)
+    _dev(adapter, "adapter", torch.int32, shape=(T,), device=dev)
+    _dev(lora_scale, "lora_scale", torch.float32, shape=(L,), device=dev)
+    return L, R
+
+
+def lora_add(base, x, lora_a, lora_b, adapter, lora_scale, out=None, workspace=None):
+    """Low-rank adapters beside a projection: out[t] = base[t] + lora_scale[l]
+    * lora_b[l] @ (lora_a[l] @ x[t]) with l = adapter[t]; rows whose adapter
+    lies outside [0, L), for instance -1, are base's.
+
+    base [T, N] float32 or bfloat16 (the projection's output), x [T, K] bf16
+    (its input), lora_a [L, R, K] and lora_b [L, N, R] bf16, adapter [T]
+    int32, lora_scale [L] float32. Rows of base, x and out may lie apart (a
+    column slice of a wider matrix). `out` may be base. Returns out.
+    """
+    bt = _type(base, "base")
+    ldb = _rows(base, "base", base.dtype, None, None)
+    T, N = base.shape
+    dev = base.device
+    ldx = _rows(x, "x", torch.bfloat16, None, dev)
+    if x.shape[0] != T:
+        raise ValueError(f"x must have base's {T} rows (got {x.shape[0]})")
+    K = x.shape[1]
+    L, R = _lora(lora_a, lora_b, adapter, lora_scale, T, K, N, dev)
+    if out is None:
+        out = base.new_empty((T, N))
+        ldo = N
+    else:
+        ldo = _rows(out, "out", base.dtype, base.shape, dev)
+    workspace = _workspace(workspace, "workspace", lib().lora_workspace_size(T, R), dev)
+    _call("lora_add", dev, _ptr(base), bt, ldb, _ptr(x), ldx, T, K, N, _ptr(lora_a), _ptr(lora_b), L, R,
+          _ptr(adapter), _ptr(lora_scale), _ptr(out), ldo, _ptr(workspace), workspace.numel())
+    return out
+
+
+def linear_i8f16_lora(x, codes, scales, lora_a, lora_b, adapter, lora_scale, out=None, workspace=None):
+    """linear_i8f16 with the adapters of the rows' requests: x [T, K] bf16,
+    codes [N, K] int8, scales [N, K/128] float16, adapters as for lora_add ->
+    y [T, N] float32."""
+    _dev(x, "x", torch.bfloat16, 2)
+    T, K = x.shape
+    dev = x.device
+    _dev(codes, "codes", torch.int8, 2, device=dev)
+    N = codes.shape[0]
+    L, R = _lora(lora_a, lora_b, adapter, lora_scale, T, K, N, dev)
+    _dev(codes, "codes", torch.int8, shape=(N, K))
+    _dev(scales, "scales", torch.float16, shape=(N, K // 128), device=dev)
+    if out is None:
+        out = torch.empty((T, N), dtype=torch.float32, device=dev)
+    else:
+        _dev(out, "out", torch.float32, shape=(T, N), device=dev)
+    workspace = _workspace(workspace, "workspace", lib().lora_workspace_size(T, R), dev)
+    _call("linear_i8f16_lora", dev, _ptr(x), T, K, _ptr(codes), _ptr(scales), N, _ptr(lora_a), _ptr(lora_b), L, R,
+          _ptr(adapter), _ptr(lora_scale), _ptr(out), _ptr(workspace), workspace.numel())
+    return out

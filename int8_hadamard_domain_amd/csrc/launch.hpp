@@ -12,7 +12,11 @@ constexpr int kMaxTopk = 32;
 
 // chunks of whole tokens (at most 256 pairs each) of the many-token routing
 int64_t route_chunks(int T, int k);
+int route_chunk_tokens(int T, int k);
 size_t route_workspace_bytes(int T, int E, int k);
+// the permutation of ids [T, k] from the chunks' histograms: totals, scan, stable ranks
+hipError_t launch_route_scatter(const int32_t* ids, int T, int E, int k, const int32_t* hist, int32_t* expert_off,
+                                int32_t* sorted_pairs, int32_t* pair_pos, hipStream_t st);
 // the allocation-free routing call's device scratch: its size, and its
 // address on the current device (which must be the stream's), looked up once
 // per device
@@ -118,6 +122,19 @@ hipError_t launch_gateup_mxfp4_few(const uint16_t* x, int T, int K, const uint8_
 hipError_t launch_down_mxfp4_few(const void* act, bool act_bf16, int T, int I, const uint8_t* codes,
                                  const uint8_t* scales, int H, int k, const int32_t* ids, const float* tw,
                                  const int32_t* pos, float* out, hipStream_t st);
+
+// experts by scores (route_scored.hip); keep of the groups stay, top values make a group's worth
+size_t scored_workspace_bytes(int T, int E, int k);
+hipError_t launch_route_scored(const void* logits, bool bf16, int T, int E, int k, bool sigmoid, const float* bias,
+                               int groups, int keep, int top, bool renorm, float scale, int32_t* ids, float* w,
+                               int32_t* expert_off, int32_t* sorted_pairs, int32_t* pair_pos, void* ws,
+                               hipStream_t st);
+
+// low-rank adapters (lora.hip): h [T, R] float32 holds the scaled inner sums
+hipError_t launch_lora_shrink(const uint16_t* x, int64_t ldx, int T, int K, const uint16_t* a, int L, int R,
+                              const int32_t* adapter, const float* scale, float* h, hipStream_t st);
+hipError_t launch_lora_add(const void* base, bool bf16, int64_t ldb, int T, int N, const uint16_t* b, int L, int R,
+                           const int32_t* adapter, const float* h, void* out, int64_t ldo, hipStream_t st);
 
 // verification of drafted tokens (draft.hip)
 int draft_chunks(int B, int V);
