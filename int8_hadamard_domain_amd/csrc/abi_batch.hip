@@ -73,8 +73,7 @@ int moe_route_scored_permute(const void* logits, int logits_type, int T, int E, 
   if (topk > (int64_t)topk_groups * (E / groups)) return I8H_EINVAL;
   if (E > kMaxExperts || topk > kMaxTopk || groups > I8H_MAX_GROUPS) return I8H_EUNSUPPORTED;
   if ((int64_t)T * topk >= (int64_t)1 << 31) return I8H_EUNSUPPORTED;
-  // the chunk histograms (E counts per chunk of whole tokens) are indexed in 32 bits
-  if (i8h::route_chunks(T, topk) * E >= (int64_t)1 << 31) return I8H_EUNSUPPORTED;
+  if (!i8h::scored_fits(T, E, topk)) return I8H_EUNSUPPORTED;
   if (T == 0) return I8H_OK;
   if (!logits || !topk_ids || !topk_w || !expert_off || !sorted_pairs || !pair_pos) return I8H_EINVAL;
   if (!aligned(logits, type_size(logits_type)) || !aligned(bias, 4) || !aligned(topk_ids, 4) ||

@@ -12,11 +12,7 @@ constexpr int kMaxTopk = 32;
 
 // chunks of whole tokens (at most 256 pairs each) of the many-token routing
 int64_t route_chunks(int T, int k);
-int route_chunk_tokens(int T, int k);
 size_t route_workspace_bytes(int T, int E, int k);
-// the permutation of ids [T, k] from the chunks' histograms: totals, scan, stable ranks
-hipError_t launch_route_scatter(const int32_t* ids, int T, int E, int k, const int32_t* hist, int32_t* expert_off,
-                                int32_t* sorted_pairs, int32_t* pair_pos, hipStream_t st);
 // the allocation-free routing call's device scratch: its size, and its
 // address on the current device (which must be the stream's), looked up once
 // per device
@@ -124,6 +120,7 @@ hipError_t launch_down_mxfp4_few(const void* act, bool act_bf16, int T, int I, c
                                  const int32_t* pos, float* out, hipStream_t st);
 
 // experts by scores (route_scored.hip); keep of the groups stay, top values make a group's worth
+bool scored_fits(int T, int E, int k);
 size_t scored_workspace_bytes(int T, int E, int k);
 hipError_t launch_route_scored(const void* logits, bool bf16, int T, int E, int k, bool sigmoid, const float* bias,
                                int groups, int keep, int top, bool renorm, float scale, int32_t* ids, float* w,

@@ -41,8 +41,6 @@ __host__ __device__ inline int chunk_tokens(int T, int k) {
   return max(1, min(most, spread));
 }
 
-int route_chunk_tokens(int T, int k) { return chunk_tokens(T, k); }
-
 int64_t route_chunks(int T, int k) {
   const int tpc = chunk_tokens(T, k);
   return ((int64_t)T + tpc - 1) / tpc;
@@ -263,14 +261,6 @@ k_route_small(const float* __restrict__ logits, int T, int E, int k,
   }
 }
 
-hipError_t launch_route_scatter(const int32_t* ids, int T, int E, int k, const int32_t* hist, int32_t* expert_off,
-                                int32_t* sorted_pairs, int32_t* pair_pos, hipStream_t st) {
-  const int nc = (int)route_chunks(T, k);
-  k_route_scatter<<<nc, kRouteThreads, 0, st>>>(ids, T * k, E, nc, chunk_tokens(T, k) * k, hist, expert_off,
-                                                sorted_pairs, pair_pos);
-  return hipGetLastError();
-}
-
 size_t route_workspace_bytes(int T, int E, int k) {
   if (T <= 4) return 0;
   return (size_t)route_chunks(T, k) * (size_t)E * sizeof(int32_t);
@@ -333,6 +323,7 @@ hipError_t launch_route(const float* logits, int T, int E, int k, int32_t* ids, 
   const int threads = kWave * min(kRowWaves, tpc);   // a wave per token of the chunk, at most 16
   if (nchunks * E >= ((int64_t)1 << 31)) return hipErrorInvalidValue;  // histogram index range
   int32_t* hist = static_cast<int32_t*>(ws);
+  const int P = T * k;
   const int nc = (int)nchunks;
   // rotation workgroups after the routing chunks: a 128-block per 16 lanes
   const int64_t rot_wgs = x != nullptr ? ((int64_t)T * (K / kGroup) + threads / 16 - 1) / (threads / 16) : 0;
@@ -351,7 +342,8 @@ hipError_t launch_route(const float* logits, int T, int E, int k, int32_t* ids, 
   else if (vpl <= 8) I8H_ROWS(8);
   else I8H_ROWS(16);
 #undef I8H_ROWS
-  return launch_route_scatter(ids, T, E, k, hist, expert_off, sorted_pairs, pair_pos, st);
+  k_route_scatter<<<nc, kRouteThreads, 0, st>>>(ids, P, E, nc, tpc * k, hist, expert_off, sorted_pairs, pair_pos);
+  return hipGetLastError();
 }
 
 }  // namespace i8h
