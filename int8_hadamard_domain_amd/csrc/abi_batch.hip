@@ -109,6 +109,9 @@ int lora_add(const void* base, int base_type, int64_t ldb, const uint16_t* x, in
   if (meets_lora(o, x, T, K, ldx, N, lora_a, lora_b, L, R, adapter, lora_scale, workspace, workspace_bytes))
     return I8H_EINVAL;
   hipStream_t st = as_stream(stream);
+  if (i8h::lora_few(T, R))
+    return from_hip(i8h::launch_lora_few(base, base_type == I8H_BF16, ldb, x, ldx, T, K, N, lora_a, lora_b, L, R,
+                                         adapter, lora_scale, out, ldo, st));
   float* h = static_cast<float*>(workspace);
   if (i8h::launch_lora_shrink(x, ldx, T, K, lora_a, L, R, adapter, lora_scale, h, st) != hipSuccess)
     return I8H_EHIP;

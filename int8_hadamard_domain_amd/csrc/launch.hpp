@@ -130,6 +130,11 @@ hipError_t launch_route_scored(const void* logits, bool bf16, int T, int E, int 
 // low-rank adapters (lora.hip): h [T, R] float32 holds the scaled inner sums
 hipError_t launch_lora_shrink(const uint16_t* x, int64_t ldx, int T, int K, const uint16_t* a, int L, int R,
                               const int32_t* adapter, const float* scale, float* h, hipStream_t st);
+// the same for few rows in one launch, no workspace
+bool lora_few(int T, int R);
+hipError_t launch_lora_few(const void* base, bool bf16, int64_t ldb, const uint16_t* x, int64_t ldx, int T, int K,
+                           int N, const uint16_t* a, const uint16_t* b, int L, int R, const int32_t* adapter,
+                           const float* scale, void* out, int64_t ldo, hipStream_t st);
 hipError_t launch_lora_add(const void* base, bool bf16, int64_t ldb, int T, int N, const uint16_t* b, int L, int R,
                            const int32_t* adapter, const float* h, void* out, int64_t ldo, hipStream_t st);
 
