@@ -25,7 +25,8 @@ extern "C" {
 
 #define I8H_LORA_MAX_RANK 256
 
-/* Device scratch of both calls, in bytes: the inner sums, T x R float32. */
+/* Device scratch of both calls, in bytes: the inner sums, T x R float32, in up
+ * to 8 slices of K. */
 size_t lora_workspace_size(int T, int R);
 
 /* out[t] = base[t] + delta[t]: adapters beside any projection, base being its

@@ -89,7 +89,7 @@ int moe_route_scored_permute(const void* logits, int logits_type, int T, int E, 
 
 size_t lora_workspace_size(int T, int R) {
   if (T <= 0 || R <= 0) return 0;
-  return round_up((size_t)T * R * sizeof(float), 256);
+  return round_up((size_t)i8h::lora_slices(T) * T * R * sizeof(float), 256);
 }
 
 int lora_add(const void* base, int base_type, int64_t ldb, const uint16_t* x, int64_t ldx, int T, int K, int N,
@@ -113,10 +113,11 @@ int lora_add(const void* base, int base_type, int64_t ldb, const uint16_t* x, in
     return from_hip(i8h::launch_lora_few(base, base_type == I8H_BF16, ldb, x, ldx, T, K, N, lora_a, lora_b, L, R,
                                          adapter, lora_scale, out, ldo, st));
   float* h = static_cast<float*>(workspace);
-  if (i8h::launch_lora_shrink(x, ldx, T, K, lora_a, L, R, adapter, lora_scale, h, st) != hipSuccess)
+  int slices = 1;
+  if (i8h::launch_lora_shrink(x, ldx, T, K, lora_a, L, R, adapter, lora_scale, h, &slices, st) != hipSuccess)
     return I8H_EHIP;
-  return from_hip(i8h::launch_lora_add(base, base_type == I8H_BF16, ldb, T, N, lora_b, L, R, adapter, h, out, ldo,
-                                       st));
+  return from_hip(i8h::launch_lora_add(base, base_type == I8H_BF16, ldb, T, N, lora_b, L, R, adapter, h, slices, out,
+                                       ldo, st));
 }
 
 int linear_i8f16_lora(const uint16_t* x, int T, int K, const int8_t* codes, const uint16_t* scales, int N,
@@ -135,9 +136,10 @@ int linear_i8f16_lora(const uint16_t* x, int T, int K, const int8_t* codes, cons
     return I8H_EINVAL;
   hipStream_t st = as_stream(stream);
   float* h = static_cast<float*>(workspace);
-  if (i8h::launch_lora_shrink(x, K, T, K, lora_a, L, R, adapter, lora_scale, h, st) != hipSuccess) return I8H_EHIP;
+  int slices = 1;
+  if (i8h::launch_lora_shrink(x, K, T, K, lora_a, L, R, adapter, lora_scale, h, &slices, st) != hipSuccess) return I8H_EHIP;
   if (i8h::launch_linear_i8f16(x, T, K, codes, scales, N, y, st) != hipSuccess) return I8H_EHIP;
-  return from_hip(i8h::launch_lora_add(y, false, N, T, N, lora_b, L, R, adapter, h, y, N, st));
+  return from_hip(i8h::launch_lora_add(y, false, N, T, N, lora_b, L, R, adapter, h, slices, y, N, st));
 }
 
 }  // extern "C"

@@ -127,16 +127,19 @@ hipError_t launch_route_scored(const void* logits, bool bf16, int T, int E, int 
                                int32_t* expert_off, int32_t* sorted_pairs, int32_t* pair_pos, void* ws,
                                hipStream_t st);
 
-// low-rank adapters (lora.hip): h [T, R] float32 holds the scaled inner sums
+// low-rank adapters (lora.hip): h [slices, T, R] float32 holds the scaled inner
+// sums of slices of K, at most lora_slices(T) of them
+int lora_slices(int T);
 hipError_t launch_lora_shrink(const uint16_t* x, int64_t ldx, int T, int K, const uint16_t* a, int L, int R,
-                              const int32_t* adapter, const float* scale, float* h, hipStream_t st);
+                              const int32_t* adapter, const float* scale, float* h, int* slices, hipStream_t st);
 // the same for few rows in one launch, no workspace
 bool lora_few(int T, int R);
 hipError_t launch_lora_few(const void* base, bool bf16, int64_t ldb, const uint16_t* x, int64_t ldx, int T, int K,
                            int N, const uint16_t* a, const uint16_t* b, int L, int R, const int32_t* adapter,
                            const float* scale, void* out, int64_t ldo, hipStream_t st);
 hipError_t launch_lora_add(const void* base, bool bf16, int64_t ldb, int T, int N, const uint16_t* b, int L, int R,
-                           const int32_t* adapter, const float* h, void* out, int64_t ldo, hipStream_t st);
+                           const int32_t* adapter, const float* h, int slices, void* out, int64_t ldo,
+                           hipStream_t st);
 
 // verification of drafted tokens (draft.hip)
 int draft_chunks(int B, int V);

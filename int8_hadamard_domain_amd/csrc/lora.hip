@@ -3,15 +3,18 @@
 //   out[t, n] = base[t, n] + sum_r B[l][n, r] h[t, r]
 //
 // Kernels
-//   k_lora_shrink  h: a workgroup owns 16 rows of the batch and goes through
-//                  the adapters they name; its eight waves split K
-//   k_lora_add     out: a wave owns 16 rows x 64 columns
+//   k_lora_few     few rows: both products in one launch, on the vector ALU
+//   k_lora_shrink  h, in slices of K
+//   k_lora_add     out
 //
-// Both run on v_mfma_f32_16x16x32_bf16 with a row of the batch per matrix row
-// (or column), so what an adapter holds reaches no row but its own: values of
-// rows that name another adapter are computed and dropped. h is float32; the
-// second product takes it as the sum of three bf16 values (8 significand bits
-// each, the split is exact), so nothing is rounded between the products.
+// The latter two run on v_mfma_f32_16x16x32_bf16 with a row of the batch per
+// matrix row (or column), so what an adapter holds reaches no row but its own:
+// values of rows that name another adapter are computed and dropped. h is
+// float32; the second product takes it as the sum of three bf16 values (8
+// significand bits each, the split is exact), so nothing is rounded between
+// the products.
+
+#include <algorithm>
 
 #include "common.hpp"
 #include "launch.hpp"
@@ -22,109 +25,130 @@ namespace i8h {
 
 namespace {
 
-constexpr int kShWaves = 8;                    // waves of the shrink kernel, each a share of K
+constexpr int kShWaves = 4;                    // the shrink kernel: rows and K of a stage
 constexpr int kShThreads = kWave * kShWaves;
+constexpr int kShRows = 64;
+constexpr int kShK = 256;
 constexpr int kFewWaves = 8;
 constexpr int kFewThreads = kWave * kFewWaves;
-constexpr int kAddWaves = 4;
-constexpr int kAddThreads = kWave * kAddWaves;
-constexpr int kAddTiles = 4;                   // 16-column tiles a wave
-constexpr int kAddCols = kAddWaves * kAddTiles * 16;
+constexpr int kAddThreads = 256;               // the add kernel: rows and columns of a step
+constexpr int kAddRows = 32;
+constexpr int kAddCols = 256;
 
-__device__ __forceinline__ bf16x8 load8(const uint16_t* p, bool live) {
-  u32x4 v = {0u, 0u, 0u, 0u};
-  if (live) v = *reinterpret_cast<const u32x4*>(p);
-  return __builtin_bit_cast(bf16x8, v);
-}
-
-// NG: 16-wide groups of R a workgroup computes; KI: 32-wide pieces of K a
-// wave's step. A load takes 64 contiguous bytes of a row (four lanes); the
-// next step's are issued before this one's products. Lanes whose row names
-// another adapter load the first row that names this one, and lanes past R the
-// last row of A: their sums are dropped.
-template <int NG, int KI>
+// h of 64 rows, 16 NG columns of R and a slice of K, for the adapters that the
+// rows name (every gridDim.z / rgroups-th of them, from its own on). Stages of
+// 256 of K go through LDS, whole lines a row, the next one's loads in flight
+// behind this one's products; a wave takes a quarter of a stage's K for all 64
+// rows, so that it reads each operand once, and the four waves' sums meet in
+// LDS. 16-byte piece p of a row lies at p ^ (row % 16): the fragment reads of
+// 16 rows take all banks. Rows that name another adapter keep what LDS held,
+// and lanes past R the last row of A: their sums are dropped.
+template <int NG>
 __global__ void __launch_bounds__(kShThreads)
 k_lora_shrink(const uint16_t* __restrict__ x, int64_t ldx, int T, int K, const uint16_t* __restrict__ a, int L, int R,
-              const int32_t* __restrict__ adapter, const float* __restrict__ scale, float* __restrict__ h) {
-  __shared__ f32x4 part[kShWaves][NG][kWave];
-  const int lane = threadIdx.x % kWave;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+              const int32_t* __restrict__ adapter, const float* __restrict__ scale, int rgroups,
+              float* __restrict__ h) {
+  constexpr int kPieces = kShK / 8;                          // of a row and stage
+  constexpr int kXL = kShRows * kPieces / kShThreads;        // loads a thread and stage
+  constexpr int kAL = 16 * NG * kPieces / kShThreads;
+  constexpr int kStageBytes = (kShRows + 16 * NG) * kShK * 2, kSumBytes = kShWaves * 4 * NG * kWave * 16;
+  __shared__ __align__(16) uint8_t sm[kStageBytes > kSumBytes ? kStageBytes : kSumBytes];
+  u32x4* xs = reinterpret_cast<u32x4*>(sm);                  // [row][piece]
+  u32x4* as = xs + kShRows * kPieces;
+  f32x4* sums = reinterpret_cast<f32x4*>(sm);                // [wave][tile][lane]
+  const int tid = threadIdx.x, lane = tid % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int c = lane % 16, kq = lane / 16;
-  const int64_t t0 = (int64_t)blockIdx.x * 16;
-  const int r0 = blockIdx.z * 16 * NG;
-  const int ad = lora_row_adapter(adapter, t0, T, L, c);
-  uint32_t left = lora_rows(ad >= 0);
-  int skip = blockIdx.y;
+  const int64_t t0 = (int64_t)blockIdx.x * kShRows;
+  const int r0 = (blockIdx.z % rgroups) * 16 * NG, every = gridDim.z / rgroups;
+  const int all = (K + kShK - 1) / kShK, slices = gridDim.y;
+  const int s0 = (int)((int64_t)all * blockIdx.y / slices), s1 = (int)((int64_t)all * (blockIdx.y + 1) / slices);
+  const int piece = tid % kPieces, row0 = tid / kPieces;     // a thread's rows: row0 + kShThreads / kPieces * j
+  constexpr int kRowStep = kShThreads / kPieces;
+  int ad = t0 + lane < T ? adapter[t0 + lane] : -1;          // lane: a row of the tile
+  ad = (uint32_t)ad < (uint32_t)L ? ad : -1;
+  uint64_t left = __ballot(ad >= 0);
+  int skip = blockIdx.z / rgroups;
   while (left != 0) {
-    const int first = __ffs(left) - 1;
-    const int l = __builtin_amdgcn_readlane(ad, first);
-    const uint32_t mine = lora_rows(ad == l);
+    const int l = __builtin_amdgcn_readlane(ad, __ffsll((unsigned long long)left) - 1);
+    const uint64_t mine = __ballot(ad == l);
     left &= ~mine;
     if (skip-- > 0) continue;
-    skip = gridDim.y - 1;
-    constexpr int kStep = 32 * KI;
-    const int steps = (K + kStep - 1) / kStep;
-    const uint16_t* xp = x + (t0 + (ad == l ? c : first)) * ldx + 8 * kq;
-    const uint16_t* ap[NG];
+    skip = every - 1;
+    const uint16_t* xp = x + (t0 + row0) * ldx + 8 * piece;
+    const uint16_t* ap = a + (size_t)l * R * K + 8 * piece;
+    u32x4 xr[kXL], ar[kAL];
+    const auto load = [&](int s) {
+      const bool in = kShK * s + 8 * piece < K;
 #pragma unroll
-    for (int g = 0; g < NG; ++g) ap[g] = a + ((size_t)l * R + min(r0 + 16 * g + c, R - 1)) * K + 8 * kq;
-    f32x4 acc[NG];
-    bf16x8 xv[2][KI], av[2][NG][KI];
+      for (int j = 0; j < kXL; ++j) {
+        xr[j] = {0u, 0u, 0u, 0u};
+        if (in && ((mine >> (row0 + kRowStep * j)) & 1))
+          xr[j] = *reinterpret_cast<const u32x4*>(xp + (int64_t)kRowStep * j * ldx + kShK * s);
+      }
 #pragma unroll
-    for (int g = 0; g < NG; ++g) acc[g] = {0.f, 0.f, 0.f, 0.f};
-    const auto load = [&](int to, int step) {
-      const int k0 = kStep * step;
-      if (k0 + kStep <= K) {
-#pragma unroll
-        for (int i = 0; i < KI; ++i) {
-          xv[to][i] = load8(xp + k0 + 32 * i, true);
-#pragma unroll
-          for (int g = 0; g < NG; ++g) av[to][g][i] = load8(ap[g] + k0 + 32 * i, true);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < KI; ++i) {
-          const bool in = k0 + 32 * i + 8 * kq < K;
-          xv[to][i] = load8(xp + k0 + 32 * i, in);
-#pragma unroll
-          for (int g = 0; g < NG; ++g) av[to][g][i] = load8(ap[g] + k0 + 32 * i, in);
-        }
+      for (int j = 0; j < kAL; ++j) {
+        const int r = min(r0 + row0 + kRowStep * j, R - 1);
+        ar[j] = {0u, 0u, 0u, 0u};
+        if (in) ar[j] = *reinterpret_cast<const u32x4*>(ap + (size_t)r * K + kShK * s);
       }
     };
-    const auto multiply = [&](int from) {
+    f32x4 acc[4][NG];
 #pragma unroll
-      for (int i = 0; i < KI; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int g = 0; g < NG; ++g)
-          acc[g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[from][i], av[from][g][i], acc[g], 0, 0, 0);
-    };
-    int s = wave;
-    if (s < steps) load(0, s);
-    while (s < steps) {
-      if (s + kShWaves < steps) load(1, s + kShWaves);
-      multiply(0);
-      s += kShWaves;
-      if (s >= steps) break;
-      if (s + kShWaves < steps) load(0, s + kShWaves);
-      multiply(1);
-      s += kShWaves;
+      for (int g = 0; g < NG; ++g) acc[i][g] = {0.f, 0.f, 0.f, 0.f};
+    load(s0);
+    for (int s = s0; s < s1; ++s) {
+#pragma unroll
+      for (int j = 0; j < kXL; ++j) {
+        const int r = row0 + kRowStep * j;
+        xs[r * kPieces + (piece ^ (r % 16))] = xr[j];
+      }
+#pragma unroll
+      for (int j = 0; j < kAL; ++j) {
+        const int r = row0 + kRowStep * j;
+        as[r * kPieces + (piece ^ (r % 16))] = ar[j];
+      }
+      __syncthreads();
+      if (s + 1 < s1) load(s + 1);
+#pragma unroll
+      for (int q = 0; q < kPieces / 4 / kShWaves; ++q) {
+        const int p = 4 * (kPieces / 4 / kShWaves * wave + q) + kq;
+        bf16x8 av[NG];
+#pragma unroll
+        for (int g = 0; g < NG; ++g) av[g] = __builtin_bit_cast(bf16x8, as[(16 * g + c) * kPieces + (p ^ c)]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bf16x8 xv = __builtin_bit_cast(bf16x8, xs[(16 * i + c) * kPieces + (p ^ c)]);
+#pragma unroll
+          for (int g = 0; g < NG; ++g) acc[i][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, av[g], acc[i][g], 0, 0, 0);
+        }
+      }
+      __syncthreads();
     }
 #pragma unroll
-    for (int g = 0; g < NG; ++g) part[wave][g][lane] = acc[g];
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int g = 0; g < NG; ++g) sums[(wave * 4 * NG + i * NG + g) * kWave + lane] = acc[i][g];
     __syncthreads();
-    if (wave < NG) {
-      f32x4 sum = part[0][wave][lane];
+    // wave w adds up the tiles of rows 16 w .. 16 w + 15
+    const float f = scale[l];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      f32x4 sum = sums[(wave * NG + g) * kWave + lane];
 #pragma unroll
       for (int w = 1; w < kShWaves; ++w) {
-        const f32x4 o = part[w][wave][lane];
+        const f32x4 o = sums[(w * 4 * NG + wave * NG + g) * kWave + lane];
 #pragma unroll
         for (int i = 0; i < 4; ++i) sum[i] += o[i];
       }
-      const int r = r0 + 16 * wave + c;
-      const float f = scale[l];
+      const int r = r0 + 16 * g + c;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (r < R && ((mine >> (4 * kq + i)) & 1)) h[(t0 + 4 * kq + i) * R + r] = f * sum[i];
+      for (int i = 0; i < 4; ++i) {
+        const int row = 16 * wave + 4 * kq + i;
+        if (r < R && ((mine >> row) & 1)) h[((int64_t)blockIdx.y * T + t0 + row) * R + r] = f * sum[i];
+      }
     }
     __syncthreads();
   }
@@ -208,98 +232,144 @@ k_lora_few(const void* base, int64_t ldb, const uint16_t* __restrict__ x, int64_
   }
 }
 
+// Four elements of a row of base or out, in float32 or as packed bf16.
 template <bool BF16>
-__global__ void __launch_bounds__(kAddThreads)
-k_lora_add(const void* base, int64_t ldb, int T, int N, const uint16_t* __restrict__ b, int L, int R,
-           const int32_t* __restrict__ adapter, const float* __restrict__ h, void* out, int64_t ldo, bool vec) {
-  const int lane = threadIdx.x % kWave;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int c = lane % 16, kq = lane / 16;
-  const int64_t t0 = (int64_t)blockIdx.x * 16;
-  const int n0 = blockIdx.y * kAddCols + wave * kAddTiles * 16;
-  if (n0 >= N) return;
-  const int ad = lora_row_adapter(adapter, t0, T, L, c);
-  // the lane's row t0 + c, columns n0 + 16 j + 4 kq ..: base is on its way before the products
-  const bool row = t0 + c < T;
-  const int n1 = n0 + 4 * kq;
-  f32x4 v[kAddTiles];
-  u32x2 w[kAddTiles];
-#pragma unroll
-  for (int j = 0; j < kAddTiles; ++j) {
-    const int n = n1 + 16 * j;
-    v[j] = {0.f, 0.f, 0.f, 0.f};
-    w[j] = {0u, 0u};
-    if (!row) continue;
+struct Quad {
+  f32x4 f;
+  u32x2 b;
+  __device__ __forceinline__ void load(const void* p, int64_t at, int n, int N, bool vec) {
     if constexpr (BF16) {
-      const uint16_t* s = static_cast<const uint16_t*>(base) + (t0 + c) * ldb + n;
+      const uint16_t* s = static_cast<const uint16_t*>(p) + at;
       if (vec && n + 3 < N) {
-        w[j] = *reinterpret_cast<const u32x2*>(s);
+        b = *reinterpret_cast<const u32x2*>(s);
       } else {
         uint32_t e[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) e[i] = n + i < N ? s[i] : 0u;
-        w[j] = {e[0] | e[1] << 16, e[2] | e[3] << 16};
+        b = {e[0] | e[1] << 16, e[2] | e[3] << 16};
       }
     } else {
-      const float* s = static_cast<const float*>(base) + (t0 + c) * ldb + n;
+      const float* s = static_cast<const float*>(p) + at;
       if (vec && n + 3 < N) {
-        v[j] = *reinterpret_cast<const f32x4*>(s);
+        f = *reinterpret_cast<const f32x4*>(s);
       } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[j][i] = n + i < N ? s[i] : 0.0f;
+        for (int i = 0; i < 4; ++i) f[i] = n + i < N ? s[i] : 0.0f;
       }
     }
   }
-  f32x4 acc[kAddTiles];
-#pragma unroll
-  for (int j = 0; j < kAddTiles; ++j) acc[j] = {0.f, 0.f, 0.f, 0.f};
-  lora_expand<kAddTiles>(b, N, R, h, t0, T, n0, ad, lane, acc);
-  if (!row) return;
-#pragma unroll
-  for (int j = 0; j < kAddTiles; ++j) {
-    const int n = n1 + 16 * j;
+  __device__ __forceinline__ void add(const f32x4& d) {
     if constexpr (BF16) {
-      uint16_t* d = static_cast<uint16_t*>(out) + (t0 + c) * ldo + n;
-      if (ad >= 0)
-        w[j] = {pack_bf16x2(bf16_lo(w[j][0]) + acc[j][0], bf16_hi(w[j][0]) + acc[j][1]),
-                pack_bf16x2(bf16_lo(w[j][1]) + acc[j][2], bf16_hi(w[j][1]) + acc[j][3])};
+      b = {pack_bf16x2(bf16_lo(b[0]) + d[0], bf16_hi(b[0]) + d[1]),
+           pack_bf16x2(bf16_lo(b[1]) + d[2], bf16_hi(b[1]) + d[3])};
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] += d[i];
+    }
+  }
+  __device__ __forceinline__ void store(void* p, int64_t at, int n, int N, bool vec) const {
+    if constexpr (BF16) {
+      uint16_t* d = static_cast<uint16_t*>(p) + at;
       if (vec && n + 3 < N) {
-        *reinterpret_cast<u32x2*>(d) = w[j];
+        *reinterpret_cast<u32x2*>(d) = b;
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (n + i < N) d[i] = (uint16_t)(w[j][i / 2] >> (16 * (i % 2)));
+          if (n + i < N) d[i] = (uint16_t)(b[i / 2] >> (16 * (i % 2)));
       }
     } else {
-      float* d = static_cast<float*>(out) + (t0 + c) * ldo + n;
-      if (ad >= 0) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[j][i] += acc[j][i];
-      }
+      float* d = static_cast<float*>(p) + at;
       if (vec && n + 3 < N) {
-        *reinterpret_cast<f32x4*>(d) = v[j];
+        *reinterpret_cast<f32x4*>(d) = f;
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (n + i < N) d[i] = v[j][i];
+          if (n + i < N) d[i] = f[i];
       }
     }
+  }
+};
+
+// out of 32 rows and `steps` times 256 columns: the slices of h are added up
+// once a workgroup and lie in LDS in three bf16 parts; a wave goes through its
+// 64 columns of each step with the next step's base on its way.
+template <bool BF16>
+__global__ void __launch_bounds__(kAddThreads)
+k_lora_add(const void* base, int64_t ldb, int T, int N, const uint16_t* __restrict__ b, int L, int R,
+           const int32_t* __restrict__ adapter, const float* __restrict__ h, int slices, int steps, void* out,
+           int64_t ldo, bool vec) {
+  extern __shared__ __align__(16) uint8_t sm[];
+  const int tid = threadIdx.x, lane = tid % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int c = lane % 16, kq = lane / 16;
+  const int64_t t0 = (int64_t)blockIdx.x * kAddRows;
+  int ad[2];
+  ad[0] = lora_row_adapter(adapter, t0, T, L, c);
+  ad[1] = lora_row_adapter(adapter, t0, T, L, 16 + c);
+  int n0 = blockIdx.y * steps * kAddCols + 64 * wave;
+  Quad<BF16> now[2][4], next[2][4];
+  const auto load = [&](Quad<BF16> (&q)[2][4], int n1) {
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (t0 + 16 * m + c < T)
+          q[m][j].load(base, (t0 + 16 * m + c) * ldb + n1 + 16 * j + 4 * kq, n1 + 16 * j + 4 * kq, N, vec);
+  };
+  load(next, n0);
+  const int ld = lora_split_stride(R);
+  lora_split_rows<kAddRows, kAddThreads>(h, slices, T, R, adapter, L, t0, sm, ld, tid);
+  __syncthreads();
+  const uint32_t rows[2] = {lora_rows(ad[0] >= 0), lora_rows(ad[1] >= 0)};
+  for (int s = 0; s < steps && n0 < N; ++s, n0 += kAddCols) {
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) now[m][j] = next[m][j];
+    if (s + 1 < steps && n0 + kAddCols < N) load(next, n0 + kAddCols);
+    uint32_t left[2] = {rows[0], rows[1]};
+    while ((left[0] | left[1]) != 0) {
+      const int l = left[0] != 0 ? __builtin_amdgcn_readlane(ad[0], __ffs(left[0]) - 1)
+                                 : __builtin_amdgcn_readlane(ad[1], __ffs(left[1]) - 1);
+      left[0] &= ~lora_rows(ad[0] == l);
+      left[1] &= ~lora_rows(ad[1] == l);
+      f32x4 d[2][4];
+      lora_products<2, 4>(b + (size_t)l * N * R, N, R, sm, ld, n0, lane, d);
+      // the rows of other adapters keep what they have, whatever this one holds
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+        if (ad[m] == l) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) now[m][j].add(d[m][j]);
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+      if (t0 + 16 * m + c < T) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          now[m][j].store(out, (t0 + 16 * m + c) * ldo + n0 + 16 * j + 4 * kq, n0 + 16 * j + 4 * kq, N, vec);
+      }
   }
 }
 
 }  // namespace
 
+int lora_slices(int T) { return std::max(1, std::min(8, 256 / ((T - 1) / kShRows + 1))); }
+
 hipError_t launch_lora_shrink(const uint16_t* x, int64_t ldx, int T, int K, const uint16_t* a, int L, int R,
-                              const int32_t* adapter, const float* scale, float* h, hipStream_t st) {
-  // a workgroup per 16 rows and adapter among them while rows are few, else one that goes through its rows' adapters
-  const int y = T <= 1024 ? min(min(T, 16), L) : 1;
-  if (R <= 16)
-    k_lora_shrink<1, 4><<<dim3(cdiv(T, 16), y, 1), kShThreads, 0, st>>>(x, ldx, T, K, a, L, R, adapter, scale, h);
-  else if (R <= 32)
-    k_lora_shrink<2, 4><<<dim3(cdiv(T, 16), y, 1), kShThreads, 0, st>>>(x, ldx, T, K, a, L, R, adapter, scale, h);
-  else
-    k_lora_shrink<4, 2><<<dim3(cdiv(T, 16), y, cdiv(R, 64)), kShThreads, 0, st>>>(x, ldx, T, K, a, L, R, adapter, scale,
-                                                                              h);
+                              const int32_t* adapter, const float* scale, float* h, int* slices, hipStream_t st) {
+  *slices = std::min(lora_slices(T), cdiv(K, kShK));
+  // while rows are few, workgroups of their own for up to 16 of a tile's adapters
+  const int spread = T <= 1024 ? std::min({16, T, L}) : 1;
+  const int rgroups = R <= 64 ? 1 : cdiv(R, 64);
+  const dim3 grid(cdiv(T, kShRows), *slices, rgroups * spread);
+#define I8H_SHRINK(NG) \
+  k_lora_shrink<NG><<<grid, kShThreads, 0, st>>>(x, ldx, T, K, a, L, R, adapter, scale, rgroups, h)
+  if (R <= 16) I8H_SHRINK(1);
+  else if (R <= 32) I8H_SHRINK(2);
+  else I8H_SHRINK(4);
+#undef I8H_SHRINK
   return hipGetLastError();
 }
 
@@ -325,13 +395,21 @@ hipError_t launch_lora_few(const void* base, bool bf16, int64_t ldb, const uint1
 }
 
 hipError_t launch_lora_add(const void* base, bool bf16, int64_t ldb, int T, int N, const uint16_t* b, int L, int R,
-                           const int32_t* adapter, const float* h, void* out, int64_t ldo, hipStream_t st) {
+                           const int32_t* adapter, const float* h, int slices, void* out, int64_t ldo,
+                           hipStream_t st) {
   const uintptr_t unit = bf16 ? 8 : 16;   // four elements
   const bool vec = reinterpret_cast<uintptr_t>(base) % unit == 0 && reinterpret_cast<uintptr_t>(out) % unit == 0 &&
                    ldb % 4 == 0 && ldo % 4 == 0;
-  const dim3 grid(cdiv(T, 16), cdiv(N, kAddCols));
-  if (bf16) k_lora_add<true><<<grid, kAddThreads, 0, st>>>(base, ldb, T, N, b, L, R, adapter, h, out, ldo, vec);
-  else k_lora_add<false><<<grid, kAddThreads, 0, st>>>(base, ldb, T, N, b, L, R, adapter, h, out, ldo, vec);
+  const int tiles = cdiv(T, kAddRows), cols = cdiv(N, kAddCols);
+  const int steps = (int)std::max<int64_t>(1, std::min<int64_t>(4, (int64_t)tiles * cols / 512));
+  const dim3 grid(tiles, cdiv(cols, steps));
+  const size_t lds = (size_t)3 * kAddRows * lora_split_stride(R);
+  if (bf16)
+    k_lora_add<true><<<grid, kAddThreads, lds, st>>>(base, ldb, T, N, b, L, R, adapter, h, slices, steps, out, ldo,
+                                                     vec);
+  else
+    k_lora_add<false><<<grid, kAddThreads, lds, st>>>(base, ldb, T, N, b, L, R, adapter, h, slices, steps, out, ldo,
+                                                      vec);
   return hipGetLastError();
 }
 

@@ -45,46 +45,67 @@ __device__ __forceinline__ Bf16Split split3(const float (&v)[8]) {
   return s;
 }
 
-// acc[j] += the adapters' part of a tile: row c of the lane, columns
-// n0 + 16 j + 4 (lane / 16) .. + 3, for each adapter the rows name in turn.
-template <int TILES>
-__device__ __forceinline__ void lora_expand(const uint16_t* __restrict__ b, int N, int R, const float* __restrict__ h,
-                                            int64_t t0, int T, int n0, int ad, int lane, f32x4 (&acc)[TILES]) {
+// Bytes between rows of a part of h in LDS: 16 bytes of padding, so that the
+// fragment reads of 16 rows spread over the banks.
+__host__ __device__ constexpr inline int lora_split_stride(int R) { return 2 * R + 16; }
+
+// The inner sums of ROWS rows from t0 on, added up over the slices of K, in
+// three bf16 parts: part p of row r at sm + (p ROWS + r) ld. Rows without an
+// adapter are zero. By a workgroup of THREADS threads; a barrier must follow.
+template <int ROWS, int THREADS>
+__device__ __forceinline__ void lora_split_rows(const float* __restrict__ h, int slices, int T, int R,
+                                                const int32_t* __restrict__ adapter, int L, int64_t t0, uint8_t* sm,
+                                                int ld, int tid) {
+  for (int i = tid; i < ROWS * (R / 8); i += THREADS) {
+    const int row = i / (R / 8), r = 8 * (i % (R / 8));
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (lora_row_adapter(adapter, t0, T, L, row) >= 0) {
+      for (int s = 0; s < slices; ++s) {
+        const f32x4* p = reinterpret_cast<const f32x4*>(h + ((int64_t)s * T + t0 + row) * R + r);
+        const f32x4 u = p[0], w = p[1];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          v[j] += u[j];
+          v[4 + j] += w[j];
+        }
+      }
+    }
+    const Bf16Split q = split3(v);
+#pragma unroll
+    for (int p = 0; p < 3; ++p) *reinterpret_cast<bf16x8*>(sm + (p * ROWS + row) * ld + 2 * r) = q.p[p];
+  }
+}
+
+// d[m][j] = an adapter's product for the 16 MT rows in LDS (lora_split_rows)
+// and columns n0 + 16 j ..: the lane gets row 16 m + lane % 16, columns
+// n0 + 16 j + 4 (lane / 16) .. + 3. b: the adapter's B.
+template <int MT, int NT>
+__device__ __forceinline__ void lora_products(const uint16_t* __restrict__ b, int N, int R, const uint8_t* sm, int ld,
+                                              int n0, int lane, f32x4 (&d)[MT][NT]) {
   const int c = lane % 16, kq = lane / 16;
-  uint32_t left = lora_rows(ad >= 0);
-  while (left != 0) {
-    const int l = __builtin_amdgcn_readlane(ad, __ffs(left) - 1);
-    left &= ~lora_rows(ad == l);
-    const uint16_t* bl = b + (size_t)l * N * R;
-    f32x4 d[TILES];
 #pragma unroll
-    for (int j = 0; j < TILES; ++j) d[j] = {0.f, 0.f, 0.f, 0.f};
-    for (int r0 = 0; r0 < R; r0 += 32) {
-      const int r = r0 + 8 * kq;
-      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (ad == l && r < R) {
-        const float* hr = h + (t0 + c) * R + r;
+  for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = hr[i];
-      }
-      const Bf16Split s = split3(v);
+    for (int j = 0; j < NT; ++j) d[m][j] = {0.f, 0.f, 0.f, 0.f};
+  for (int r0 = 0; r0 < R; r0 += 32) {
+    const int r = r0 + 8 * kq;
+    bf16x8 bv[NT];
 #pragma unroll
-      for (int j = 0; j < TILES; ++j) {
-        const int n = n0 + 16 * j + c;
-        u32x4 w = {0u, 0u, 0u, 0u};
-        if (n < N && r < R) w = *reinterpret_cast<const u32x4*>(bl + (size_t)n * R + r);
-        const bf16x8 bv = __builtin_bit_cast(bf16x8, w);
-#pragma unroll
-        for (int p = 0; p < 3; ++p) d[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bv, s.p[p], d[j], 0, 0, 0);
-      }
+    for (int j = 0; j < NT; ++j) {
+      const int n = n0 + 16 * j + c;
+      u32x4 w = {0u, 0u, 0u, 0u};
+      if (n < N && r < R) w = *reinterpret_cast<const u32x4*>(b + (size_t)n * R + r);
+      bv[j] = __builtin_bit_cast(bf16x8, w);
     }
-    // the rows of other adapters keep what they have, whatever this one holds
-    if (ad == l) {
 #pragma unroll
-      for (int j = 0; j < TILES; ++j)
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[j][i] += d[j][i];
-    }
+      for (int p = 0; p < 3; ++p) {
+        bf16x8 hv = __builtin_bit_cast(bf16x8, u32x4{0u, 0u, 0u, 0u});
+        if (r < R) hv = *reinterpret_cast<const bf16x8*>(sm + (p * 16 * MT + 16 * m + c) * ld + 2 * r);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) d[m][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bv[j], hv, d[m][j], 0, 0, 0);
+      }
   }
 }
 
