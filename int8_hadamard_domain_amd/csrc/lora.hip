@@ -15,6 +15,7 @@
 // the products.
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.hpp"
 #include "launch.hpp"
@@ -28,30 +29,44 @@ namespace {
 constexpr int kShWaves = 4;                    // the shrink kernel: rows and K of a stage
 constexpr int kShThreads = kWave * kShWaves;
 constexpr int kShRows = 64;
-constexpr int kShK = 256;
+constexpr int kShK = 128;
 constexpr int kFewWaves = 8;
 constexpr int kFewThreads = kWave * kFewWaves;
 constexpr int kAddThreads = 256;               // the add kernel: rows and columns of a step
 constexpr int kAddRows = 32;
 constexpr int kAddCols = 256;
 
+// Workgroups are dealt to the XCDs in turn: the i-th of n (a multiple of their
+// number) takes place i % kXcds * n / kXcds + i / kXcds, so that each XCD's L2
+// sees neighbouring ones.
+constexpr int kXcds = 8;
+__device__ __forceinline__ int xcd_run(int i, int n) { return i % kXcds * (n / kXcds) + i / kXcds; }
+
+// 16 bytes at a uniform address and a lane's byte offset (32 bits: the entry
+// points bound row distances and K).
+__device__ __forceinline__ u32x4 load16(const void* p, uint32_t off) {
+  return *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(p) + off);
+}
+
 // h of 64 rows, 16 NG columns of R and a slice of K, for the adapters that the
-// rows name (every gridDim.z / rgroups-th of them, from its own on). Stages of
-// 256 of K go through LDS, whole lines a row, the next one's loads in flight
+// rows name (each `every`-th of them, from its own on). Stages of
+// 128 of K go through LDS, whole lines a row, the next two's loads in flight
 // behind this one's products; a wave takes a quarter of a stage's K for all 64
 // rows, so that it reads each operand once, and the four waves' sums meet in
 // LDS. 16-byte piece p of a row lies at p ^ (row % 16): the fragment reads of
 // 16 rows take all banks. Rows that name another adapter keep what LDS held,
-// and lanes past R the last row of A: their sums are dropped.
+// and lanes past R the last row of A: their sums are dropped. The tiles start
+// at different stages: rows lie a power of two apart more often than not, and
+// all tiles at the same piece of K would ask the same L2 channels.
 template <int NG>
-__global__ void __launch_bounds__(kShThreads)
+__global__ void __launch_bounds__(kShThreads, 2)
 k_lora_shrink(const uint16_t* __restrict__ x, int64_t ldx, int T, int K, const uint16_t* __restrict__ a, int L, int R,
-              const int32_t* __restrict__ adapter, const float* __restrict__ scale, int rgroups,
-              float* __restrict__ h) {
+              const int32_t* __restrict__ adapter, const float* __restrict__ scale, int slices, int rgroups, int every,
+              int wgs, float* __restrict__ h) {
   constexpr int kPieces = kShK / 8;                          // of a row and stage
   constexpr int kXL = kShRows * kPieces / kShThreads;        // loads a thread and stage
   constexpr int kAL = 16 * NG * kPieces / kShThreads;
-  constexpr int kStageBytes = (kShRows + 16 * NG) * kShK * 2, kSumBytes = kShWaves * 4 * NG * kWave * 16;
+  constexpr int kStageBytes = (kShRows + 16 * NG) * kShK * 2, kSumBytes = kShWaves * 2 * NG * kWave * 16;
   __shared__ __align__(16) uint8_t sm[kStageBytes > kSumBytes ? kStageBytes : kSumBytes];
   u32x4* xs = reinterpret_cast<u32x4*>(sm);                  // [row][piece]
   u32x4* as = xs + kShRows * kPieces;
@@ -59,38 +74,47 @@ k_lora_shrink(const uint16_t* __restrict__ x, int64_t ldx, int T, int K, const u
   const int tid = threadIdx.x, lane = tid % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int c = lane % 16, kq = lane / 16;
-  const int64_t t0 = (int64_t)blockIdx.x * kShRows;
-  const int r0 = (blockIdx.z % rgroups) * 16 * NG, every = gridDim.z / rgroups;
-  const int all = (K + kShK - 1) / kShK, slices = gridDim.y;
-  const int s0 = (int)((int64_t)all * blockIdx.y / slices), s1 = (int)((int64_t)all * (blockIdx.y + 1) / slices);
+  // the workgroup's tile, slice, group of R and first adapter
+  int wg = xcd_run(blockIdx.x, gridDim.x);
+  if (wg >= wgs) return;
+  const int slice = wg % slices;
+  wg /= slices;
+  const int r0 = wg % rgroups * 16 * NG;
+  wg /= rgroups;
+  int skip = wg % every;
+  const int tile = wg / every;
+  const int64_t t0 = (int64_t)tile * kShRows;
+  const int all = (K + kShK - 1) / kShK;
+  const int s0 = (int)((int64_t)all * slice / slices), stages = (int)((int64_t)all * (slice + 1) / slices) - s0;
+  const int turn = tile % stages;
   const int piece = tid % kPieces, row0 = tid / kPieces;     // a thread's rows: row0 + kShThreads / kPieces * j
   constexpr int kRowStep = kShThreads / kPieces;
+  const uint16_t* xt = x + t0 * ldx;
   int ad = t0 + lane < T ? adapter[t0 + lane] : -1;          // lane: a row of the tile
   ad = (uint32_t)ad < (uint32_t)L ? ad : -1;
   uint64_t left = __ballot(ad >= 0);
-  int skip = blockIdx.z / rgroups;
   while (left != 0) {
     const int l = __builtin_amdgcn_readlane(ad, __ffsll((unsigned long long)left) - 1);
     const uint64_t mine = __ballot(ad == l);
     left &= ~mine;
     if (skip-- > 0) continue;
     skip = every - 1;
-    const uint16_t* xp = x + (t0 + row0) * ldx + 8 * piece;
-    const uint16_t* ap = a + (size_t)l * R * K + 8 * piece;
-    u32x4 xr[kXL], ar[kAL];
-    const auto load = [&](int s) {
+    const uint16_t* al = a + (size_t)l * R * K;
+    u32x4 xr[2][kXL], ar[2][kAL];
+    const auto load = [&](int to, int i) {
+      const int s = s0 + (i + turn < stages ? i + turn : i + turn - stages);
       const bool in = kShK * s + 8 * piece < K;
 #pragma unroll
       for (int j = 0; j < kXL; ++j) {
-        xr[j] = {0u, 0u, 0u, 0u};
+        xr[to][j] = {0u, 0u, 0u, 0u};
         if (in && ((mine >> (row0 + kRowStep * j)) & 1))
-          xr[j] = *reinterpret_cast<const u32x4*>(xp + (int64_t)kRowStep * j * ldx + kShK * s);
+          xr[to][j] = load16(xt + kShK * s, 2u * ((uint32_t)(row0 + kRowStep * j) * (uint32_t)ldx + 8u * piece));
       }
 #pragma unroll
       for (int j = 0; j < kAL; ++j) {
         const int r = min(r0 + row0 + kRowStep * j, R - 1);
-        ar[j] = {0u, 0u, 0u, 0u};
-        if (in) ar[j] = *reinterpret_cast<const u32x4*>(ap + (size_t)r * K + kShK * s);
+        ar[to][j] = {0u, 0u, 0u, 0u};
+        if (in) ar[to][j] = load16(al + kShK * s, 2u * ((uint32_t)r * (uint32_t)K + 8u * piece));
       }
     };
     f32x4 acc[4][NG];
@@ -98,20 +122,19 @@ k_lora_shrink(const uint16_t* __restrict__ x, int64_t ldx, int T, int K, const u
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int g = 0; g < NG; ++g) acc[i][g] = {0.f, 0.f, 0.f, 0.f};
-    load(s0);
-    for (int s = s0; s < s1; ++s) {
+    const auto stage = [&](int from, int s) {
 #pragma unroll
       for (int j = 0; j < kXL; ++j) {
         const int r = row0 + kRowStep * j;
-        xs[r * kPieces + (piece ^ (r % 16))] = xr[j];
+        xs[r * kPieces + (piece ^ (r % 16))] = xr[from][j];
       }
 #pragma unroll
       for (int j = 0; j < kAL; ++j) {
         const int r = row0 + kRowStep * j;
-        as[r * kPieces + (piece ^ (r % 16))] = ar[j];
+        as[r * kPieces + (piece ^ (r % 16))] = ar[from][j];
       }
       __syncthreads();
-      if (s + 1 < s1) load(s + 1);
+      if (s + 2 < stages) load(from, s + 2);
 #pragma unroll
       for (int q = 0; q < kPieces / 4 / kShWaves; ++q) {
         const int p = 4 * (kPieces / 4 / kShWaves * wave + q) + kq;
@@ -126,31 +149,39 @@ k_lora_shrink(const uint16_t* __restrict__ x, int64_t ldx, int T, int K, const u
         }
       }
       __syncthreads();
+    };
+    load(0, 0);
+    if (stages > 1) load(1, 1);
+    for (int s = 0; s < stages; s += 2) {
+      stage(0, s);
+      if (s + 1 < stages) stage(1, s + 1);
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int g = 0; g < NG; ++g) sums[(wave * 4 * NG + i * NG + g) * kWave + lane] = acc[i][g];
-    __syncthreads();
-    // wave w adds up the tiles of rows 16 w .. 16 w + 15
+    // the waves' sums, 32 rows at a time
     const float f = scale[l];
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      f32x4 sum = sums[(wave * NG + g) * kWave + lane];
+    for (int half = 0; half < 2; ++half) {
 #pragma unroll
-      for (int w = 1; w < kShWaves; ++w) {
-        const f32x4 o = sums[(w * 4 * NG + wave * NG + g) * kWave + lane];
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sum[i] += o[i];
+        for (int g = 0; g < NG; ++g) sums[((wave * 2 + i) * NG + g) * kWave + lane] = acc[2 * half + i][g];
+      __syncthreads();
+      for (int tile = wave; tile < 2 * NG; tile += kShWaves) {
+        f32x4 sum = sums[tile * kWave + lane];
+#pragma unroll
+        for (int w = 1; w < kShWaves; ++w) {
+          const f32x4 o = sums[(w * 2 * NG + tile) * kWave + lane];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sum[i] += o[i];
+        }
+        const int r = r0 + 16 * (tile % NG) + c;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = 16 * (2 * half + tile / NG) + 4 * kq + i;
+          if (r < R && ((mine >> row) & 1)) h[((int64_t)slice * T + t0 + row) * R + r] = f * sum[i];
+        }
       }
-      const int r = r0 + 16 * g + c;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = 16 * wave + 4 * kq + i;
-        if (r < R && ((mine >> row) & 1)) h[((int64_t)blockIdx.y * T + t0 + row) * R + r] = f * sum[i];
-      }
+      __syncthreads();
     }
-    __syncthreads();
   }
 }
 
@@ -232,59 +263,75 @@ k_lora_few(const void* base, int64_t ldb, const uint16_t* __restrict__ x, int64_
   }
 }
 
-// Four elements of a row of base or out, in float32 or as packed bf16.
+// Eight elements of a row of base or out that a lane holds: in float32 those
+// from n and from n + 16 on, four each (the four lanes of a row load 64
+// contiguous bytes; eight neighbours a lane would load 16 of every 32 bytes,
+// four times the accesses), as packed bf16 the eight from n on. FULL: all there
+// and aligned to 16 bytes.
 template <bool BF16>
-struct Quad {
-  f32x4 f;
-  u32x2 b;
-  __device__ __forceinline__ void load(const void* p, int64_t at, int n, int N, bool vec) {
+struct Eight {
+  f32x4 f[2];
+  u32x4 b;
+  template <bool FULL>
+  __device__ __forceinline__ void load(const void* p, uint32_t at, int n, int N) {
     if constexpr (BF16) {
       const uint16_t* s = static_cast<const uint16_t*>(p) + at;
-      if (vec && n + 3 < N) {
-        b = *reinterpret_cast<const u32x2*>(s);
-      } else {
-        uint32_t e[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) e[i] = n + i < N ? s[i] : 0u;
-        b = {e[0] | e[1] << 16, e[2] | e[3] << 16};
-      }
-    } else {
-      const float* s = static_cast<const float*>(p) + at;
-      if (vec && n + 3 < N) {
-        f = *reinterpret_cast<const f32x4*>(s);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = n + i < N ? s[i] : 0.0f;
-      }
-    }
-  }
-  __device__ __forceinline__ void add(const f32x4& d) {
-    if constexpr (BF16) {
-      b = {pack_bf16x2(bf16_lo(b[0]) + d[0], bf16_hi(b[0]) + d[1]),
-           pack_bf16x2(bf16_lo(b[1]) + d[2], bf16_hi(b[1]) + d[3])};
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) f[i] += d[i];
-    }
-  }
-  __device__ __forceinline__ void store(void* p, int64_t at, int n, int N, bool vec) const {
-    if constexpr (BF16) {
-      uint16_t* d = static_cast<uint16_t*>(p) + at;
-      if (vec && n + 3 < N) {
-        *reinterpret_cast<u32x2*>(d) = b;
+      if constexpr (FULL) {
+        b = *reinterpret_cast<const u32x4*>(s);
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
+          b[i] = (n + 2 * i < N ? (uint32_t)s[2 * i] : 0u) | (n + 2 * i + 1 < N ? (uint32_t)s[2 * i + 1] << 16 : 0u);
+      }
+    } else {
+      const float* s = static_cast<const float*>(p) + at;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        if constexpr (FULL) {
+          f[q] = *reinterpret_cast<const f32x4*>(s + 16 * q);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) f[q][i] = n + 16 * q + i < N ? s[16 * q + i] : 0.0f;
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void add(const f32x4& d0, const f32x4& d1) {
+    if constexpr (BF16) {
+      b = {pack_bf16x2(bf16_lo(b[0]) + d0[0], bf16_hi(b[0]) + d0[1]),
+           pack_bf16x2(bf16_lo(b[1]) + d0[2], bf16_hi(b[1]) + d0[3]),
+           pack_bf16x2(bf16_lo(b[2]) + d1[0], bf16_hi(b[2]) + d1[1]),
+           pack_bf16x2(bf16_lo(b[3]) + d1[2], bf16_hi(b[3]) + d1[3])};
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f[0][i] += d0[i];
+        f[1][i] += d1[i];
+      }
+    }
+  }
+  template <bool FULL>
+  __device__ __forceinline__ void store(void* p, uint32_t at, int n, int N) const {
+    if constexpr (BF16) {
+      uint16_t* d = static_cast<uint16_t*>(p) + at;
+      if constexpr (FULL) {
+        *reinterpret_cast<u32x4*>(d) = b;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
           if (n + i < N) d[i] = (uint16_t)(b[i / 2] >> (16 * (i % 2)));
       }
     } else {
       float* d = static_cast<float*>(p) + at;
-      if (vec && n + 3 < N) {
-        *reinterpret_cast<f32x4*>(d) = f;
-      } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (n + i < N) d[i] = f[i];
+      for (int q = 0; q < 2; ++q) {
+        if constexpr (FULL) {
+          *reinterpret_cast<f32x4*>(d + 16 * q) = f[q];
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (n + 16 * q + i < N) d[16 * q + i] = f[q][i];
+        }
       }
     }
   }
@@ -294,68 +341,78 @@ struct Quad {
 // once a workgroup and lie in LDS in three bf16 parts; a wave goes through its
 // 64 columns of each step with the next step's base on its way.
 template <bool BF16>
-__global__ void __launch_bounds__(kAddThreads)
+__global__ void __launch_bounds__(kAddThreads, 4)
 k_lora_add(const void* base, int64_t ldb, int T, int N, const uint16_t* __restrict__ b, int L, int R,
-           const int32_t* __restrict__ adapter, const float* __restrict__ h, int slices, int steps, void* out,
-           int64_t ldo, bool vec) {
+           const int32_t* __restrict__ adapter, const float* __restrict__ h, int slices, int colgroups, int wgs,
+           void* out, int64_t ldo, bool vec) {
   extern __shared__ __align__(16) uint8_t sm[];
   const int tid = threadIdx.x, lane = tid % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int c = lane % 16, kq = lane / 16;
-  const int64_t t0 = (int64_t)blockIdx.x * kAddRows;
+  const int wg = xcd_run(blockIdx.x, gridDim.x);
+  if (wg >= wgs) return;
+  const int64_t t0 = (int64_t)(wg / colgroups) * kAddRows;
   int ad[2];
   ad[0] = lora_row_adapter(adapter, t0, T, L, c);
   ad[1] = lora_row_adapter(adapter, t0, T, L, 16 + c);
-  int n0 = blockIdx.y * steps * kAddCols + 64 * wave;
-  Quad<BF16> now[2][4], next[2][4];
-  const auto load = [&](Quad<BF16> (&q)[2][4], int n1) {
+  const int n0 = wg % colgroups * kAddCols + 64 * wave;
+  const void* from = static_cast<const uint8_t*>(base) + t0 * ldb * (BF16 ? 2 : 4);
+  void* to = static_cast<uint8_t*>(out) + t0 * ldo * (BF16 ? 2 : 4);
+  // FULL: all of the workgroup's rows and columns are there, and vectors are aligned
+  const auto run = [&](auto full) {
+    constexpr bool FULL = decltype(full)::value;
+    // row m: t0 + 16 m + c, columns from n0 + 32 j + kQuad kq on
+    constexpr int kQuad = BF16 ? 8 : 4;
+    Eight<BF16> q[2][2];
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (t0 + 16 * m + c < T)
-          q[m][j].load(base, (t0 + 16 * m + c) * ldb + n1 + 16 * j + 4 * kq, n1 + 16 * j + 4 * kq, N, vec);
-  };
-  load(next, n0);
-  const int ld = lora_split_stride(R);
-  lora_split_rows<kAddRows, kAddThreads>(h, slices, T, R, adapter, L, t0, sm, ld, tid);
-  __syncthreads();
-  const uint32_t rows[2] = {lora_rows(ad[0] >= 0), lora_rows(ad[1] >= 0)};
-  for (int s = 0; s < steps && n0 < N; ++s, n0 += kAddCols) {
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) now[m][j] = next[m][j];
-    if (s + 1 < steps && n0 + kAddCols < N) load(next, n0 + kAddCols);
-    uint32_t left[2] = {rows[0], rows[1]};
+      for (int j = 0; j < 2; ++j) {
+        const int n = n0 + 32 * j + kQuad * kq;
+        if (FULL || t0 + 16 * m + c < T) q[m][j].template load<FULL>(from, (uint32_t)(16 * m + c) * (uint32_t)ldb + n, n, N);
+      }
+    const int ld = lora_split_stride(R);
+    lora_split_rows<kAddRows, kAddThreads>(h, slices, T, R, adapter, L, t0, sm, ld, tid);
+    __syncthreads();
+    uint32_t left[2] = {lora_rows(ad[0] >= 0), lora_rows(ad[1] >= 0)};
     while ((left[0] | left[1]) != 0) {
       const int l = left[0] != 0 ? __builtin_amdgcn_readlane(ad[0], __ffs(left[0]) - 1)
                                  : __builtin_amdgcn_readlane(ad[1], __ffs(left[1]) - 1);
       left[0] &= ~lora_rows(ad[0] == l);
       left[1] &= ~lora_rows(ad[1] == l);
       f32x4 d[2][4];
-      lora_products<2, 4>(b + (size_t)l * N * R, N, R, sm, ld, n0, lane, d);
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) d[m][j] = {0.f, 0.f, 0.f, 0.f};
+      for (int r0 = 0; r0 < R; r0 += 32) {
+        bf16x8 bv[4];
+        lora_load_b<2, FULL, BF16>(b + (size_t)l * N * R, N, R, n0, r0, lane, bv);
+        lora_multiply<2, 2>(bv, R, r0, sm, ld, lane, d);
+      }
       // the rows of other adapters keep what they have, whatever this one holds
 #pragma unroll
       for (int m = 0; m < 2; ++m)
         if (ad[m] == l) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) now[m][j].add(d[m][j]);
+          for (int j = 0; j < 2; ++j) q[m][j].add(d[m][2 * j], d[m][2 * j + 1]);
         }
     }
 #pragma unroll
     for (int m = 0; m < 2; ++m)
-      if (t0 + 16 * m + c < T) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          now[m][j].store(out, (t0 + 16 * m + c) * ldo + n0 + 16 * j + 4 * kq, n0 + 16 * j + 4 * kq, N, vec);
+      for (int j = 0; j < 2; ++j) {
+        const int n = n0 + 32 * j + kQuad * kq;
+        if (FULL || t0 + 16 * m + c < T) q[m][j].template store<FULL>(to, (uint32_t)(16 * m + c) * (uint32_t)ldo + n, n, N);
       }
-  }
+  };
+  if (vec && t0 + kAddRows <= T && wg % colgroups * kAddCols + kAddCols <= N) run(std::true_type{});
+  else run(std::false_type{});
 }
 
 }  // namespace
 
-int lora_slices(int T) { return std::max(1, std::min(8, 256 / ((T - 1) / kShRows + 1))); }
+int lora_slices(int T) { return std::max(1, std::min(8, 512 / ((T - 1) / kShRows + 1))); }
 
 hipError_t launch_lora_shrink(const uint16_t* x, int64_t ldx, int T, int K, const uint16_t* a, int L, int R,
                               const int32_t* adapter, const float* scale, float* h, int* slices, hipStream_t st) {
@@ -363,9 +420,10 @@ hipError_t launch_lora_shrink(const uint16_t* x, int64_t ldx, int T, int K, cons
   // while rows are few, workgroups of their own for up to 16 of a tile's adapters
   const int spread = T <= 1024 ? std::min({16, T, L}) : 1;
   const int rgroups = R <= 64 ? 1 : cdiv(R, 64);
-  const dim3 grid(cdiv(T, kShRows), *slices, rgroups * spread);
-#define I8H_SHRINK(NG) \
-  k_lora_shrink<NG><<<grid, kShThreads, 0, st>>>(x, ldx, T, K, a, L, R, adapter, scale, rgroups, h)
+  const int wgs = cdiv(T, kShRows) * *slices * rgroups * spread, grid = cdiv(wgs, kXcds) * kXcds;
+#define I8H_SHRINK(NG)                                                                                            \
+  k_lora_shrink<NG><<<grid, kShThreads, 0, st>>>(x, ldx, T, K, a, L, R, adapter, scale, *slices, rgroups, spread, \
+                                                 wgs, h)
   if (R <= 16) I8H_SHRINK(1);
   else if (R <= 32) I8H_SHRINK(2);
   else I8H_SHRINK(4);
@@ -397,18 +455,16 @@ hipError_t launch_lora_few(const void* base, bool bf16, int64_t ldb, const uint1
 hipError_t launch_lora_add(const void* base, bool bf16, int64_t ldb, int T, int N, const uint16_t* b, int L, int R,
                            const int32_t* adapter, const float* h, int slices, void* out, int64_t ldo,
                            hipStream_t st) {
-  const uintptr_t unit = bf16 ? 8 : 16;   // four elements
-  const bool vec = reinterpret_cast<uintptr_t>(base) % unit == 0 && reinterpret_cast<uintptr_t>(out) % unit == 0 &&
-                   ldb % 4 == 0 && ldo % 4 == 0;
-  const int tiles = cdiv(T, kAddRows), cols = cdiv(N, kAddCols);
-  const int steps = (int)std::max<int64_t>(1, std::min<int64_t>(4, (int64_t)tiles * cols / 512));
-  const dim3 grid(tiles, cdiv(cols, steps));
+  const int unit = bf16 ? 8 : 4;          // elements of 16 bytes
+  const bool vec = reinterpret_cast<uintptr_t>(base) % 16 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0 &&
+                   ldb % unit == 0 && ldo % unit == 0;
+  const int colgroups = cdiv(N, kAddCols), wgs = cdiv(T, kAddRows) * colgroups, grid = cdiv(wgs, kXcds) * kXcds;
   const size_t lds = (size_t)3 * kAddRows * lora_split_stride(R);
   if (bf16)
-    k_lora_add<true><<<grid, kAddThreads, lds, st>>>(base, ldb, T, N, b, L, R, adapter, h, slices, steps, out, ldo,
+    k_lora_add<true><<<grid, kAddThreads, lds, st>>>(base, ldb, T, N, b, L, R, adapter, h, slices, colgroups, wgs, out, ldo,
                                                      vec);
   else
-    k_lora_add<false><<<grid, kAddThreads, lds, st>>>(base, ldb, T, N, b, L, R, adapter, h, slices, steps, out, ldo,
+    k_lora_add<false><<<grid, kAddThreads, lds, st>>>(base, ldb, T, N, b, L, R, adapter, h, slices, colgroups, wgs, out, ldo,
                                                       vec);
   return hipGetLastError();
 }
