@@ -37,8 +37,8 @@ size_t lora_workspace_size(int T, int R);
  * x [T, K] bf16, rows ldx apart (ldx % 8 == 0), 16-B aligned; lora_a
  * [L, R, K], lora_b [L, N, R] bf16, 16-B aligned; adapter [T] int32;
  * lora_scale [L] float32. K % 8 == 0, R % 8 == 0, L >= 1, any N >= 1 (else
- * I8H_EINVAL); R <= I8H_LORA_MAX_RANK, N <= 2^22, T <= 2^26 (else
- * I8H_EUNSUPPORTED).
+ * I8H_EINVAL); R <= I8H_LORA_MAX_RANK, N and K <= 2^22, T <= 2^26, row
+ * distances <= 2^24 (else I8H_EUNSUPPORTED).
  * workspace: at least lora_workspace_size(T, R) bytes, 256-B aligned,
  * contents on entry ignored. */
 int lora_add(const void* base, int base_type, int64_t ldb, const uint16_t* x, int64_t ldx, int T, int K, int N,
@@ -48,8 +48,8 @@ int lora_add(const void* base, int base_type, int64_t ldb, const uint16_t* x, in
 
 /* y[t] = linear_i8f16's product + delta[t]: the dense int8 linear with f16
  * scales and its adapters in one product. x, codes, scales, y as for
- * linear_i8f16 (K % 128 == 0, N % 16 == 0), the adapters as above; T * K <
- * 2^31, T <= 16 * 65535 (else I8H_EUNSUPPORTED). y overlaps no input. */
+ * linear_i8f16 (K % 128 == 0, N % 16 == 0), the adapters and limits as above;
+ * T * K < 2^31, T <= 16 * 65535 (else I8H_EUNSUPPORTED). y overlaps no input. */
 int linear_i8f16_lora(const uint16_t* x, int T, int K, const int8_t* codes, const uint16_t* scales, int N,
                       const uint16_t* lora_a, const uint16_t* lora_b, int L, int R, const int32_t* adapter,
                       const float* lora_scale, float* y, void* workspace, size_t workspace_bytes, void* stream);

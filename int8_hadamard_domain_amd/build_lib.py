@@ -37,7 +37,7 @@ RESOURCES = os.path.join(ROOT, "_build", "kernel_resources.txt")
 SOURCES = ["abi.hip", "route.hip", "fwht.hip", "gateup_i8h_gemv.hip", "gateup_gemm.hip", "gateup_fp8.hip",
            "down.hip", "linear.hip", "gateup_skinny.hip", "gateup_i8g.hip",
            "abi_mx.hip", "mxfp4.hip", "moe_mx.hip", "moe_mx_few.hip", "draft.hip",
-           "abi_batch.hip", "route_scored.hip", "lora.hip"]
+           "abi_batch.hip", "route_scored.hip", "lora.hip", "linear_lora.hip"]
 
 
 def _resources(src, stderr):

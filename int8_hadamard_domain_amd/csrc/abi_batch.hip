@@ -14,6 +14,8 @@ using i8h::kMaxExperts;
 using i8h::kMaxTopk;
 
 constexpr int kLoraMaxN = 1 << 22;      // grid rows of 64 columns and more
+constexpr int kLoraMaxK = 1 << 22;      // rows of a tile are addressed with 32-bit offsets
+constexpr int64_t kLoraMaxLd = 1 << 24;
 constexpr int kLoraMaxT = 1 << 26;      // a workgroup of 512 threads per 16 rows: fewer than 2^32 threads
 
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -99,7 +101,8 @@ int lora_add(const void* base, int base_type, int64_t ldb, const uint16_t* x, in
   if (!is_type(base_type) || T < 0 || K <= 0 || (K % 8) != 0 || N <= 0 || L <= 0 || R <= 0 || (R % 8) != 0)
     return I8H_EINVAL;
   if (ldb < N || ldo < N || ldx < K || (ldx % 8) != 0) return I8H_EINVAL;
-  if (R > I8H_LORA_MAX_RANK || N > kLoraMaxN || T > kLoraMaxT) return I8H_EUNSUPPORTED;
+  if (R > I8H_LORA_MAX_RANK || N > kLoraMaxN || T > kLoraMaxT || K > kLoraMaxK) return I8H_EUNSUPPORTED;
+  if (ldb > kLoraMaxLd || ldo > kLoraMaxLd || ldx > kLoraMaxLd) return I8H_EUNSUPPORTED;
   const int rc = check_lora(x, T, lora_a, lora_b, R, adapter, lora_scale, workspace, workspace_bytes);
   if (rc != I8H_OK || T == 0) return rc;
   const size_t el = type_size(base_type);
@@ -125,7 +128,7 @@ int linear_i8f16_lora(const uint16_t* x, int T, int K, const int8_t* codes, cons
                       const float* lora_scale, float* y, void* workspace, size_t workspace_bytes, void* stream) {
   if (T < 0 || K <= 0 || (K % 128) != 0 || N <= 0 || (N % 16) != 0 || L <= 0 || R <= 0 || (R % 8) != 0)
     return I8H_EINVAL;
-  if (R > I8H_LORA_MAX_RANK || N > kLoraMaxN || (int64_t)T * K >= (int64_t)1 << 31) return I8H_EUNSUPPORTED;
+  if (R > I8H_LORA_MAX_RANK || N > kLoraMaxN || K > kLoraMaxK || (int64_t)T * K >= (int64_t)1 << 31) return I8H_EUNSUPPORTED;
   if ((int64_t)T > (int64_t)65535 * 16) return I8H_EUNSUPPORTED;       // a grid row per 16 tokens
   const int rc = check_lora(x, T, lora_a, lora_b, R, adapter, lora_scale, workspace, workspace_bytes);
   if (rc != I8H_OK || T == 0) return rc;
@@ -138,8 +141,7 @@ int linear_i8f16_lora(const uint16_t* x, int T, int K, const int8_t* codes, cons
   float* h = static_cast<float*>(workspace);
   int slices = 1;
   if (i8h::launch_lora_shrink(x, K, T, K, lora_a, L, R, adapter, lora_scale, h, &slices, st) != hipSuccess) return I8H_EHIP;
-  if (i8h::launch_linear_i8f16(x, T, K, codes, scales, N, y, st) != hipSuccess) return I8H_EHIP;
-  return from_hip(i8h::launch_lora_add(y, false, N, T, N, lora_b, L, R, adapter, h, slices, y, N, st));
+  return from_hip(i8h::launch_linear_i8f16_lora(x, T, K, codes, scales, N, lora_b, L, R, adapter, h, slices, y, st));
 }
 
 }  // extern "C"

@@ -132,7 +132,11 @@ hipError_t launch_route_scored(const void* logits, bool bf16, int T, int E, int 
 int lora_slices(int T);
 hipError_t launch_lora_shrink(const uint16_t* x, int64_t ldx, int T, int K, const uint16_t* a, int L, int R,
                               const int32_t* adapter, const float* scale, float* h, int* slices, hipStream_t st);
-// the same for few rows in one launch, no workspace
+// the dense int8 linear with the adapters' products (linear_lora.hip)
+hipError_t launch_linear_i8f16_lora(const uint16_t* x, int T, int K, const int8_t* codes, const uint16_t* scales,
+                                    int N, const uint16_t* b, int L, int R, const int32_t* adapter, const float* h,
+                                    int slices, float* y, hipStream_t st);
+// lora_add for few rows in one launch, no workspace
 bool lora_few(int T, int R);
 hipError_t launch_lora_few(const void* base, bool bf16, int64_t ldb, const uint16_t* x, int64_t ldx, int T, int K,
                            int N, const uint16_t* a, const uint16_t* b, int L, int R, const int32_t* adapter,

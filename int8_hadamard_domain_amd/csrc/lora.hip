@@ -372,7 +372,7 @@ k_lora_add(const void* base, int64_t ldb, int T, int N, const uint16_t* __restri
         if (FULL || t0 + 16 * m + c < T) q[m][j].template load<FULL>(from, (uint32_t)(16 * m + c) * (uint32_t)ldb + n, n, N);
       }
     const int ld = lora_split_stride(R);
-    lora_split_rows<kAddRows, kAddThreads>(h, slices, T, R, adapter, L, t0, sm, ld, tid);
+    lora_split_rows<kAddRows, kAddThreads>(h, slices, T, R, 0, R, adapter, L, t0, sm, ld, tid);
     __syncthreads();
     uint32_t left[2] = {lora_rows(ad[0] >= 0), lora_rows(ad[1] >= 0)};
     while ((left[0] | left[1]) != 0) {
