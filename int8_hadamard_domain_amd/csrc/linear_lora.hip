@@ -102,6 +102,10 @@ k_linear_lora(const uint16_t* __restrict__ x, int T, int K, const int8_t* __rest
   const int wg = blockIdx.x % kLlXcds * (gridDim.x / kLlXcds) + blockIdx.x / kLlXcds;
   if (wg >= wgs) return;
   const int t0 = wg % ttiles * S::kRows, n0 = wg / ttiles * S::kCols + 16 * NT * wn;
+  int ad[MT < WK ? 1 : MT / WK];               // of the tiles that the wave keeps in the end
+#pragma unroll
+  for (int o = 0; o < (MT < WK ? 1 : MT / WK); ++o)
+    ad[o] = lora_row_adapter(adapter, t0 + 16 * (wk + o * WK), T, L, c);
   const int G = K / kGroup, stages = (G + WK - 1) / WK;
   // Workgroups start at different stages: rows lie a power of two apart more often than not, and all of them at the
   // same piece of K would ask the same L2 channels.
@@ -223,64 +227,91 @@ k_linear_lora(const uint16_t* __restrict__ x, int T, int K, const int8_t* __rest
     __syncthreads();
   }
 
-  // the WK waves' results of a column: wave wk keeps the token tiles wk, wk + WK, ..
+  // the WK waves' results of a column meet in LDS: wave wk keeps the token tiles wk, wk + WK, .. (res[o]: tile wk + o WK)
+  constexpr int MO = MT < WK ? 1 : MT / WK;
+  const bool keeps = wk < MT;
   f32x4* part = reinterpret_cast<f32x4*>(sm);          // [wave][tile][lane]
+  f32x4 res[MO][NT];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+    for (int j = 0; j < NT; ++j) {
       if (m % WK != wk) part[((wave * MT + m) * NT + j) * kWave + lane] = acc[m][j];
+      else res[m / WK][j] = acc[m][j];
+    }
   __syncthreads();
+  // the adapters of its tiles, the first one's B and the thread's first item of h are on their way meanwhile
+  const int rc0 = min(R, kLlRank);
+  const auto load_b = [&](int l, int r, int rc, bf16x8 (&to)[NT]) {
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
-    if (m % WK == wk) {
+    for (int j = 0; j < NT; ++j) {
+      u32x4 v = {0u, 0u, 0u, 0u};
+      if (r % kLlRank + 8 * kq < rc)
+        v = *reinterpret_cast<const u32x4*>(b + ((size_t)l * N + min(n0 + 16 * j + c, N - 1)) * R + r + 8 * kq);
+      to[j] = __builtin_bit_cast(bf16x8, v);
+    }
+  };
+  bf16x8 bv[MO][NT];
+  LoraItem<kLoraSlices> item;
+  const int item_row = tid / (rc0 / 8), item_r = 8 * (tid % (rc0 / 8));
+  const bool has_item = item_row < S::kRows, has_sum = has_item && lora_row_adapter(adapter, t0, T, L, item_row) >= 0;
+  if (has_sum) item.load(h, 0, slices, T, R, t0 + item_row, item_r);
+  if (keeps) {
 #pragma unroll
-      for (int o = 1; o < WK; ++o) {
-        const int from = (wk + o) % WK * WN + wn;
+    for (int o = 0; o < MO; ++o) {
+      const uint32_t rows = lora_rows(ad[o] >= 0);
+      if (rows != 0) load_b(__builtin_amdgcn_readlane(ad[o], __ffs(rows) - 1), 0, rc0, bv[o]);
+    }
+#pragma unroll
+    for (int o = 0; o < MO; ++o)
+#pragma unroll
+      for (int v = 1; v < WK; ++v) {
+        const int from = (wk + v) % WK * WN + wn;
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          const f32x4 v = part[((from * MT + m) * NT + j) * kWave + lane];
+          const f32x4 u = part[((from * MT + wk + o * WK) * NT + j) * kWave + lane];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[m][j][i] += v[i];
+          for (int i = 0; i < 4; ++i) res[o][j][i] += u[i];
         }
       }
-    }
+  }
   __syncthreads();
 
   // the adapters: h of the workgroup's rows in LDS, kLlRank of R at a time
-  const int ld = lora_split_stride(min(R, kLlRank));
+  const int ld = lora_split_stride(rc0);
+  if (has_item) {
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (has_sum) item.add(0, slices, v);
+    lora_split_store<S::kRows>(v, item_row, item_r, sm, ld);
+  }
   for (int r0 = 0; r0 < R; r0 += kLlRank) {
     const int rc = min(R - r0, kLlRank);
-    lora_split_rows<S::kRows, S::kThreads>(h, slices, T, R, r0, rc, adapter, L, t0, sm, ld, tid);
+    lora_split_rows<S::kRows, S::kThreads>(h, slices, T, R, r0, rc, adapter, L, t0, sm, ld,
+                                           tid + (r0 == 0 ? S::kThreads : 0));
     __syncthreads();
+    if (keeps) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-      if (m % WK == wk) {
-        const int ad = lora_row_adapter(adapter, t0 + 16 * m, T, L, c);
-        uint32_t left = lora_rows(ad >= 0);
+      for (int o = 0; o < MO; ++o) {
+        const int row0 = 16 * (wk + o * WK);
+        uint32_t left = lora_rows(ad[o] >= 0);
+        bool ready = r0 == 0;                          // bv[o] holds this adapter's first piece
         while (left != 0) {
-          const int l = __builtin_amdgcn_readlane(ad, __ffs(left) - 1);
-          const uint32_t mine = lora_rows(ad == l);
+          const int l = __builtin_amdgcn_readlane(ad[o], __ffs(left) - 1);
+          const uint32_t mine = lora_rows(ad[o] == l);
           left &= ~mine;
-          const uint16_t* bl = b + (size_t)l * N * R;
           f32x4 d[NT];
 #pragma unroll
           for (int j = 0; j < NT; ++j) d[j] = {0.f, 0.f, 0.f, 0.f};
           for (int r = 0; r < rc; r += 32) {
-            const bool in = r + 8 * kq < rc;
-            bf16x8 bv[NT];
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-              u32x4 v = {0u, 0u, 0u, 0u};
-              if (in) v = *reinterpret_cast<const u32x4*>(bl + (size_t)min(n0 + 16 * j + c, N - 1) * R + r0 + r + 8 * kq);
-              bv[j] = __builtin_bit_cast(bf16x8, v);
-            }
+            if (!ready) load_b(l, r0 + r, rc, bv[o]);
+            ready = false;
 #pragma unroll
             for (int p = 0; p < 3; ++p) {
               bf16x8 hv = __builtin_bit_cast(bf16x8, u32x4{0u, 0u, 0u, 0u});
-              if (in) hv = *reinterpret_cast<const bf16x8*>(sm + (p * S::kRows + 16 * m + c) * ld + 2 * (r + 8 * kq));
+              if (r + 8 * kq < rc)
+                hv = *reinterpret_cast<const bf16x8*>(sm + (p * S::kRows + row0 + c) * ld + 2 * (r + 8 * kq));
 #pragma unroll
-              for (int j = 0; j < NT; ++j) d[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hv, bv[j], d[j], 0, 0, 0);
+              for (int j = 0; j < NT; ++j) d[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hv, bv[o][j], d[j], 0, 0, 0);
             }
           }
           // the rows of other adapters keep what they have, whatever this one holds
@@ -288,22 +319,23 @@ k_linear_lora(const uint16_t* __restrict__ x, int T, int K, const int8_t* __rest
           for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              if ((mine >> (4 * kq + i)) & 1) acc[m][j][i] += d[j][i];
+              if ((mine >> (4 * kq + i)) & 1) res[o][j][i] += d[j][i];
         }
       }
+    }
     __syncthreads();
   }
+  if (keeps) {
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
-    if (m % WK == wk) {
+    for (int o = 0; o < MO; ++o)
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int t = t0 + 16 * m + 4 * kq + i, n = n0 + 16 * j + c;
-          if (t < T && n < N) y[(size_t)t * N + n] = acc[m][j][i];
+          const int t = t0 + 16 * (wk + o * WK) + 4 * kq + i, n = n0 + 16 * j + c;
+          if (t < T && n < N) y[(size_t)t * N + n] = res[o][j][i];
         }
-    }
+  }
 }
 
 template <int MT, int NT, int WN, int WAVES>

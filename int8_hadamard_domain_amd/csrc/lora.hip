@@ -412,7 +412,7 @@ k_lora_add(const void* base, int64_t ldb, int T, int N, const uint16_t* __restri
 
 }  // namespace
 
-int lora_slices(int T) { return std::max(1, std::min(8, 512 / ((T - 1) / kShRows + 1))); }
+int lora_slices(int T) { return std::max(1, std::min(kLoraSlices, 512 / ((T - 1) / kShRows + 1))); }
 
 hipError_t launch_lora_shrink(const uint16_t* x, int64_t ldx, int T, int K, const uint16_t* a, int L, int R,
                               const int32_t* adapter, const float* scale, float* h, int* slices, hipStream_t st) {

@@ -49,42 +49,61 @@ __device__ __forceinline__ Bf16Split split3(const float (&v)[8]) {
 // fragment reads of 16 rows spread over the banks.
 __host__ __device__ constexpr inline int lora_split_stride(int R) { return 2 * R + 16; }
 
+constexpr int kLoraSlices = 8;               // most slices of K
+
+// Eight inner sums of a row: the loads of up to S slices at once, added up in
+// the slices' order, and the store of the sum in three bf16 parts.
+template <int S>
+struct LoraItem {
+  f32x4 u[S][2];
+  __device__ __forceinline__ void load(const float* __restrict__ h, int s0, int slices, int T, int R, int64_t t,
+                                       int r) {
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+      if (s0 + s < slices) {
+        const f32x4* p = reinterpret_cast<const f32x4*>(h + ((int64_t)(s0 + s) * T + t) * R + r);
+        u[s][0] = p[0];
+        u[s][1] = p[1];
+      }
+  }
+  __device__ __forceinline__ void add(int s0, int slices, float (&v)[8]) const {
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+      if (s0 + s < slices) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          v[j] += u[s][0][j];
+          v[4 + j] += u[s][1][j];
+        }
+      }
+  }
+};
+template <int ROWS>
+__device__ __forceinline__ void lora_split_store(const float (&v)[8], int row, int r, uint8_t* sm, int ld) {
+  const Bf16Split q = split3(v);
+#pragma unroll
+  for (int p = 0; p < 3; ++p) *reinterpret_cast<bf16x8*>(sm + (p * ROWS + row) * ld + 2 * r) = q.p[p];
+}
+
 // The inner sums r0 .. r0 + rc - 1 of ROWS rows from t0 on, added up over the
 // slices of K, in three bf16 parts: part p of row r at sm + (p ROWS + r) ld.
-// Rows without an adapter are zero. By a workgroup of THREADS threads; a
-// barrier must follow.
+// Rows without an adapter are zero. By a workgroup of THREADS threads, from
+// item `from` on (a thread's next one is THREADS further); a barrier must follow.
 template <int ROWS, int THREADS>
-__device__ __forceinline__ void lora_split_rows(const float* __restrict__ h, int slices, int T, int R, int r0,
-                                                int rc, const int32_t* __restrict__ adapter, int L, int64_t t0, uint8_t* sm,
-                                                int ld, int tid) {
-  for (int i = tid; i < ROWS * (rc / 8); i += THREADS) {
+__device__ __forceinline__ void lora_split_rows(const float* __restrict__ h, int slices, int T, int R, int r0, int rc,
+                                                const int32_t* __restrict__ adapter, int L, int64_t t0, uint8_t* sm,
+                                                int ld, int from) {
+#pragma unroll 1
+  for (int i = from; i < ROWS * (rc / 8); i += THREADS) {
     const int row = i / (rc / 8), r = 8 * (i % (rc / 8));
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (lora_row_adapter(adapter, t0, T, L, row) >= 0) {
-      // four slices' loads at a time, added up in order
-      for (int s0 = 0; s0 < slices; s0 += 4) {
-        f32x4 u[4][2];
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const int at = min(s0 + s, slices - 1);
-          const f32x4* p = reinterpret_cast<const f32x4*>(h + ((int64_t)at * T + t0 + row) * R + r0 + r);
-          u[s][0] = p[0];
-          u[s][1] = p[1];
-        }
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-          if (s0 + s < slices) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              v[j] += u[s][0][j];
-              v[4 + j] += u[s][1][j];
-            }
-          }
+    if (lora_row_adapter(adapter, t0, T, L, row) >= 0)
+      for (int s = 0; s < slices; s += 4) {
+        LoraItem<4> item;
+        item.load(h, s, slices, T, R, t0 + row, r0 + r);
+        item.add(s, slices, v);
       }
-    }
-    const Bf16Split q = split3(v);
-#pragma unroll
-    for (int p = 0; p < 3; ++p) *reinterpret_cast<bf16x8*>(sm + (p * ROWS + row) * ld + 2 * r) = q.p[p];
+    lora_split_store<ROWS>(v, row, r, sm, ld);
   }
 }
 
