@@ -59,10 +59,10 @@ __device__ __forceinline__ void ll_copy16(uint32_t off, const void* base, uint32
                : "memory", "m0");
 }
 #pragma clang diagnostic pop
-// s_waitcnt vmcnt(0) with expcnt and lgkmcnt unconstrained (gfx9 field layout)
-constexpr int kLlVmcnt0 = (0x7 << 4) | (0xF << 8);
+// s_waitcnt vmcnt(n) with expcnt and lgkmcnt unconstrained (gfx9 field layout)
+constexpr int ll_vmcnt(int n) { return (n & 15) | (n >> 4) << 14 | (0x7 << 4) | (0xF << 8); }
 
-template <int MT, int NT, int WN, int WAVES>
+template <int MT, int NT, int WN, int WAVES, int BUFS>
 struct LlShape {
   static constexpr int kThreads = kWave * WAVES, kWk = WAVES / WN;
   static constexpr int kRows = 16 * MT, kCols = 16 * NT * WN;
@@ -85,13 +85,13 @@ __device__ __forceinline__ int ll_place(int r, int p) {
   else return r * (16 * PIECES + 16) + 16 * p;
 }
 
-template <int MT, int NT, int WN, int WAVES>
+template <int MT, int NT, int WN, int WAVES, int BUFS>
 __global__ void __launch_bounds__(kWave * WAVES)
 k_linear_lora(const uint16_t* __restrict__ x, int T, int K, const int8_t* __restrict__ codes,
               const uint16_t* __restrict__ scales, int N, const uint16_t* __restrict__ b, int L, int R,
               const int32_t* __restrict__ adapter, const float* __restrict__ h, int slices, int ttiles, int wgs,
               float* __restrict__ y) {
-  using S = LlShape<MT, NT, WN, WAVES>;
+  using S = LlShape<MT, NT, WN, WAVES, BUFS>;
   constexpr int WK = S::kWk;
   extern __shared__ __align__(16) uint8_t sm[];
   const int tid = threadIdx.x, lane = tid % kWave;
@@ -135,16 +135,18 @@ k_linear_lora(const uint16_t* __restrict__ x, int T, int K, const int8_t* __rest
     coff[j] = n * (uint32_t)K + 16 * kq;
     soff[j] = n * (uint32_t)G;
   }
-  u32x4 cv[NT][2], cn[NT][2];                  // this stage's codes and scales, and the next one's
-  uint16_t sv[NT], sn[NT];
-  const auto load_codes = [&](int s) {
-    const int g = s * WK + wk;
-    if (g >= G) return;
+  // stages on their way: kAhead of them, their codes and scales in registers
+  constexpr int kAhead = BUFS - 1;
+  u32x4 cn[kAhead][NT][2];
+  uint16_t sn[kAhead][NT];
+  const auto load_codes = [&](auto to, int s) {
+    const int g = min(s * WK + wk, G - 1);     // (past the last group: not used)
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) cn[j][i] = *reinterpret_cast<const u32x4*>(cbase + g * kGroup + 64 * i + coff[j]);
-      sn[j] = sbase[g + soff[j]];
+      for (int i = 0; i < 2; ++i)
+        cn[to.value][j][i] = *reinterpret_cast<const u32x4*>(cbase + g * kGroup + 64 * i + coff[j]);
+      sn[to.value][j] = sbase[g + soff[j]];
     }
   };
   f32x4 acc[MT][NT];
@@ -152,18 +154,23 @@ k_linear_lora(const uint16_t* __restrict__ x, int T, int K, const int8_t* __rest
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[m][j] = {0.f, 0.f, 0.f, 0.f};
-  const auto multiply = [&](const uint8_t* xs) {
-    bf16x8 w[NT][4];
-    float sc[NT];
+  bf16x8 w[NT][4];
+  float sc[NT];
+  const auto decode = [&](auto from) {
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      sc[j] = (float)__builtin_bit_cast(_Float16, sv[j]);
+      sc[j] = (float)__builtin_bit_cast(_Float16, sn[from.value][j]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        w[j][i] = ll_decode(cv[j][i / 2][2 * (i % 2)], cv[j][i / 2][2 * (i % 2) + 1]);
+        uint32_t lo = cn[from.value][j][i / 2][2 * (i % 2)], hi = cn[from.value][j][i / 2][2 * (i % 2) + 1];
+        // opaque to the compiler: it would take the words apart where they are loaded, and wait for them there
+        asm volatile("" : "+v"(lo), "+v"(hi));
+        w[j][i] = ll_decode(lo, hi);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
+  };
+  const auto multiply = [&](const uint8_t* xs) {
     // A token tile's fragments are read while the tile before multiplies, and its sums folded while the next one does:
     // the barriers keep the compiler from moving them apart.
     bf16x8 xv[2][4];
@@ -200,31 +207,46 @@ k_linear_lora(const uint16_t* __restrict__ x, int T, int K, const int8_t* __rest
     fold(MT - 1);
   };
 
-  load_x(turn, 0);
-  load_codes(turn);
-  __builtin_amdgcn_s_waitcnt(kLlVmcnt0);
+  const auto nth = [&](int i) { return i + turn < stages ? i + turn : i + turn - stages; };
+  // The copies of a stage are awaited by count: those of the kAhead - 1 stages behind it may be on their way (the codes'
+  // loads among them only make the wait longer). At the end of K there are fewer, and all are awaited.
+  const auto stage = [&](auto slot, int i) {   // slot = i % kAhead
+    decode(slot);
+    if (i + kAhead < stages) {
+      load_x(nth(i + kAhead), (i + kAhead) % BUFS);
+      load_codes(slot, nth(i + kAhead));
+    }
+    if (nth(i) * WK + wk < G) multiply(sm + i % BUFS * S::kStage);
+    if (i + kAhead < stages) __builtin_amdgcn_s_waitcnt(ll_vmcnt((kAhead - 1) * S::kLoads));
+    else __builtin_amdgcn_s_waitcnt(ll_vmcnt(0));
+    __syncthreads();
+  };
+  const std::integral_constant<int, 0> s0;
+  const std::integral_constant<int, kAhead - 1 < 1 ? kAhead - 1 : 1> s1;
+  const std::integral_constant<int, kAhead - 1 < 2 ? kAhead - 1 : 2> s2;
+  static_assert(kAhead == 1 || kAhead == 3, "stages are written out below");
+  load_x(nth(0), 0);
+  load_codes(s0, nth(0));
+  if constexpr (kAhead == 3) {
+    if (stages > 1) {
+      load_x(nth(1), 1);
+      load_codes(s1, nth(1));
+    }
+    if (stages > 2) {
+      load_x(nth(2), 2);
+      load_codes(s2, nth(2));
+    }
+  }
+  if (stages >= kAhead) __builtin_amdgcn_s_waitcnt(ll_vmcnt((kAhead - 1) * S::kLoads));
+  else __builtin_amdgcn_s_waitcnt(ll_vmcnt(0));
   __syncthreads();
 #pragma unroll 1
-  for (int i = 0; i < stages; ++i) {
-    const int s = i + turn < stages ? i + turn : i + turn - stages, next = s + 1 < stages ? s + 1 : 0;
-    // opaque to the compiler: it would take the words apart where they are loaded, and wait for them there
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        uint32_t w = cn[j][q / 4][q % 4];
-        asm volatile("" : "+v"(w));
-        cv[j][q / 4][q % 4] = w;
-      }
-      sv[j] = sn[j];
+  for (int i = 0; i < stages; i += kAhead) {
+    stage(s0, i);
+    if constexpr (kAhead == 3) {
+      if (i + 1 < stages) stage(s1, i + 1);
+      if (i + 2 < stages) stage(s2, i + 2);
     }
-    if (i + 1 < stages) {
-      load_x(next, (i + 1) % 2);
-      load_codes(next);
-    }
-    if (s * WK + wk < G) multiply(sm + i % 2 * S::kStage);
-    __builtin_amdgcn_s_waitcnt(kLlVmcnt0);             // this wave's copies of the next stage
-    __syncthreads();
   }
 
   // the WK waves' results of a column meet in LDS: wave wk keeps the token tiles wk, wk + WK, .. (res[o]: tile wk + o WK)
@@ -338,15 +360,15 @@ k_linear_lora(const uint16_t* __restrict__ x, int T, int K, const int8_t* __rest
   }
 }
 
-template <int MT, int NT, int WN, int WAVES>
+template <int MT, int NT, int WN, int WAVES, int BUFS>
 hipError_t launch(const uint16_t* x, int T, int K, const int8_t* codes, const uint16_t* scales, int N,
                   const uint16_t* b, int L, int R, const int32_t* adapter, const float* h, int slices, float* y,
                   hipStream_t st) {
-  using S = LlShape<MT, NT, WN, WAVES>;
+  using S = LlShape<MT, NT, WN, WAVES, BUFS>;
   const int ttiles = cdiv(T, S::kRows), wgs = ttiles * cdiv(N, S::kCols), grid = cdiv(wgs, kLlXcds) * kLlXcds;
-  const size_t lds = std::max<size_t>({(size_t)2 * S::kStage, (size_t)S::kJoin,
+  const size_t lds = std::max<size_t>({(size_t)BUFS * S::kStage, (size_t)S::kJoin,
                                        (size_t)3 * S::kRows * lora_split_stride(std::min(R, kLlRank))});
-  k_linear_lora<MT, NT, WN, WAVES><<<grid, S::kThreads, lds, st>>>(x, T, K, codes, scales, N, b, L, R, adapter, h, slices,
+  k_linear_lora<MT, NT, WN, WAVES, BUFS><<<grid, S::kThreads, lds, st>>>(x, T, K, codes, scales, N, b, L, R, adapter, h, slices,
                                                            ttiles, wgs, y);
   return hipGetLastError();
 }
@@ -356,13 +378,14 @@ hipError_t launch(const uint16_t* x, int T, int K, const int8_t* codes, const ui
 hipError_t launch_linear_i8f16_lora(const uint16_t* x, int T, int K, const int8_t* codes, const uint16_t* scales,
                                     int N, const uint16_t* b, int L, int R, const int32_t* adapter, const float* h,
                                     int slices, float* y, hipStream_t st) {
-#define I8H_LL(MT, NT, WN, WAVES) return launch<MT, NT, WN, WAVES>(x, T, K, codes, scales, N, b, L, R, adapter, h, slices, y, st)
+#define I8H_LL(MT, NT, WN, WAVES, BUFS) \
+  return launch<MT, NT, WN, WAVES, BUFS>(x, T, K, codes, scales, N, b, L, R, adapter, h, slices, y, st)
   // the largest tile that leaves a workgroup to every CU
   const auto fills = [&](int rows, int cols) { return (int64_t)cdiv(T, rows) * cdiv(N, cols) >= 256; };
-  if (fills(128, 128)) I8H_LL(8, 2, 4, 8);
-  if (fills(64, 128)) I8H_LL(4, 2, 4, 8);
-  if (fills(32, 64)) I8H_LL(2, 2, 2, 8);
-  I8H_LL(1, 1, 1, 8);
+  if (fills(128, 128)) I8H_LL(8, 2, 4, 8, 2);
+  if (fills(64, 128)) I8H_LL(4, 2, 4, 8, 4);
+  if (fills(32, 64)) I8H_LL(2, 2, 2, 8, 4);
+  I8H_LL(1, 1, 1, 8, 4);
 #undef I8H_LL
 }
 

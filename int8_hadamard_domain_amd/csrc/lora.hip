@@ -35,6 +35,7 @@ constexpr int kFewThreads = kWave * kFewWaves;
 constexpr int kAddThreads = 256;               // the add kernel: rows and columns of a step
 constexpr int kAddRows = 32;
 constexpr int kAddCols = 256;
+constexpr int kAddBRow = 80;                   // bytes of LDS of a row of B, 32 of R: 64 and 16 of padding
 
 // Workgroups are dealt to the XCDs in turn: the i-th of n (a multiple of their
 // number) takes place i % kXcds * n / kXcds + i / kXcds, so that each XCD's L2
@@ -263,88 +264,72 @@ k_lora_few(const void* base, int64_t ldb, const uint16_t* __restrict__ x, int64_
   }
 }
 
-// Eight elements of a row of base or out that a lane holds: in float32 those
-// from n and from n + 16 on, four each (the four lanes of a row load 64
-// contiguous bytes; eight neighbours a lane would load 16 of every 32 bytes,
-// four times the accesses), as packed bf16 the eight from n on. FULL: all there
-// and aligned to 16 bytes.
+// 16 bytes of a row of base or out, four float32 values or eight bf16. FULL: all there and aligned.
 template <bool BF16>
-struct Eight {
-  f32x4 f[2];
-  u32x4 b;
+struct Piece {
+  static constexpr int kE = BF16 ? 8 : 4;
+  u32x4 v;
   template <bool FULL>
   __device__ __forceinline__ void load(const void* p, uint32_t at, int n, int N) {
-    if constexpr (BF16) {
+    if constexpr (FULL) {
+      v = load16(p, (16 / kE) * at);
+    } else if constexpr (BF16) {
       const uint16_t* s = static_cast<const uint16_t*>(p) + at;
-      if constexpr (FULL) {
-        b = *reinterpret_cast<const u32x4*>(s);
-      } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          b[i] = (n + 2 * i < N ? (uint32_t)s[2 * i] : 0u) | (n + 2 * i + 1 < N ? (uint32_t)s[2 * i + 1] << 16 : 0u);
-      }
+      for (int i = 0; i < 4; ++i)
+        v[i] = (n + 2 * i < N ? (uint32_t)s[2 * i] : 0u) | (n + 2 * i + 1 < N ? (uint32_t)s[2 * i + 1] << 16 : 0u);
     } else {
-      const float* s = static_cast<const float*>(p) + at;
+      const uint32_t* s = static_cast<const uint32_t*>(p) + at;
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        if constexpr (FULL) {
-          f[q] = *reinterpret_cast<const f32x4*>(s + 16 * q);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) f[q][i] = n + 16 * q + i < N ? s[16 * q + i] : 0.0f;
-        }
-      }
+      for (int i = 0; i < 4; ++i) v[i] = n + i < N ? s[i] : 0u;
     }
   }
-  __device__ __forceinline__ void add(const f32x4& d0, const f32x4& d1) {
+  __device__ __forceinline__ void add(const float* d) {
+    const f32x4 d0 = *reinterpret_cast<const f32x4*>(d);
     if constexpr (BF16) {
-      b = {pack_bf16x2(bf16_lo(b[0]) + d0[0], bf16_hi(b[0]) + d0[1]),
-           pack_bf16x2(bf16_lo(b[1]) + d0[2], bf16_hi(b[1]) + d0[3]),
-           pack_bf16x2(bf16_lo(b[2]) + d1[0], bf16_hi(b[2]) + d1[1]),
-           pack_bf16x2(bf16_lo(b[3]) + d1[2], bf16_hi(b[3]) + d1[3])};
+      const f32x4 d1 = *reinterpret_cast<const f32x4*>(d + 4);
+      v = {pack_bf16x2(bf16_lo(v[0]) + d0[0], bf16_hi(v[0]) + d0[1]),
+           pack_bf16x2(bf16_lo(v[1]) + d0[2], bf16_hi(v[1]) + d0[3]),
+           pack_bf16x2(bf16_lo(v[2]) + d1[0], bf16_hi(v[2]) + d1[1]),
+           pack_bf16x2(bf16_lo(v[3]) + d1[2], bf16_hi(v[3]) + d1[3])};
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        f[0][i] += d0[i];
-        f[1][i] += d1[i];
-      }
+      for (int i = 0; i < 4; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + d0[i]);
     }
   }
   template <bool FULL>
   __device__ __forceinline__ void store(void* p, uint32_t at, int n, int N) const {
-    if constexpr (BF16) {
+    if constexpr (FULL) {
+      *reinterpret_cast<u32x4*>(static_cast<uint8_t*>(p) + (16 / kE) * at) = v;
+    } else if constexpr (BF16) {
       uint16_t* d = static_cast<uint16_t*>(p) + at;
-      if constexpr (FULL) {
-        *reinterpret_cast<u32x4*>(d) = b;
-      } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (n + i < N) d[i] = (uint16_t)(b[i / 2] >> (16 * (i % 2)));
-      }
+      for (int i = 0; i < 8; ++i)
+        if (n + i < N) d[i] = (uint16_t)(v[i / 2] >> (16 * (i % 2)));
     } else {
-      float* d = static_cast<float*>(p) + at;
+      uint32_t* d = static_cast<uint32_t*>(p) + at;
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        if constexpr (FULL) {
-          *reinterpret_cast<f32x4*>(d + 16 * q) = f[q];
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (n + 16 * q + i < N) d[16 * q + i] = f[q][i];
-        }
-      }
+      for (int i = 0; i < 4; ++i)
+        if (n + i < N) d[i] = v[i];
     }
   }
 };
 
-// out of 32 rows and `steps` times 256 columns: the slices of h are added up
-// once a workgroup and lie in LDS in three bf16 parts; a wave goes through its
-// 64 columns of each step with the next step's base on its way.
+// out of 32 rows and 256 columns, 64 a wave. h is added up over its slices
+// once a workgroup and lies in LDS in three bf16 parts. Neighbouring lanes are
+// served together only where they take neighbouring bytes, and the matrix
+// layouts deal a row to lanes 16 apart; so base and out are loaded and stored
+// with 128 bytes of a row on neighbouring lanes, B 64 bytes of a row on four,
+// and a wave's own LDS turns B's rows and the products into the other order
+// (64 us without, 55 with, of 8191 x 4096 float32 rows).
 template <bool BF16>
-__global__ void __launch_bounds__(kAddThreads, 4)
+__global__ void __launch_bounds__(kAddThreads, BF16 ? 3 : 4)
 k_lora_add(const void* base, int64_t ldb, int T, int N, const uint16_t* __restrict__ b, int L, int R,
            const int32_t* __restrict__ adapter, const float* __restrict__ h, int slices, int colgroups, int wgs,
            void* out, int64_t ldo, bool vec) {
+  using P = Piece<BF16>;
+  constexpr int kNT = BF16 ? 2 : 1, kPasses = 2 / kNT, kCols = 32 * kNT;             // columns a pass: 128 bytes a row
+  constexpr int kLpr = kCols / P::kE, kRpc = kWave / kLpr, kChunks = kAddRows / kRpc;   // lanes a row, rows a load
   extern __shared__ __align__(16) uint8_t sm[];
   const int tid = threadIdx.x, lane = tid % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -355,56 +340,92 @@ k_lora_add(const void* base, int64_t ldb, int T, int N, const uint16_t* __restri
   int ad[2];
   ad[0] = lora_row_adapter(adapter, t0, T, L, c);
   ad[1] = lora_row_adapter(adapter, t0, T, L, 16 + c);
+  const uint32_t rows[2] = {lora_rows(ad[0] >= 0), lora_rows(ad[1] >= 0)};
   const int n0 = wg % colgroups * kAddCols + 64 * wave;
   const void* from = static_cast<const uint8_t*>(base) + t0 * ldb * (BF16 ? 2 : 4);
   void* to = static_cast<uint8_t*>(out) + t0 * ldo * (BF16 ? 2 : 4);
+  const int ld = lora_split_stride(R);
+  uint8_t* own = sm + 3 * kAddRows * ld + wave * (kCols * kAddBRow);
   // FULL: all of the workgroup's rows and columns are there, and vectors are aligned
   const auto run = [&](auto full) {
     constexpr bool FULL = decltype(full)::value;
-    // row m: t0 + 16 m + c, columns from n0 + 32 j + kQuad kq on
-    constexpr int kQuad = BF16 ? 8 : 4;
-    Eight<BF16> q[2][2];
+    const int row = lane / kLpr, n1 = n0 + P::kE * (lane % kLpr);      // chunk i of pass g: row + kRpc i, n1 + kCols g
+    P q[kPasses][kChunks];
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+    for (int g = 0; g < kPasses; ++g)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int n = n0 + 32 * j + kQuad * kq;
-        if (FULL || t0 + 16 * m + c < T) q[m][j].template load<FULL>(from, (uint32_t)(16 * m + c) * (uint32_t)ldb + n, n, N);
-      }
-    const int ld = lora_split_stride(R);
+      for (int i = 0; i < kChunks; ++i)
+        if (FULL || t0 + row + kRpc * i < T)
+          q[g][i].template load<FULL>(from, (uint32_t)(row + kRpc * i) * (uint32_t)ldb + n1 + kCols * g, n1 + kCols * g, N);
     lora_split_rows<kAddRows, kAddThreads>(h, slices, T, R, 0, R, adapter, L, t0, sm, ld, tid);
     __syncthreads();
-    uint32_t left[2] = {lora_rows(ad[0] >= 0), lora_rows(ad[1] >= 0)};
-    while ((left[0] | left[1]) != 0) {
-      const int l = left[0] != 0 ? __builtin_amdgcn_readlane(ad[0], __ffs(left[0]) - 1)
-                                 : __builtin_amdgcn_readlane(ad[1], __ffs(left[1]) - 1);
-      left[0] &= ~lora_rows(ad[0] == l);
-      left[1] &= ~lora_rows(ad[1] == l);
-      f32x4 d[2][4];
+#pragma unroll
+    for (int g = 0; g < kPasses; ++g) {
+      const int ng = n0 + kCols * g, n = n1 + kCols * g;
+      f32x4 sum[2][2 * kNT];
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) d[m][j] = {0.f, 0.f, 0.f, 0.f};
-      for (int r0 = 0; r0 < R; r0 += 32) {
-        bf16x8 bv[4];
-        lora_load_b<2, FULL, BF16>(b + (size_t)l * N * R, N, R, n0, r0, lane, bv);
-        lora_multiply<2, 2>(bv, R, r0, sm, ld, lane, d);
-      }
-      // the rows of other adapters keep what they have, whatever this one holds
+        for (int j = 0; j < 2 * kNT; ++j) sum[m][j] = {0.f, 0.f, 0.f, 0.f};
+      uint32_t left[2] = {rows[0], rows[1]};
+      while ((left[0] | left[1]) != 0) {
+        const int l = left[0] != 0 ? __builtin_amdgcn_readlane(ad[0], __ffs(left[0]) - 1)
+                                   : __builtin_amdgcn_readlane(ad[1], __ffs(left[1]) - 1);
+        left[0] &= ~lora_rows(ad[0] == l);
+        left[1] &= ~lora_rows(ad[1] == l);
+        f32x4 d[2][2 * kNT];
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
-        if (ad[m] == l) {
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) q[m][j].add(d[m][2 * j], d[m][2 * j + 1]);
+          for (int j = 0; j < 2 * kNT; ++j) d[m][j] = {0.f, 0.f, 0.f, 0.f};
+        const uint16_t* bl = b + ((size_t)l * N + ng) * R;
+        for (int r0 = 0; r0 < R; r0 += 32) {
+          // 32 of R of the pass's rows of B
+          u32x4 w[2 * kNT];
+#pragma unroll
+          for (int i = 0; i < 2 * kNT; ++i) {
+            const int nb = 16 * i + lane / 4, r = 8 * (lane % 4);
+            w[i] = {0u, 0u, 0u, 0u};
+            if ((FULL || ng + nb < N) && r0 + r < R) w[i] = load16(bl + r0, 2u * ((uint32_t)nb * (uint32_t)R + r));
+          }
+          lora_wave_order();
+#pragma unroll
+          for (int i = 0; i < 2 * kNT; ++i)
+            *reinterpret_cast<u32x4*>(own + (16 * i + lane / 4) * kAddBRow + 16 * (lane % 4)) = w[i];
+          lora_wave_order();
+          bf16x8 bv[2 * kNT];
+#pragma unroll
+          for (int j = 0; j < 2 * kNT; ++j)
+            bv[j] = *reinterpret_cast<const bf16x8*>(own + (16 * j + c) * kAddBRow + 16 * kq);
+          lora_multiply<2, kNT>(bv, R, r0, sm, ld, lane, d);
         }
-    }
+        // the rows of other adapters keep what they have, whatever this one holds
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int n = n0 + 32 * j + kQuad * kq;
-        if (FULL || t0 + 16 * m + c < T) q[m][j].template store<FULL>(to, (uint32_t)(16 * m + c) * (uint32_t)ldo + n, n, N);
+          for (int j = 0; j < 2 * kNT; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[m][j][i] = ad[m] == l ? d[m][j][i] : sum[m][j][i];
       }
+      // 16 rows at a time through the wave's LDS
+      constexpr int kTurn = kCols + 4;         // floats from row to row
+      float* turn = reinterpret_cast<float*>(own);
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        if (rows[m] != 0) {
+          lora_wave_order();
+#pragma unroll
+          for (int j = 0; j < 2 * kNT; ++j) *reinterpret_cast<f32x4*>(turn + kTurn * c + 16 * j + 4 * kq) = sum[m][j];
+          lora_wave_order();
+        }
+#pragma unroll
+        for (int i = m * kChunks / 2; i < (m + 1) * kChunks / 2; ++i) {
+          const int r = row + kRpc * i;
+          if ((rows[m] >> (r % 16)) & 1) q[g][i].add(turn + kTurn * (r % 16) + P::kE * (lane % kLpr));
+          if (FULL || t0 + r < T) q[g][i].template store<FULL>(to, (uint32_t)r * (uint32_t)ldo + n, n, N);
+        }
+      }
+    }
   };
   if (vec && t0 + kAddRows <= T && wg % colgroups * kAddCols + kAddCols <= N) run(std::true_type{});
   else run(std::false_type{});
@@ -459,7 +480,7 @@ hipError_t launch_lora_add(const void* base, bool bf16, int64_t ldb, int T, int 
   const bool vec = reinterpret_cast<uintptr_t>(base) % 16 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0 &&
                    ldb % unit == 0 && ldo % unit == 0;
   const int colgroups = cdiv(N, kAddCols), wgs = cdiv(T, kAddRows) * colgroups, grid = cdiv(wgs, kXcds) * kXcds;
-  const size_t lds = (size_t)3 * kAddRows * lora_split_stride(R);
+  const size_t lds = (size_t)3 * kAddRows * lora_split_stride(R) + kAddThreads / kWave * (bf16 ? 64 : 32) * kAddBRow;
   if (bf16)
     k_lora_add<true><<<grid, kAddThreads, lds, st>>>(base, ldb, T, N, b, L, R, adapter, h, slices, colgroups, wgs, out, ldo,
                                                      vec);

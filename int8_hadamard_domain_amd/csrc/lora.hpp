@@ -107,28 +107,17 @@ __device__ __forceinline__ void lora_split_rows(const float* __restrict__ h, int
   }
 }
 
-// The products of the adapters' second half: d[m][2 j + i] += B h for the 16 MT
-// rows in LDS (lora_split_rows) and columns n0 ..: the lane gets row
-// 16 m + lane % 16, and four columns from n0 + 32 j + 16 i + 4 (lane / 16) on,
-// or (EIGHT) n0 + 32 j + 8 (lane / 16) + 4 i: eight neighbours for i = 0, 1 (the
-// rows of B are dealt to the matrix rows accordingly). lora_load_b loads 32 of
-// R from r0 on (b: the adapter's B; FULL: all 32 NT columns are there),
-// lora_multiply takes them.
-template <int NT, bool FULL, bool EIGHT>
-__device__ __forceinline__ void lora_load_b(const uint16_t* __restrict__ b, int N, int R, int n0, int r0, int lane,
-                                            bf16x8 (&bv)[2 * NT]) {
-  const int c = lane % 16, r = r0 + 8 * (lane / 16), n = EIGHT ? 8 * (c / 4) + c % 4 : c;
-  const uint32_t off = 2u * ((uint32_t)n * (uint32_t)R + 8u * (lane / 16));
-#pragma unroll
-  for (int j = 0; j < 2 * NT; ++j) {
-    const int nj = n0 + 32 * (j / 2) + (EIGHT ? 4 : 16) * (j % 2);
-    u32x4 w = {0u, 0u, 0u, 0u};
-    if ((FULL || nj + n < N) && r < R)
-      w = *reinterpret_cast<const u32x4*>(reinterpret_cast<const uint8_t*>(b + (size_t)nj * R + r0) + off);
-    bv[j] = __builtin_bit_cast(bf16x8, w);
-  }
+// LDS that a wave's lanes hand on to each other: writes before, reads after.
+__device__ __forceinline__ void lora_wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// The products of the adapters' second half, 32 of R from r0 on: d[m][j] += B h
+// for the 16 MT rows in LDS (lora_split_rows) and 32 NT columns, bv[j] holding
+// row 16 j + lane % 16 of B: the lane gets row 16 m + lane % 16, columns
+// 16 j + 4 (lane / 16) .. + 3.
 template <int MT, int NT>
 __device__ __forceinline__ void lora_multiply(const bf16x8 (&bv)[2 * NT], int R, int r0, const uint8_t* sm, int ld,
                                               int lane, f32x4 (&d)[MT][2 * NT]) {
