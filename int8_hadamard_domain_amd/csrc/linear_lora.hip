@@ -380,12 +380,20 @@ hipError_t launch_linear_i8f16_lora(const uint16_t* x, int T, int K, const int8_
                                     int slices, float* y, hipStream_t st) {
 #define I8H_LL(MT, NT, WN, WAVES, BUFS) \
   return launch<MT, NT, WN, WAVES, BUFS>(x, T, K, codes, scales, N, b, L, R, adapter, h, slices, y, st)
-  // the largest tile that leaves a workgroup to every CU
-  const auto fills = [&](int rows, int cols) { return (int64_t)cdiv(T, rows) * cdiv(N, cols) >= 256; };
-  if (fills(128, 128)) I8H_LL(8, 2, 4, 8, 2);
-  if (fills(64, 128)) I8H_LL(4, 2, 4, 8, 4);
-  if (fills(32, 64)) I8H_LL(2, 2, 2, 8, 4);
-  I8H_LL(1, 1, 1, 8, 4);
+  // The smallest tile whose workgroups the 256 CUs hold in about one turn: small ones cost least where there is little
+  // to do, large ones read and decode a code for more tokens. Measured with the shrink, K = 2048, rank 16, us:
+  //   tokens x columns    16 x 16   32 x 32   64 x 128   128 x 128
+  //     32 x 4096          13.5      14.3       24.8       28.5       (512 workgroups of 16 x 16)
+  //     64 x 4096          20.9      14.9       26.2       29.8
+  //    512 x 1024          34.6      19.6       26.8       33.4       (512 workgroups of 32 x 32)
+  //    256 x 4096          58.7      29.2       27.0       32.7
+  //    512 x 4096         107        48.7       28.6       33.8       (256 workgroups of 64 x 128)
+  //   1024 x 4096         225       104         52.3       40.7
+  const auto within = [&](int rows, int cols, int wgs) { return (int64_t)cdiv(T, rows) * cdiv(N, cols) <= wgs; };
+  if (within(16, 16, 512)) I8H_LL(1, 1, 1, 8, 2);
+  if (within(32, 32, 512)) I8H_LL(2, 1, 2, 8, 2);
+  if (within(64, 128, 256)) I8H_LL(4, 2, 4, 8, 4);
+  I8H_LL(8, 2, 4, 8, 2);
 #undef I8H_LL
 }
 
