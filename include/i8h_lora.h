@@ -12,7 +12,7 @@
  * them. Adapters of smaller rank are padded with zeros to R. Products are
  * exact, sums float32; the inner sums enter the second product as float32
  * values (as three bf16 parts), not rounded. Results are the same, bit for
- * bit, in every run.
+ * bit, in every run. (An infinity in B may give NaN where a part is 0.)
  */
 #ifndef I8H_LORA_H
 #define I8H_LORA_H
@@ -33,12 +33,13 @@ size_t lora_workspace_size(int T, int R);
  * output. base and out [T, N] of base_type (I8H_F32 or I8H_BF16: the float32
  * sum is rounded once, to nearest even), rows ldb and ldo elements apart,
  * aligned to the element; out may be base (with ldo == ldb), other overlap of
- * out with an input is refused. Rows without an adapter are copied bit for bit.
+ * out with an input is refused (column slices of one matrix may lie side by
+ * side). Rows without an adapter are copied bit for bit.
  * x [T, K] bf16, rows ldx apart (ldx % 8 == 0), 16-B aligned; lora_a
  * [L, R, K], lora_b [L, N, R] bf16, 16-B aligned; adapter [T] int32;
  * lora_scale [L] float32. K % 8 == 0, R % 8 == 0, L >= 1, any N >= 1 (else
- * I8H_EINVAL); R <= I8H_LORA_MAX_RANK, N and K <= 2^22, T <= 2^26, row
- * distances <= 2^24 (else I8H_EUNSUPPORTED).
+ * I8H_EINVAL); R <= I8H_LORA_MAX_RANK, N and K <= 2^22, T <= 2^26, T * N <=
+ * 2^35, row distances <= 2^24 (else I8H_EUNSUPPORTED).
  * workspace: at least lora_workspace_size(T, R) bytes, 256-B aligned,
  * contents on entry ignored. */
 int lora_add(const void* base, int base_type, int64_t ldb, const uint16_t* x, int64_t ldx, int T, int K, int N,
@@ -49,7 +50,7 @@ int lora_add(const void* base, int base_type, int64_t ldb, const uint16_t* x, in
 /* y[t] = linear_i8f16's product + delta[t]: the dense int8 linear with f16
  * scales and its adapters in one product. x, codes, scales, y as for
  * linear_i8f16 (K % 128 == 0, N % 16 == 0), the adapters and limits as above;
- * T * K < 2^31, T <= 16 * 65535 (else I8H_EUNSUPPORTED). y overlaps no input. */
+ * T * K < 2^31 (else I8H_EUNSUPPORTED). y overlaps no input. */
 int linear_i8f16_lora(const uint16_t* x, int T, int K, const int8_t* codes, const uint16_t* scales, int N,
                       const uint16_t* lora_a, const uint16_t* lora_b, int L, int R, const int32_t* adapter,
                       const float* lora_scale, float* y, void* workspace, size_t workspace_bytes, void* stream);

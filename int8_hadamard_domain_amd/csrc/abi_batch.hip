@@ -16,7 +16,10 @@ using i8h::kMaxTopk;
 constexpr int kLoraMaxN = 1 << 22;      // grid rows of 64 columns and more
 constexpr int kLoraMaxK = 1 << 22;      // rows of a tile are addressed with 32-bit offsets
 constexpr int64_t kLoraMaxLd = 1 << 24;
-constexpr int kLoraMaxT = 1 << 26;      // a workgroup of 512 threads per 16 rows: fewer than 2^32 threads
+constexpr int kLoraMaxT = 1 << 26;
+// A launch holds fewer than 2^32 threads: workgroups of 256 take 32 x 256 of the output, of 512 (the linear) 128 x 128,
+// and ragged edges make them fewer than four times as many.
+constexpr int64_t kLoraMaxOutput = (int64_t)1 << 35;
 
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 inline int from_hip(hipError_t e) { return e == hipSuccess ? I8H_OK : I8H_EHIP; }
@@ -27,12 +30,20 @@ inline size_t type_size(int t) { return t == I8H_F32 ? 4 : 2; }
 
 // rows x cols elements, rows ld elements apart
 struct Span {
-  uintptr_t from, to;
+  uintptr_t from, to, width, step;        // bytes: the whole, of a row, from row to row
   Span(const void* p, int64_t rows, int64_t cols, int64_t ld, size_t size) {
     from = reinterpret_cast<uintptr_t>(p);
     to = from + size * (uintptr_t)((rows - 1) * ld + cols);
+    width = size * (uintptr_t)cols;
+    step = size * (uintptr_t)ld;
   }
-  bool meets(const Span& o) const { return from < o.to && o.from < to; }
+  bool meets(const Span& o) const {
+    if (from >= o.to || o.from >= to) return false;
+    if (step != o.step) return true;
+    // rows the same distance apart: column slices of one matrix do not meet where their columns do not
+    const uintptr_t d = o.from >= from ? (o.from - from) % step : (step - (from - o.from) % step) % step;
+    return d < width || step - d < o.width;
+  }
 };
 
 // whether the output meets what the kernels still read while they write it
@@ -102,6 +113,7 @@ int lora_add(const void* base, int base_type, int64_t ldb, const uint16_t* x, in
     return I8H_EINVAL;
   if (ldb < N || ldo < N || ldx < K || (ldx % 8) != 0) return I8H_EINVAL;
   if (R > I8H_LORA_MAX_RANK || N > kLoraMaxN || T > kLoraMaxT || K > kLoraMaxK) return I8H_EUNSUPPORTED;
+  if ((int64_t)T * N > kLoraMaxOutput) return I8H_EUNSUPPORTED;
   if (ldb > kLoraMaxLd || ldo > kLoraMaxLd || ldx > kLoraMaxLd) return I8H_EUNSUPPORTED;
   const int rc = check_lora(x, T, lora_a, lora_b, R, adapter, lora_scale, workspace, workspace_bytes);
   if (rc != I8H_OK || T == 0) return rc;
@@ -129,7 +141,7 @@ int linear_i8f16_lora(const uint16_t* x, int T, int K, const int8_t* codes, cons
   if (T < 0 || K <= 0 || (K % 128) != 0 || N <= 0 || (N % 16) != 0 || L <= 0 || R <= 0 || (R % 8) != 0)
     return I8H_EINVAL;
   if (R > I8H_LORA_MAX_RANK || N > kLoraMaxN || K > kLoraMaxK || (int64_t)T * K >= (int64_t)1 << 31) return I8H_EUNSUPPORTED;
-  if ((int64_t)T > (int64_t)65535 * 16) return I8H_EUNSUPPORTED;       // a grid row per 16 tokens
+  if (T > kLoraMaxT || (int64_t)T * N > kLoraMaxOutput) return I8H_EUNSUPPORTED;
   const int rc = check_lora(x, T, lora_a, lora_b, R, adapter, lora_scale, workspace, workspace_bytes);
   if (rc != I8H_OK || T == 0) return rc;
   if (!codes || !scales || !y || !aligned(codes, 16) || !aligned(scales, 2) || !aligned(y, 4)) return I8H_EINVAL;

@@ -105,7 +105,7 @@ def test_linear_lora_validation(L):
     for bad in (dict(y=A[0]), dict(y=A[1]), dict(y=A[2]), dict(y=A[3]), dict(y=A[4]), dict(y=A[5]), dict(y=A[6]),
                 dict(y=A[7])):
         assert call(**bad) == EINVAL, bad
-    for bad in (dict(R=264), dict(N=(1 << 22) + 16), dict(T=1 << 24), dict(T=1 << 21)):
+    for bad in (dict(R=264), dict(N=(1 << 22) + 16), dict(T=1 << 24), dict(T=1 << 21, N=1 << 15)):
         assert call(**bad) == EUNSUP, bad
     assert call(T=0) == OK
 
@@ -126,3 +126,27 @@ def test_binding_refuses_tensors_off_the_gpu():
         i8h.lora_add(torch.zeros(2, 16, dtype=torch.float64), *args[1:])
     with pytest.raises(ValueError, match="GPU"):
         i8h.linear_i8f16_lora(args[1], torch.zeros(16, 64, dtype=torch.int8), torch.zeros(16, 0), *args[2:])
+
+
+def test_limits(L):
+    """The documented limits: at them a call is taken (shown with T = 0), past them it is refused."""
+    need = L.lora_workspace_size(9, 16)
+
+    def add(**kw):
+        v = dict(lora_kwargs(need), **kw)
+        return L.lora_add(v["base"], v["bt"], v["ldb"], v["x"], v["ldx"], v["T"], v["K"], v["N"], v["a"], v["b"],
+                          v["L_"], v["R"], v["ad"], v["sc"], v["out"], v["ldo"], v["ws"], v["wsb"], None)
+    m = 1 << 22
+    for ok, bad in ((dict(K=m, ldx=m), dict(K=m + 8, ldx=m + 8)), (dict(N=m, ldb=m, ldo=m), dict(N=m + 1, ldb=m + 1, ldo=m + 1)),
+                    (dict(ldb=1 << 24), dict(ldb=(1 << 24) + 1)), (dict(ldo=1 << 24), dict(ldo=(1 << 24) + 1)),
+                    (dict(ldx=1 << 24), dict(ldx=(1 << 24) + 8)), (dict(R=256), dict(R=264)),
+                    (dict(), dict(T=(1 << 13) + 1, N=m, ldb=m, ldo=m))):
+        assert add(T=0, **ok) == OK and add(**bad) == EUNSUP, (ok, bad)
+
+    def linear(T, K, N, R):
+        return L.linear_i8f16_lora(A[1], T, K, A[0], A[6], N, A[2], A[3], 3, R, A[4], A[5], A[8], A[7], need, None)
+    assert linear(0, m, m, 256) == OK
+    for bad in ((9, m + 128, 48, 16), (9, 128, m + 16, 16), (9, 128, 48, 264), (512, m, 48, 16), ((1 << 20) + 1, 128, 1 << 15, 16)):
+        assert linear(*bad) == EUNSUP, bad
+    for T, R in ((1, 8), (64, 64), (1 << 20, 256), ((1 << 26), 256)):
+        assert L.lora_workspace_size(T, R) >= 4 * T * R
