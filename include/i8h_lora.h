@@ -26,8 +26,10 @@ extern "C" {
 #define I8H_LORA_MAX_RANK 256
 
 /* Device scratch of both calls, in bytes: the inner sums, T x R float32, in up
- * to 8 slices of K. */
+ * to 8 slices of K. lora_add takes none for few rows (T and R <= 64): its own
+ * size is 0 there, else the same. */
 size_t lora_workspace_size(int T, int R);
+size_t lora_add_workspace_size(int T, int R);
 
 /* out[t] = base[t] + delta[t]: adapters beside any projection, base being its
  * output. base and out [T, N] of base_type (I8H_F32 or I8H_BF16: the float32
@@ -40,8 +42,8 @@ size_t lora_workspace_size(int T, int R);
  * lora_scale [L] float32. K % 8 == 0, R % 8 == 0, L >= 1, any N >= 1 (else
  * I8H_EINVAL); R <= I8H_LORA_MAX_RANK, N and K <= 2^22, T <= 2^26, T * N <=
  * 2^35, row distances <= 2^24 (else I8H_EUNSUPPORTED).
- * workspace: at least lora_workspace_size(T, R) bytes, 256-B aligned,
- * contents on entry ignored. */
+ * workspace: at least lora_add_workspace_size(T, R) bytes, 256-B aligned,
+ * contents on entry ignored (may be NULL when that size is 0). */
 int lora_add(const void* base, int base_type, int64_t ldb, const uint16_t* x, int64_t ldx, int T, int K, int N,
              const uint16_t* lora_a, const uint16_t* lora_b, int L, int R, const int32_t* adapter,
              const float* lora_scale, void* out, int64_t ldo, void* workspace, size_t workspace_bytes,
@@ -50,7 +52,8 @@ int lora_add(const void* base, int base_type, int64_t ldb, const uint16_t* x, in
 /* y[t] = linear_i8f16's product + delta[t]: the dense int8 linear with f16
  * scales and its adapters in one product. x, codes, scales, y as for
  * linear_i8f16 (K % 128 == 0, N % 16 == 0), the adapters and limits as above;
- * T * K < 2^31 (else I8H_EUNSUPPORTED). y overlaps no input. */
+ * T * K < 2^31 (else I8H_EUNSUPPORTED). y overlaps no input. workspace: at
+ * least lora_workspace_size(T, R) bytes. */
 int linear_i8f16_lora(const uint16_t* x, int T, int K, const int8_t* codes, const uint16_t* scales, int N,
                       const uint16_t* lora_a, const uint16_t* lora_b, int L, int R, const int32_t* adapter,
                       const float* lora_scale, float* y, void* workspace, size_t workspace_bytes, void* stream);

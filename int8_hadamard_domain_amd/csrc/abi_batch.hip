@@ -52,16 +52,16 @@ bool meets_lora(const Span& o, const uint16_t* x, int64_t T, int64_t K, int64_t 
                 const void* workspace, size_t workspace_bytes) {
   return o.meets(Span(x, T, K, ldx, 2)) || o.meets(Span(a, L, R * K, R * K, 2)) ||
          o.meets(Span(b, L, N * R, N * R, 2)) || o.meets(Span(adapter, 1, T, T, 4)) ||
-         o.meets(Span(scale, 1, L, L, 4)) || o.meets(Span(workspace, 1, workspace_bytes, 0, 1));
+         o.meets(Span(scale, 1, L, L, 4)) || (workspace_bytes > 0 && o.meets(Span(workspace, 1, workspace_bytes, 1, 1)));
 }
 
-int check_lora(const uint16_t* x, int T, const uint16_t* a, const uint16_t* b, int R, const int32_t* adapter, const float* scale,
-               const void* workspace, size_t workspace_bytes) {
+int check_lora(const uint16_t* x, int T, const uint16_t* a, const uint16_t* b, const int32_t* adapter, const float* scale,
+               const void* workspace, size_t workspace_bytes, size_t need) {
   if (T == 0) return I8H_OK;
-  if (!x || !a || !b || !adapter || !scale || !workspace) return I8H_EINVAL;
+  if (!x || !a || !b || !adapter || !scale) return I8H_EINVAL;
   if (!aligned(x, 16) || !aligned(a, 16) || !aligned(b, 16) || !aligned(adapter, 4) || !aligned(scale, 4))
     return I8H_EINVAL;
-  if (!aligned(workspace, 256) || workspace_bytes < lora_workspace_size(T, R)) return I8H_EINVAL;
+  if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return I8H_EINVAL;
   return I8H_OK;
 }
 
@@ -105,6 +105,8 @@ size_t lora_workspace_size(int T, int R) {
   return round_up((size_t)i8h::lora_slices(T) * T * R * sizeof(float), 256);
 }
 
+size_t lora_add_workspace_size(int T, int R) { return i8h::lora_few(T, R) ? 0 : lora_workspace_size(T, R); }
+
 int lora_add(const void* base, int base_type, int64_t ldb, const uint16_t* x, int64_t ldx, int T, int K, int N,
              const uint16_t* lora_a, const uint16_t* lora_b, int L, int R, const int32_t* adapter,
              const float* lora_scale, void* out, int64_t ldo, void* workspace, size_t workspace_bytes,
@@ -115,13 +117,14 @@ int lora_add(const void* base, int base_type, int64_t ldb, const uint16_t* x, in
   if (R > I8H_LORA_MAX_RANK || N > kLoraMaxN || T > kLoraMaxT || K > kLoraMaxK) return I8H_EUNSUPPORTED;
   if ((int64_t)T * N > kLoraMaxOutput) return I8H_EUNSUPPORTED;
   if (ldb > kLoraMaxLd || ldo > kLoraMaxLd || ldx > kLoraMaxLd) return I8H_EUNSUPPORTED;
-  const int rc = check_lora(x, T, lora_a, lora_b, R, adapter, lora_scale, workspace, workspace_bytes);
+  const size_t need = lora_add_workspace_size(T, R);
+  const int rc = check_lora(x, T, lora_a, lora_b, adapter, lora_scale, workspace, workspace_bytes, need);
   if (rc != I8H_OK || T == 0) return rc;
   const size_t el = type_size(base_type);
   if (!base || !out || !aligned(base, el) || !aligned(out, el)) return I8H_EINVAL;
   const Span o(out, T, N, ldo, el);
   if (base == out ? ldb != ldo : o.meets(Span(base, T, N, ldb, el))) return I8H_EINVAL;
-  if (meets_lora(o, x, T, K, ldx, N, lora_a, lora_b, L, R, adapter, lora_scale, workspace, workspace_bytes))
+  if (meets_lora(o, x, T, K, ldx, N, lora_a, lora_b, L, R, adapter, lora_scale, workspace, need))
     return I8H_EINVAL;
   hipStream_t st = as_stream(stream);
   if (i8h::lora_few(T, R))
@@ -142,12 +145,13 @@ int linear_i8f16_lora(const uint16_t* x, int T, int K, const int8_t* codes, cons
     return I8H_EINVAL;
   if (R > I8H_LORA_MAX_RANK || N > kLoraMaxN || K > kLoraMaxK || (int64_t)T * K >= (int64_t)1 << 31) return I8H_EUNSUPPORTED;
   if (T > kLoraMaxT || (int64_t)T * N > kLoraMaxOutput) return I8H_EUNSUPPORTED;
-  const int rc = check_lora(x, T, lora_a, lora_b, R, adapter, lora_scale, workspace, workspace_bytes);
+  const size_t need = lora_workspace_size(T, R);
+  const int rc = check_lora(x, T, lora_a, lora_b, adapter, lora_scale, workspace, workspace_bytes, need);
   if (rc != I8H_OK || T == 0) return rc;
   if (!codes || !scales || !y || !aligned(codes, 16) || !aligned(scales, 2) || !aligned(y, 4)) return I8H_EINVAL;
   const Span o(y, T, N, N, 4);
   if (o.meets(Span(codes, N, K, K, 1)) || o.meets(Span(scales, N, K / 128, K / 128, 2)) ||
-      meets_lora(o, x, T, K, K, N, lora_a, lora_b, L, R, adapter, lora_scale, workspace, workspace_bytes))
+      meets_lora(o, x, T, K, K, N, lora_a, lora_b, L, R, adapter, lora_scale, workspace, need))
     return I8H_EINVAL;
   hipStream_t st = as_stream(stream);
   float* h = static_cast<float*>(workspace);
