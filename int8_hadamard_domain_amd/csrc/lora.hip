@@ -438,8 +438,10 @@ int lora_slices(int T) { return std::max(1, std::min(kLoraSlices, 512 / ((T - 1)
 hipError_t launch_lora_shrink(const uint16_t* x, int64_t ldx, int T, int K, const uint16_t* a, int L, int R,
                               const int32_t* adapter, const float* scale, float* h, int* slices, hipStream_t st) {
   *slices = std::min(lora_slices(T), cdiv(K, kShK));
-  // while rows are few, workgroups of their own for up to 16 of a tile's adapters
-  const int spread = T <= 1024 ? std::min({16, T, L}) : 1;
+  // While rows are few, workgroups of their own for several of a tile's adapters. Measured, us with 1, 2, 4 and 16 of
+  // them: 1024 rows of 64 requests (rank 32, and the linear with it) -, -, 40.8, 42.7; 2048 rows of five requests (rank 64,
+  // and the add) 24.4, 21.3, 22.4, -; 4096 rows of five 32.9, -, 35.3, -.
+  const int spread = std::min({T <= 512 ? 8 : T <= 1024 ? 4 : T <= 2048 ? 2 : 1, T, L});
   const int rgroups = R <= 64 ? 1 : cdiv(R, 64);
   const int wgs = cdiv(T, kShRows) * *slices * rgroups * spread, grid = cdiv(wgs, kXcds) * kXcds;
 #define I8H_SHRINK(NG)                                                                                            \
