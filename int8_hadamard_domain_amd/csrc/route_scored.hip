@@ -43,6 +43,8 @@ constexpr int sc_waves() { return VPL <= 4 ? 16 : 64 / VPL; }
 struct ScoredRule {
   const float* bias;       // [E] or NULL
   int E, k, groups, keep, top;
+  int size;                // experts a group
+  int lanes;               // log2 of a group's lanes, -1 where a group is not a power of two of whole lanes
   bool sigmoid, renorm;
   float scale;
 };
@@ -167,7 +169,7 @@ __device__ __forceinline__ float exp_carried(float x) {
 template <int VPL>
 __device__ __forceinline__ uint64_t groups_float64(const uint64_t (&value)[VPL], const ScoredRule& R, bool sum, int lane,
                                                    uint64_t* lds) {
-  const int size = R.E / R.groups;
+  const int size = R.size;
   wave_order();
 #pragma unroll
   for (int i = 0; i < VPL; ++i)
@@ -252,11 +254,10 @@ __device__ __forceinline__ bool choose(const float (&v)[VPL], const float (&b)[V
 #pragma unroll
       for (int i = 0; i < VPL; ++i) value[i] = by_logit && R.top == 2 ? order_key64(s[i]) : key[i];
       const uint64_t stays = groups_float64<VPL>(value, R, R.top == 2, lane, reinterpret_cast<uint64_t*>(lds));
-      const int size = E / R.groups;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
         const int e = min(VPL * lane + i, E - 1);
-        kv[i] = (stays >> (e / size)) & 1 ? max((uint32_t)(key[i] >> 32), 1u) : 0u;
+        kv[i] = (stays >> (e / R.size)) & 1 ? max((uint32_t)(key[i] >> 32), 1u) : 0u;
       }
     } else {
 #pragma unroll
@@ -307,9 +308,9 @@ __device__ __forceinline__ bool choose(const float (&v)[VPL], const float (&b)[V
       if (__ballot(!(fabsf(test) < INFINITY)) != 0) return false;
     }
     if (limited) {
-      const int size = E / R.groups, lpg = size / VPL;
-      // whole lanes a group, a power of two of them
-      const bool lanes = size == lpg * VPL && (lpg & (lpg - 1)) == 0;
+      const int size = R.size;
+      const bool lanes = R.lanes >= 0;                 // (no division here: a third of this block's instructions)
+      const int lpg = lanes ? 1 << R.lanes : 0;
       const bool exact = by_logit && R.top == 1;
       uint32_t wk = 0;                                 // exact: the largest key
       float wa = -INFINITY, wb = -INFINITY;            // else the two largest values
@@ -349,22 +350,22 @@ __device__ __forceinline__ bool choose(const float (&v)[VPL], const float (&b)[V
           }
         }
       }
-      const int step = lanes ? lpg : 1;                // group g's worth is lane g * step's
-      const int mine = lane / step;
+      const int shift = lanes ? R.lanes : 0;           // group g's worth is lane g << shift's
+      const int mine = lane >> shift;
       const bool live = mine < R.groups;
       int above = 0;                                   // groups (surely) of more worth
       if (exact) {
         for (int g = 0; g < R.groups; ++g) {
-          const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)wk, g * step);
+          const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)wk, g << shift);
           above += o > wk || (o == wk && g < mine) ? 1 : 0;
         }
       } else {
         const float w = R.top == 2 ? wa + wb : wa;
         const float up = w + (2.0f * unit + 0x1p-21f * (fabsf(wa) + (R.top == 2 ? fabsf(wb) : 0.0f)));
         for (int g = 0; g < R.groups; ++g)
-          above += __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w), g * step)) > up ? 1 : 0;
+          above += __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w), g << shift)) > up ? 1 : 0;
         // the `keep` best are below that many at most: no others, or the border is not sure
-        if (__popcll(__ballot(live && above < R.keep)) != R.keep * step) return false;
+        if (__popcll(__ballot(live && above < R.keep)) != R.keep << shift) return false;
       }
       if (lanes) {
 #pragma unroll
@@ -916,7 +917,9 @@ hipError_t launch_route_scored(const void* logits, bool bf16, int T, int E, int 
                                int groups, int keep, int top, bool renorm, float scale, int32_t* ids, float* w,
                                int32_t* expert_off, int32_t* sorted_pairs, int32_t* pair_pos, void* ws,
                                hipStream_t st) {
-  const ScoredRule R = {bias, E, k, groups, keep, top, sigmoid, renorm, scale};
+  const int size = E / groups, vpl = vpl_of(E), lpg = size / vpl;
+  const bool whole = size == lpg * vpl && (lpg & (lpg - 1)) == 0;
+  const ScoredRule R = {bias, E, k, groups, keep, top, size, whole ? __builtin_ctz(lpg) : -1, sigmoid, renorm, scale};
   if (bf16) return launch<uint16_t>(logits, T, R, ids, w, expert_off, sorted_pairs, pair_pos, ws, st);
   return launch<float>(logits, T, R, ids, w, expert_off, sorted_pairs, pair_pos, ws, st);
 }
