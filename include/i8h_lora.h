@@ -26,8 +26,8 @@ extern "C" {
 #define I8H_LORA_MAX_RANK 256
 
 /* Device scratch of both calls, in bytes: the inner sums, T x R float32, in up
- * to 8 slices of K. lora_add takes none for few rows (T and R <= 64): its own
- * size is 0 there, else the same. */
+ * to 8 slices of K. lora_add takes none for few rows of low rank (T <= 256,
+ * R <= 64, T * R <= 4096): its own size is 0 there, else the same. */
 size_t lora_workspace_size(int T, int R);
 size_t lora_add_workspace_size(int T, int R);
 

@@ -6,20 +6,33 @@
 // A workgroup of eight waves owns 16 MT tokens x 16 NT WN columns. WK waves
 // share a wave's columns and split the K groups; the others stand side by side
 // along N. A stage is WK groups of K: the tokens' rows go through LDS, whole
-// lines a row, the next stage's copies in flight behind this one's products
-// (two buffers, one barrier a stage); each wave streams its codes
-// into registers (64 contiguous bytes a row), a group ahead, and decodes them
-// to bf16 (exact) once for all its tokens. Per group a wave runs
-// v_mfma_f32_16x16x32_bf16 from zero accumulators and folds the sums into its
-// float32 result with the column's scale. The K positions of an operand are
-// dealt so that a lane's codes are whole 16-byte loads: of the 64 positions
-// 64 j .. of a group's half, lane quarter q holds 16 q .. 16 q + 15, and MFMA
-// 2 j + u takes 8 u .. 8 u + 7 of them, of both operands alike.
+// lines a row, BUFS - 1 stages' copies in flight behind this one's products (one
+// barrier a stage); each wave streams its codes into registers (64 contiguous
+// bytes a row), as far ahead, and decodes them to bf16 (exact) once for all its
+// tokens. Per group a wave runs v_mfma_f32_16x16x32_bf16 from zero accumulators
+// and folds the sums into its float32 result with the column's scale. The K
+// positions of an operand are dealt so that a lane's codes are whole 16-byte
+// loads: of the 64 positions 64 j .. of a group's half, lane quarter q holds
+// 16 q .. 16 q + 15, and MFMA 2 j + u takes 8 u .. 8 u + 7 of them, of both
+// operands alike.
 //
 // At the end the WK waves' results meet in LDS, each wave taking its share of
 // the token tiles, and the adapters' products are added from there: h in three
 // bf16 parts (their sum is the float32 value), the rows of other adapters
 // dropped after the product.
+//
+// Measured (4096 x 2048, medians, without the shrink): 16 tokens of rank 16 7.0
+// us, 128 tokens 14.2 (both bound by the chain first loads, stages, join,
+// adapters), 1024 tokens of rank 32 34.6 us: 496 TFLOP/s. Of its 65,000 cycles
+// 8,000 go by before the first products (every CU asks for its first 96 KB at
+// once), 11,000 in the join and the adapters; each of the eight stages takes
+// 5,500, of which the matrix units need 2,050: the tokens' copies go at 31 bytes
+// a clock and CU, as long as the products, and codes of 16 bytes a row at 15.
+// Tried at that size and not kept: copies dealt between the products (42.2
+// against 40.9 us with the shrink), codes loaded 64 bytes a quad of lanes and
+// exchanged between lanes and registers (43.4), the next stage's decoding between
+// this one's products with both of these (40.3, and 69.8 against 69.9 at 2048
+// tokens), codes through LDS as well (55), two workgroups of four waves a CU (47).
 
 #include <algorithm>
 #include <type_traits>

@@ -49,6 +49,10 @@ __device__ __forceinline__ u32x4 load16(const void* p, uint32_t off) {
   return *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(p) + off);
 }
 
+// (12.0 us for 2048 rows of K = 4096 and rank 64, five requests: 1.4 TB/s; 14 us
+// for 8191 rows of K = 2048 and rank 32. Bound by the chain adapter, first loads,
+// four or eight stages, sums in LDS: the loads of two stages in flight are all
+// that the registers hold.)
 // h of 64 rows, 16 NG columns of R and a slice of K, for the adapters that the
 // rows name (each `every`-th of them, from its own on). Stages of
 // 128 of K go through LDS, whole lines a row, the next two's loads in flight
@@ -93,72 +97,94 @@ k_lora_shrink(const uint16_t* __restrict__ x, int64_t ldx, int T, int K, const u
   const uint16_t* xt = x + t0 * ldx;
   int ad = t0 + lane < T ? adapter[t0 + lane] : -1;          // lane: a row of the tile
   ad = (uint32_t)ad < (uint32_t)L ? ad : -1;
-  uint64_t left = __ballot(ad >= 0);
-  while (left != 0) {
-    const int l = __builtin_amdgcn_readlane(ad, __ffsll((unsigned long long)left) - 1);
-    const uint64_t mine = __ballot(ad == l);
-    left &= ~mine;
-    if (skip-- > 0) continue;
-    skip = every - 1;
+  uint64_t left = __ballot(ad >= 0), mine = 0;
+  int l = -1;
+  // the next of the workgroup's adapters, and its rows
+  const auto next = [&]() {
+    l = -1;
+    while (left != 0 && l < 0) {
+      const int at = __builtin_amdgcn_readlane(ad, __ffsll((unsigned long long)left) - 1);
+      const uint64_t of = __ballot(ad == at);
+      left &= ~of;
+      if (skip-- > 0) continue;
+      skip = every - 1;
+      l = at;
+      mine = of;
+    }
+  };
+  u32x4 xr[2][kXL], ar[2][kAL];
+  const auto load = [&](int to, int i) {
+    const int s = s0 + (i + turn < stages ? i + turn : i + turn - stages);
+    const bool in = kShK * s + 8 * piece < K;
     const uint16_t* al = a + (size_t)l * R * K;
-    u32x4 xr[2][kXL], ar[2][kAL];
-    const auto load = [&](int to, int i) {
-      const int s = s0 + (i + turn < stages ? i + turn : i + turn - stages);
-      const bool in = kShK * s + 8 * piece < K;
 #pragma unroll
-      for (int j = 0; j < kXL; ++j) {
-        xr[to][j] = {0u, 0u, 0u, 0u};
-        if (in && ((mine >> (row0 + kRowStep * j)) & 1))
-          xr[to][j] = load16(xt + kShK * s, 2u * ((uint32_t)(row0 + kRowStep * j) * (uint32_t)ldx + 8u * piece));
-      }
+    for (int j = 0; j < kXL; ++j) {
+      xr[to][j] = {0u, 0u, 0u, 0u};
+      if (in && ((mine >> (row0 + kRowStep * j)) & 1))
+        xr[to][j] = load16(xt + kShK * s, 2u * ((uint32_t)(row0 + kRowStep * j) * (uint32_t)ldx + 8u * piece));
+    }
 #pragma unroll
-      for (int j = 0; j < kAL; ++j) {
-        const int r = min(r0 + row0 + kRowStep * j, R - 1);
-        ar[to][j] = {0u, 0u, 0u, 0u};
-        if (in) ar[to][j] = load16(al + kShK * s, 2u * ((uint32_t)r * (uint32_t)K + 8u * piece));
+    for (int j = 0; j < kAL; ++j) {
+      const int r = min(r0 + row0 + kRowStep * j, R - 1);
+      ar[to][j] = {0u, 0u, 0u, 0u};
+      if (in) ar[to][j] = load16(al + kShK * s, 2u * ((uint32_t)r * (uint32_t)K + 8u * piece));
+    }
+  };
+  f32x4 acc[4][NG];
+  const auto stage = [&](int from, int s) {
+#pragma unroll
+    for (int j = 0; j < kXL; ++j) {
+      const int r = row0 + kRowStep * j;
+      xs[r * kPieces + (piece ^ (r % 16))] = xr[from][j];
+    }
+#pragma unroll
+    for (int j = 0; j < kAL; ++j) {
+      const int r = row0 + kRowStep * j;
+      as[r * kPieces + (piece ^ (r % 16))] = ar[from][j];
+    }
+    __syncthreads();
+    if (s + 2 < stages) load(from, s + 2);
+#pragma unroll
+    for (int q = 0; q < kPieces / 4 / kShWaves; ++q) {
+      const int p = 4 * (kPieces / 4 / kShWaves * wave + q) + kq;
+      bf16x8 av[NG];
+#pragma unroll
+      for (int g = 0; g < NG; ++g) av[g] = __builtin_bit_cast(bf16x8, as[(16 * g + c) * kPieces + (p ^ c)]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bf16x8 xv = __builtin_bit_cast(bf16x8, xs[(16 * i + c) * kPieces + (p ^ c)]);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) acc[i][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, av[g], acc[i][g], 0, 0, 0);
       }
-    };
-    f32x4 acc[4][NG];
+    }
+    __syncthreads();
+  };
+  next();
+  float f = 0.0f;
+  if (l >= 0) {
+    f = scale[l];
+    load(0, 0);
+    if (stages > 1) load(1, 1);
+  }
+  while (l >= 0) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int g = 0; g < NG; ++g) acc[i][g] = {0.f, 0.f, 0.f, 0.f};
-    const auto stage = [&](int from, int s) {
-#pragma unroll
-      for (int j = 0; j < kXL; ++j) {
-        const int r = row0 + kRowStep * j;
-        xs[r * kPieces + (piece ^ (r % 16))] = xr[from][j];
-      }
-#pragma unroll
-      for (int j = 0; j < kAL; ++j) {
-        const int r = row0 + kRowStep * j;
-        as[r * kPieces + (piece ^ (r % 16))] = ar[from][j];
-      }
-      __syncthreads();
-      if (s + 2 < stages) load(from, s + 2);
-#pragma unroll
-      for (int q = 0; q < kPieces / 4 / kShWaves; ++q) {
-        const int p = 4 * (kPieces / 4 / kShWaves * wave + q) + kq;
-        bf16x8 av[NG];
-#pragma unroll
-        for (int g = 0; g < NG; ++g) av[g] = __builtin_bit_cast(bf16x8, as[(16 * g + c) * kPieces + (p ^ c)]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const bf16x8 xv = __builtin_bit_cast(bf16x8, xs[(16 * i + c) * kPieces + (p ^ c)]);
-#pragma unroll
-          for (int g = 0; g < NG; ++g) acc[i][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, av[g], acc[i][g], 0, 0, 0);
-        }
-      }
-      __syncthreads();
-    };
-    load(0, 0);
-    if (stages > 1) load(1, 1);
     for (int s = 0; s < stages; s += 2) {
       stage(0, s);
       if (s + 1 < stages) stage(1, s + 1);
     }
+    // the next adapter's first loads are on their way while this one's sums are added up
+    const uint64_t done = mine;
+    const float by = f;
+    next();
+    if (l >= 0) {
+      f = scale[l];
+      load(0, 0);
+      if (stages > 1) load(1, 1);
+    }
     // the waves' sums, 32 rows at a time
-    const float f = scale[l];
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
 #pragma unroll
@@ -178,7 +204,7 @@ k_lora_shrink(const uint16_t* __restrict__ x, int64_t ldx, int T, int K, const u
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int row = 16 * (2 * half + tile / NG) + 4 * kq + i;
-          if (r < R && ((mine >> row) & 1)) h[((int64_t)slice * T + t0 + row) * R + r] = f * sum[i];
+          if (r < R && ((done >> row) & 1)) h[((int64_t)slice * T + t0 + row) * R + r] = by * sum[i];
         }
       }
       __syncthreads();
@@ -198,7 +224,9 @@ __device__ __forceinline__ void fma8(float& s, const u32x4& p, const u32x4& q) {
 // compute the row's R inner sums, a wave per sum (whole lines of A, 8 values a
 // lane and load; each workgroup of a row does it again, from L2), then a
 // thread per column multiplies them with its row of B, which is on its way
-// from the start. PIECES: 16-byte pieces of B a thread keeps (R <= 8 PIECES).
+// from the start. 3.3 us for one row of 2048 x 2048 and rank 16: a launch and two
+// loads that depend on each other; 6.7 us for 64 rows of 48 adapters, which read
+// each adapter's A once per row and 512 columns (L2). PIECES: 16-byte pieces of B a thread keeps (R <= 8 PIECES).
 template <bool BF16, int PIECES>
 __global__ void __launch_bounds__(kFewThreads)
 k_lora_few(const void* base, int64_t ldb, const uint16_t* __restrict__ x, int64_t ldx, int K, int N,
@@ -321,7 +349,9 @@ struct Piece {
 // layouts deal a row to lanes 16 apart; so base and out are loaded and stored
 // with 128 bytes of a row on neighbouring lanes, B 64 bytes of a row on four,
 // and a wave's own LDS turns B's rows and the products into the other order
-// (64 us without, 55 with, of 8191 x 4096 float32 rows).
+// (64 us without, 55 with, of 8191 x 4096 float32 rows: 268 MB at 4.8 TB/s, a
+// copy takes 45 here; 2048 x 2048 bf16 rows of rank 64 10.2 us, 1.6 TB/s, bound
+// by the chain of h, B and the products in each workgroup).
 template <bool BF16>
 __global__ void __launch_bounds__(kAddThreads, BF16 ? 3 : 4)
 k_lora_add(const void* base, int64_t ldb, int T, int N, const uint16_t* __restrict__ b, int L, int R,
@@ -368,9 +398,25 @@ k_lora_add(const void* base, int64_t ldb, int T, int N, const uint16_t* __restri
 #pragma unroll
         for (int j = 0; j < 2 * kNT; ++j) sum[m][j] = {0.f, 0.f, 0.f, 0.f};
       uint32_t left[2] = {rows[0], rows[1]};
-      while ((left[0] | left[1]) != 0) {
-        const int l = left[0] != 0 ? __builtin_amdgcn_readlane(ad[0], __ffs(left[0]) - 1)
-                                   : __builtin_amdgcn_readlane(ad[1], __ffs(left[1]) - 1);
+      // 32 of R of the pass's rows of B, a step ahead of their use: an adapter's first while the one before multiplies
+      u32x4 w[2 * kNT];
+      const auto fetch = [&](int l, int r0) {
+        const uint16_t* bl = b + ((size_t)l * N + ng) * R;
+#pragma unroll
+        for (int i = 0; i < 2 * kNT; ++i) {
+          const int nb = 16 * i + lane / 4, r = 8 * (lane % 4);
+          w[i] = {0u, 0u, 0u, 0u};
+          if ((FULL || ng + nb < N) && r0 + r < R) w[i] = load16(bl + r0, 2u * ((uint32_t)nb * (uint32_t)R + r));
+        }
+      };
+      const auto first = [&]() {
+        return left[0] != 0 ? __builtin_amdgcn_readlane(ad[0], __ffs(left[0]) - 1)
+                            : __builtin_amdgcn_readlane(ad[1], __ffs(left[1]) - 1);
+      };
+      int ahead = -1;
+      if ((left[0] | left[1]) != 0) fetch(ahead = first(), 0);
+      while (ahead >= 0) {
+        const int l = ahead;
         left[0] &= ~lora_rows(ad[0] == l);
         left[1] &= ~lora_rows(ad[1] == l);
         f32x4 d[2][2 * kNT];
@@ -378,16 +424,8 @@ k_lora_add(const void* base, int64_t ldb, int T, int N, const uint16_t* __restri
         for (int m = 0; m < 2; ++m)
 #pragma unroll
           for (int j = 0; j < 2 * kNT; ++j) d[m][j] = {0.f, 0.f, 0.f, 0.f};
-        const uint16_t* bl = b + ((size_t)l * N + ng) * R;
+        ahead = (left[0] | left[1]) != 0 ? first() : -1;
         for (int r0 = 0; r0 < R; r0 += 32) {
-          // 32 of R of the pass's rows of B
-          u32x4 w[2 * kNT];
-#pragma unroll
-          for (int i = 0; i < 2 * kNT; ++i) {
-            const int nb = 16 * i + lane / 4, r = 8 * (lane % 4);
-            w[i] = {0u, 0u, 0u, 0u};
-            if ((FULL || ng + nb < N) && r0 + r < R) w[i] = load16(bl + r0, 2u * ((uint32_t)nb * (uint32_t)R + r));
-          }
           lora_wave_order();
 #pragma unroll
           for (int i = 0; i < 2 * kNT; ++i)
@@ -397,6 +435,8 @@ k_lora_add(const void* base, int64_t ldb, int T, int N, const uint16_t* __restri
 #pragma unroll
           for (int j = 0; j < 2 * kNT; ++j)
             bv[j] = *reinterpret_cast<const bf16x8*>(own + (16 * j + c) * kAddBRow + 16 * kq);
+          if (r0 + 32 < R) fetch(l, r0 + 32);
+          else if (ahead >= 0) fetch(ahead, 0);
           lora_multiply<2, kNT>(bv, R, r0, sm, ld, lane, d);
         }
         // the rows of other adapters keep what they have, whatever this one holds
@@ -454,7 +494,14 @@ hipError_t launch_lora_shrink(const uint16_t* x, int64_t ldx, int T, int K, cons
   return hipGetLastError();
 }
 
-bool lora_few(int T, int R) { return T <= 64 && R <= 64; }
+// Few rows of low rank take one launch on the vector unit, which reads A and B once a row: what it costs grows with T R,
+// and it does not mind that every row has another adapter; the two kernels work once for each adapter of a tile. Measured
+// (2048 x 4096 bf16, 48 adapters), us here and there with as many requests as rows, then with 4 (128 rows: 8) requests:
+//    64 rows, rank 16    6.4  36.8     3.9   9.7      256 rows, rank 16   14.9  37.4     9.5   9.6
+//    64 rows, rank 64   23.9  54.4    20.5  13.2      512 rows, rank 8    22.4  39.1    22.8  10.8
+//   128 rows, rank 16    9.3  37.4     6.8  10.5      128 rows, rank 64   44.0  58.0    33.3  16.1
+// (the left column is taken, the right one is not)
+bool lora_few(int T, int R) { return T <= 256 && R <= 64 && T * R <= 4096; }
 
 hipError_t launch_lora_few(const void* base, bool bf16, int64_t ldb, const uint16_t* x, int64_t ldx, int T, int K,
                            int N, const uint16_t* a, const uint16_t* b, int L, int R, const int32_t* adapter,

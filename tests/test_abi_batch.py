@@ -62,17 +62,18 @@ def test_scored_routing_validation(L):
 
 
 def lora_kwargs(need):
-    return dict(base=A[0], bt=0, ldb=100, x=A[1], ldx=64, T=70, K=64, N=100, a=A[2], b=A[3], L_=3, R=16, ad=A[4],
+    return dict(base=A[0], bt=0, ldb=100, x=A[1], ldx=64, T=300, K=64, N=100, a=A[2], b=A[3], L_=3, R=16, ad=A[4],
                 sc=A[5], out=A[6], ldo=100, ws=A[7], wsb=need)
 
 
 def test_lora_add_validation(L):
-    need = L.lora_add_workspace_size(70, 16)
-    assert need >= 70 * 16 * 4 and need % 256 == 0 and need == L.lora_workspace_size(70, 16)
+    need = L.lora_add_workspace_size(300, 16)
+    assert need >= 300 * 16 * 4 and need % 256 == 0 and need == L.lora_workspace_size(300, 16)
     assert L.lora_workspace_size(0, 16) == 0 and L.lora_workspace_size(9, 0) == 0 and L.lora_add_workspace_size(0, 0) == 0
     # few rows take none
     assert L.lora_add_workspace_size(64, 64) == 0 and L.lora_add_workspace_size(64, 72) > 0
-    assert L.lora_add_workspace_size(65, 8) > 0 and L.lora_workspace_size(9, 16) > 0
+    assert L.lora_add_workspace_size(65, 64) > 0 and L.lora_add_workspace_size(256, 16) == 0
+    assert L.lora_add_workspace_size(257, 8) > 0 and L.lora_workspace_size(9, 16) > 0
 
     def call(**kw):
         v = dict(lora_kwargs(need), **kw)
@@ -87,7 +88,7 @@ def test_lora_add_validation(L):
     # out may be base, with the same rows; it may meet no other input, nor base in part
     for bad in (dict(out=A[0], ldo=104), dict(out=P(A[0].value + 4)), dict(out=P(A[0].value - 4)), dict(out=A[1]),
                 dict(out=A[2]), dict(out=A[3]), dict(out=A[4]), dict(out=A[5]), dict(out=A[7]),
-                dict(out=P(A[1].value - 4 * 6999)), dict(out=P(A[2].value + 2 * 3 * 16 * 64 - 4))):
+                dict(out=P(A[1].value - 4 * 29999)), dict(out=P(A[2].value + 2 * 3 * 16 * 64 - 4))):
         assert call(**bad) == EINVAL, bad
     for bad in (dict(R=264), dict(N=(1 << 22) + 1, ldb=1 << 23, ldo=1 << 23), dict(T=(1 << 26) + 1), dict(T=MAX)):
         assert call(**bad) == EUNSUP, bad
@@ -133,7 +134,7 @@ def test_binding_refuses_tensors_off_the_gpu():
 
 def test_limits(L):
     """The documented limits: at them a call is taken (shown with T = 0), past them it is refused."""
-    need = L.lora_workspace_size(70, 16)
+    need = L.lora_workspace_size(300, 16)
 
     def add(**kw):
         v = dict(lora_kwargs(need), **kw)

@@ -61,7 +61,8 @@ def test_linear_tiles_keep_broken_adapters_to_their_rows(gpu_available, T, N):
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("T,K,N,R,L,kind", [(66, 72, 700, 256, 3, "mixed"), (64, 64, 300, 64, 70, "mixed"),
-                                            (64, 64, 300, 72, 9, "mixed"), (300, 520, 259, 200, 40, "mixed"),
+                                            (64, 64, 300, 72, 9, "mixed"), (128, 264, 700, 32, 40, "mixed"), (129, 264, 700, 32, 40, "mixed"),
+                                            (256, 520, 300, 16, 50, "mixed"), (257, 520, 300, 16, 50, "mixed"), (300, 520, 259, 200, 40, "mixed"),
                                             (1025, 40, 77, 24, 200, "mixed"), (5000, 136, 300, 72, 3, "runs")])
 def test_add_sizes(gpu_available, T, K, N, R, L, kind, dtype):
     print(f"add sizes T={T} K={K} N={N} R={R} L={L} {kind} {dtype}", flush=True)
@@ -90,7 +91,7 @@ def test_rows_far_apart(gpu_available, T):
     assert torch.equal(vb, want) and torch.equal(vx, x)
 
 
-@pytest.mark.parametrize("T", [9, 100])
+@pytest.mark.parametrize("T", [9, 300])
 def test_slices_side_by_side(gpu_available, T):
     """base, out and x as slices of one matrix, next to each other: nothing but out's columns changes."""
     N = K = 64

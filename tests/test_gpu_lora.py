@@ -201,7 +201,7 @@ def test_refusals(gpu_available):
                 (base, x, a, b, ad.long(), s), (base, x, a, b, ad, s.double())):
         with pytest.raises(TypeError):
             i8h.lora_add(*bad)
-    big = problem(65, 64, 16, 8, 2, "one", F32)
+    big = problem(300, 64, 16, 8, 2, "one", F32)
     with pytest.raises(ValueError):
         i8h.lora_add(*big[:4], big[5], big[4], workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
     with pytest.raises(i8h.I8HError):                                   # ranks are multiples of 8
