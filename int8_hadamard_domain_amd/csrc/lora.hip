@@ -33,7 +33,6 @@ constexpr int kShK = 128;
 constexpr int kFewWaves = 8;
 constexpr int kFewThreads = kWave * kFewWaves;
 constexpr int kAddThreads = 256;               // the add kernel: rows and columns of a step
-constexpr int kAddRows = 32;
 constexpr int kAddCols = 256;
 constexpr int kAddBRow = 80;                   // bytes of LDS of a row of B, 32 of R: 64 and 16 of padding
 
@@ -343,7 +342,7 @@ struct Piece {
   }
 };
 
-// out of 32 rows and 256 columns, 64 a wave. h is added up over its slices
+// out of 16 MT rows and 256 columns, 64 a wave. h is added up over its slices
 // once a workgroup and lies in LDS in three bf16 parts. Neighbouring lanes are
 // served together only where they take neighbouring bytes, and the matrix
 // layouts deal a row to lanes 16 apart; so base and out are loaded and stored
@@ -352,30 +351,33 @@ struct Piece {
 // (64 us without, 55 with, of 8191 x 4096 float32 rows: 268 MB at 4.8 TB/s, a
 // copy takes 45 here; 2048 x 2048 bf16 rows of rank 64 10.2 us, 1.6 TB/s, bound
 // by the chain of h, B and the products in each workgroup).
-template <bool BF16>
+template <bool BF16, int MT>
 __global__ void __launch_bounds__(kAddThreads, BF16 ? 3 : 4)
 k_lora_add(const void* base, int64_t ldb, int T, int N, const uint16_t* __restrict__ b, int L, int R,
            const int32_t* __restrict__ adapter, const float* __restrict__ h, int slices, int colgroups, int wgs,
            void* out, int64_t ldo, bool vec) {
   using P = Piece<BF16>;
   constexpr int kNT = BF16 ? 2 : 1, kPasses = 2 / kNT, kCols = 32 * kNT;             // columns a pass: 128 bytes a row
-  constexpr int kLpr = kCols / P::kE, kRpc = kWave / kLpr, kChunks = kAddRows / kRpc;   // lanes a row, rows a load
+  constexpr int kLpr = kCols / P::kE, kRpc = kWave / kLpr, kRows = 16 * MT, kChunks = kRows / kRpc;   // lanes a row, rows a load
   extern __shared__ __align__(16) uint8_t sm[];
   const int tid = threadIdx.x, lane = tid % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int c = lane % 16, kq = lane / 16;
   const int wg = xcd_run(blockIdx.x, gridDim.x);
   if (wg >= wgs) return;
-  const int64_t t0 = (int64_t)(wg / colgroups) * kAddRows;
-  int ad[2];
-  ad[0] = lora_row_adapter(adapter, t0, T, L, c);
-  ad[1] = lora_row_adapter(adapter, t0, T, L, 16 + c);
-  const uint32_t rows[2] = {lora_rows(ad[0] >= 0), lora_rows(ad[1] >= 0)};
+  const int64_t t0 = (int64_t)(wg / colgroups) * kRows;
+  int ad[MT];
+  uint32_t rows[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    ad[m] = lora_row_adapter(adapter, t0, T, L, 16 * m + c);
+    rows[m] = lora_rows(ad[m] >= 0);
+  }
   const int n0 = wg % colgroups * kAddCols + 64 * wave;
   const void* from = static_cast<const uint8_t*>(base) + t0 * ldb * (BF16 ? 2 : 4);
   void* to = static_cast<uint8_t*>(out) + t0 * ldo * (BF16 ? 2 : 4);
   const int ld = lora_split_stride(R);
-  uint8_t* own = sm + 3 * kAddRows * ld + wave * (kCols * kAddBRow);
+  uint8_t* own = sm + 3 * kRows * ld + wave * (kCols * kAddBRow);
   // FULL: all of the workgroup's rows and columns are there, and vectors are aligned
   const auto run = [&](auto full) {
     constexpr bool FULL = decltype(full)::value;
@@ -387,17 +389,19 @@ k_lora_add(const void* base, int64_t ldb, int T, int N, const uint16_t* __restri
       for (int i = 0; i < kChunks; ++i)
         if (FULL || t0 + row + kRpc * i < T)
           q[g][i].template load<FULL>(from, (uint32_t)(row + kRpc * i) * (uint32_t)ldb + n1 + kCols * g, n1 + kCols * g, N);
-    lora_split_rows<kAddRows, kAddThreads>(h, slices, T, R, 0, R, adapter, L, t0, sm, ld, tid);
+    lora_split_rows<kRows, kAddThreads>(h, slices, T, R, 0, R, adapter, L, t0, sm, ld, tid);
     __syncthreads();
 #pragma unroll
     for (int g = 0; g < kPasses; ++g) {
       const int ng = n0 + kCols * g, n = n1 + kCols * g;
-      f32x4 sum[2][2 * kNT];
+      f32x4 sum[MT][2 * kNT];
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int j = 0; j < 2 * kNT; ++j) sum[m][j] = {0.f, 0.f, 0.f, 0.f};
-      uint32_t left[2] = {rows[0], rows[1]};
+      uint32_t left[MT];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) left[m] = rows[m];
       // 32 of R of the pass's rows of B, a step ahead of their use: an adapter's first while the one before multiplies
       u32x4 w[2 * kNT];
       const auto fetch = [&](int l, int r0) {
@@ -410,21 +414,24 @@ k_lora_add(const void* base, int64_t ldb, int T, int N, const uint16_t* __restri
         }
       };
       const auto first = [&]() {
-        return left[0] != 0 ? __builtin_amdgcn_readlane(ad[0], __ffs(left[0]) - 1)
-                            : __builtin_amdgcn_readlane(ad[1], __ffs(left[1]) - 1);
+        int l = -1;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+          if (l < 0 && left[m] != 0) l = __builtin_amdgcn_readlane(ad[m], __ffs(left[m]) - 1);
+        return l;
       };
-      int ahead = -1;
-      if ((left[0] | left[1]) != 0) fetch(ahead = first(), 0);
+      int ahead = first();
+      if (ahead >= 0) fetch(ahead, 0);
       while (ahead >= 0) {
         const int l = ahead;
-        left[0] &= ~lora_rows(ad[0] == l);
-        left[1] &= ~lora_rows(ad[1] == l);
-        f32x4 d[2][2 * kNT];
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+        for (int m = 0; m < MT; ++m) left[m] &= ~lora_rows(ad[m] == l);
+        f32x4 d[MT][2 * kNT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
           for (int j = 0; j < 2 * kNT; ++j) d[m][j] = {0.f, 0.f, 0.f, 0.f};
-        ahead = (left[0] | left[1]) != 0 ? first() : -1;
+        ahead = first();
         for (int r0 = 0; r0 < R; r0 += 32) {
           lora_wave_order();
 #pragma unroll
@@ -437,11 +444,11 @@ k_lora_add(const void* base, int64_t ldb, int T, int N, const uint16_t* __restri
             bv[j] = *reinterpret_cast<const bf16x8*>(own + (16 * j + c) * kAddBRow + 16 * kq);
           if (r0 + 32 < R) fetch(l, r0 + 32);
           else if (ahead >= 0) fetch(ahead, 0);
-          lora_multiply<2, kNT>(bv, R, r0, sm, ld, lane, d);
+          lora_multiply<MT, kNT>(bv, R, r0, sm, ld, lane, d);
         }
         // the rows of other adapters keep what they have, whatever this one holds
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
           for (int j = 0; j < 2 * kNT; ++j)
 #pragma unroll
@@ -451,7 +458,7 @@ k_lora_add(const void* base, int64_t ldb, int T, int N, const uint16_t* __restri
       constexpr int kTurn = kCols + 4;         // floats from row to row
       float* turn = reinterpret_cast<float*>(own);
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
+      for (int m = 0; m < MT; ++m) {
         if (rows[m] != 0) {
           lora_wave_order();
 #pragma unroll
@@ -459,7 +466,7 @@ k_lora_add(const void* base, int64_t ldb, int T, int N, const uint16_t* __restri
           lora_wave_order();
         }
 #pragma unroll
-        for (int i = m * kChunks / 2; i < (m + 1) * kChunks / 2; ++i) {
+        for (int i = m * kChunks / MT; i < (m + 1) * kChunks / MT; ++i) {
           const int r = row + kRpc * i;
           if ((rows[m] >> (r % 16)) & 1) q[g][i].add(turn + kTurn * (r % 16) + P::kE * (lane % kLpr));
           if (FULL || t0 + r < T) q[g][i].template store<FULL>(to, (uint32_t)r * (uint32_t)ldo + n, n, N);
@@ -467,7 +474,7 @@ k_lora_add(const void* base, int64_t ldb, int T, int N, const uint16_t* __restri
       }
     }
   };
-  if (vec && t0 + kAddRows <= T && wg % colgroups * kAddCols + kAddCols <= N) run(std::true_type{});
+  if (vec && t0 + kRows <= T && wg % colgroups * kAddCols + kAddCols <= N) run(std::true_type{});
   else run(std::false_type{});
 }
 
@@ -497,10 +504,10 @@ hipError_t launch_lora_shrink(const uint16_t* x, int64_t ldx, int T, int K, cons
 // Few rows of low rank take one launch on the vector unit, which reads A and B once a row: what it costs grows with T R,
 // and it does not mind that every row has another adapter; the two kernels work once for each adapter of a tile. Measured
 // (2048 x 4096 bf16, 48 adapters), us here and there with as many requests as rows, then with 4 (128 rows: 8) requests:
-//    64 rows, rank 16    6.4  36.8     3.9   9.7      256 rows, rank 16   14.9  37.4     9.5   9.6
-//    64 rows, rank 64   23.9  54.4    20.5  13.2      512 rows, rank 8    22.4  39.1    22.8  10.8
-//   128 rows, rank 16    9.3  37.4     6.8  10.5      128 rows, rank 64   44.0  58.0    33.3  16.1
-// (the left column is taken, the right one is not)
+//    64 rows, rank 16    6.4  36.8     3.9   9.7      and past the border:
+//    64 rows, rank 64   23.9  54.4    20.5  13.2      128 rows, rank 64   44.0  58.0    33.3  16.1
+//   128 rows, rank 16    9.3  37.4     6.8  10.5      512 rows, rank 8    22.4  39.1    22.8  10.8
+//   256 rows, rank 16   14.9  37.4     9.5   9.6
 bool lora_few(int T, int R) { return T <= 256 && R <= 64 && T * R <= 4096; }
 
 hipError_t launch_lora_few(const void* base, bool bf16, int64_t ldb, const uint16_t* x, int64_t ldx, int T, int K,
@@ -528,14 +535,24 @@ hipError_t launch_lora_add(const void* base, bool bf16, int64_t ldb, int T, int 
   const int unit = bf16 ? 8 : 4;          // elements of 16 bytes
   const bool vec = reinterpret_cast<uintptr_t>(base) % 16 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0 &&
                    ldb % unit == 0 && ldo % unit == 0;
-  const int colgroups = cdiv(N, kAddCols), wgs = cdiv(T, kAddRows) * colgroups, grid = cdiv(wgs, kXcds) * kXcds;
-  const size_t lds = (size_t)3 * kAddRows * lora_split_stride(R) + kAddThreads / kWave * (bf16 ? 64 : 32) * kAddBRow;
-  if (bf16)
-    k_lora_add<true><<<grid, kAddThreads, lds, st>>>(base, ldb, T, N, b, L, R, adapter, h, slices, colgroups, wgs, out, ldo,
-                                                     vec);
-  else
-    k_lora_add<false><<<grid, kAddThreads, lds, st>>>(base, ldb, T, N, b, L, R, adapter, h, slices, colgroups, wgs, out, ldo,
-                                                      vec);
+  const int colgroups = cdiv(N, kAddCols);
+  const auto run = [&](auto type, auto mt) {
+    constexpr int kRows = 16 * decltype(mt)::value;
+    const int wgs = cdiv(T, kRows) * colgroups, grid = cdiv(wgs, kXcds) * kXcds;
+    const size_t lds = (size_t)3 * kRows * lora_split_stride(R) + kAddThreads / kWave * (bf16 ? 64 : 32) * kAddBRow;
+    k_lora_add<decltype(type)::value, decltype(mt)::value>
+        <<<grid, kAddThreads, lds, st>>>(base, ldb, T, N, b, L, R, adapter, h, slices, colgroups, wgs, out, ldo, vec);
+  };
+  const std::integral_constant<int, 1> one;
+  const std::integral_constant<int, 2> two;
+  // 16 rows a workgroup while that many make few workgroups: a tile then has half the adapters, one after the other. us
+  // with 16 and 32 rows (2048 x 4096 bf16, rank 16, and the shrink): 512 rows of 512 requests 29.3, 40.3, of 4 requests
+  // 9.8, 10.6; 2048 rows of 64 requests 22.5, 24.1, of 4 17.7, 18.6; 8191 rows of 64 requests 61.0, 58.5.
+  const bool few = (int64_t)cdiv(T, 32) * colgroups <= 1024;
+  if (bf16 && few) run(std::true_type{}, one);
+  else if (bf16) run(std::true_type{}, two);
+  else if (few) run(std::false_type{}, one);
+  else run(std::false_type{}, two);
   return hipGetLastError();
 }
 
