@@ -349,7 +349,7 @@ struct Piece {
 // with 128 bytes of a row on neighbouring lanes, B 64 bytes of a row on four,
 // and a wave's own LDS turns B's rows and the products into the other order
 // (64 us without, 55 with, of 8191 x 4096 float32 rows: 268 MB at 4.8 TB/s, a
-// copy takes 45 here; 2048 x 2048 bf16 rows of rank 64 10.2 us, 1.6 TB/s, bound
+// copy takes 45 here; 2048 x 2048 bf16 rows of rank 64 9.2 us, 1.8 TB/s, bound
 // by the chain of h, B and the products in each workgroup).
 template <bool BF16, int MT>
 __global__ void __launch_bounds__(kAddThreads, BF16 ? 3 : 4)
