@@ -30,7 +30,7 @@ constexpr int kShWaves = 4;                    // the shrink kernel: rows and K 
 constexpr int kShThreads = kWave * kShWaves;
 constexpr int kShRows = 64;
 constexpr int kShK = 128;
-constexpr int kFewWaves = 8;
+constexpr int kFewWaves = 16;
 constexpr int kFewThreads = kWave * kFewWaves;
 constexpr int kAddThreads = 256;               // the add kernel: rows and columns of a step
 constexpr int kAddCols = 256;
@@ -219,23 +219,31 @@ __device__ __forceinline__ void fma8(float& s, const u32x4& p, const u32x4& q) {
   }
 }
 
-// Few rows, one launch: a workgroup owns a row and 512 columns. Its waves
-// compute the row's R inner sums, a wave per sum (whole lines of A, 8 values a
-// lane and load; each workgroup of a row does it again, from L2), then a
-// thread per column multiplies them with its row of B, which is on its way
-// from the start. 3.3 us for one row of 2048 x 2048 and rank 16: a launch and two
-// loads that depend on each other; 6.7 us for 64 rows of 48 adapters, which read
-// each adapter's A once per row and 512 columns (L2). PIECES: 16-byte pieces of B a thread keeps (R <= 8 PIECES).
-template <bool BF16, int PIECES>
+// Few rows, one launch: a workgroup owns a row and 1024 columns. Its waves
+// compute the row's R inner sums, SUMS of them at a time each (whole lines of A,
+// 8 values a lane and load; each workgroup of a row does it again, from L2). A
+// wave's 64 columns of B lie one behind the other in memory and are on their way
+// from the start, 64 pieces of 16 bytes a load; a piece's part of the product goes
+// to its column by way of LDS. (A column a lane takes the load path 64 accesses an
+// instruction: 64 rows of 64 requests, 2048 x 4096 bf16, rank 64 18.4 against 15.7
+// us, 16 rows 15.7 against 12.6. Up to rank 16 that is little, and LDS a detour:
+// one row 3.3 against 3.7 us.) 16 waves: with 8 of twice the sums one row of rank
+// 16 takes 3.1 us, 64 rows 6.4 in place of 5.5, of rank 64 25 in place of 18. One
+// row is a launch and two loads that depend on each other; more read A once a row
+// and 1024 columns from L2. PIECES: 16-byte pieces of B a lane keeps (R <= 8 PIECES).
+template <bool BF16, int PIECES, int SUMS>
 __global__ void __launch_bounds__(kFewThreads)
 k_lora_few(const void* base, int64_t ldb, const uint16_t* __restrict__ x, int64_t ldx, int K, int N,
            const uint16_t* __restrict__ a, const uint16_t* __restrict__ b, int L, int R,
            const int32_t* __restrict__ adapter, const float* __restrict__ scale, void* out, int64_t ldo) {
-  __shared__ float hs[8 * PIECES];
+  constexpr bool kTurn = PIECES > 2;
+  constexpr int kParts = kTurn ? kWave * PIECES * 9 / 8 : 1;       // a float of padding after each eight
+  __shared__ __align__(16) float hs[8 * PIECES];
+  __shared__ float parts[kFewWaves][kParts];
   const int lane = threadIdx.x % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int64_t t = blockIdx.y;
-  const int n = blockIdx.x * kFewThreads + threadIdx.x;
+  const int n0 = blockIdx.x * kFewThreads + kWave * wave, n = n0 + lane;
   const int l = adapter[t];
   const bool has = (uint32_t)l < (uint32_t)L;
   uint32_t bits = 0;                           // base's element
@@ -244,43 +252,75 @@ k_lora_few(const void* base, int64_t ldb, const uint16_t* __restrict__ x, int64_
     else bits = static_cast<const uint32_t*>(base)[t * ldb + n];
   }
   if (has) {
+    const int per = R / 8;                     // pieces a column
+    const int pieces = max(0, min(kWave, N - n0)) * per;
+    const u32x4* bl = reinterpret_cast<const u32x4*>(b + ((size_t)l * N + min(n0, N)) * R);
     u32x4 bv[PIECES];
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
+      const int at = kTurn ? kWave * i + lane : per * lane + i;
       bv[i] = {0u, 0u, 0u, 0u};
-      if (n < N && 8 * i < R) bv[i] = *reinterpret_cast<const u32x4*>(b + ((size_t)l * N + n) * R + 8 * i);
+      if (at < pieces && (kTurn || i < per)) bv[i] = bl[at];
     }
     const uint16_t* xr = x + t * ldx;
-    for (int r = wave; r < R; r += 2 * kFewWaves) {
-      // two sums at a time: r and r + kFewWaves
-      const bool two = r + kFewWaves < R;
-      const uint16_t* a0 = a + ((size_t)l * R + r) * K;
-      const uint16_t* a1 = two ? a0 + (size_t)kFewWaves * K : a0;
-      float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll 4
+    for (int r = wave; r < R; r += SUMS * kFewWaves) {
+      // r, r + kFewWaves, .. (past R: the first again, dropped)
+      const uint16_t* ar[SUMS];
+      float sum[SUMS];
+#pragma unroll
+      for (int i = 0; i < SUMS; ++i) {
+        ar[i] = a + ((size_t)l * R + (r + i * kFewWaves < R ? r + i * kFewWaves : r)) * K;
+        sum[i] = 0.0f;
+      }
+#pragma unroll (SUMS == 1 ? 4 : 2)
       for (int64_t k = 8 * lane; k < K; k += 8 * kWave) {
         const u32x4 xv = *reinterpret_cast<const u32x4*>(xr + k);
-        fma8(s0, *reinterpret_cast<const u32x4*>(a0 + k), xv);
-        fma8(s1, *reinterpret_cast<const u32x4*>(a1 + k), xv);
+#pragma unroll
+        for (int i = 0; i < SUMS; ++i) fma8(sum[i], *reinterpret_cast<const u32x4*>(ar[i] + k), xv);
       }
-      s0 = wave_sum(s0);
-      s1 = wave_sum(s1);
-      if (lane == 0) {
-        hs[r] = scale[l] * s0;
-        if (two) hs[r + kFewWaves] = scale[l] * s1;
+#pragma unroll
+      for (int i = 0; i < SUMS; ++i) {
+        const float v = wave_sum(sum[i]);
+        if (lane == 0 && r + i * kFewWaves < R) hs[r + i * kFewWaves] = scale[l] * v;
       }
     }
     __syncthreads();
+    // the products of a piece of B with its part of h
+    const auto product = [&](int i, int piece) {
+      const f32x4 h0 = *reinterpret_cast<const f32x4*>(hs + 8 * piece);
+      const f32x4 h1 = *reinterpret_cast<const f32x4*>(hs + 8 * piece + 4);
+      float p = bf16_lo(bv[i][0]) * h0[0];
+      p = fmaf(bf16_hi(bv[i][0]), h0[1], p);
+      p = fmaf(bf16_lo(bv[i][1]), h0[2], p);
+      p = fmaf(bf16_hi(bv[i][1]), h0[3], p);
+      p = fmaf(bf16_lo(bv[i][2]), h1[0], p);
+      p = fmaf(bf16_hi(bv[i][2]), h1[1], p);
+      p = fmaf(bf16_lo(bv[i][3]), h1[2], p);
+      return fmaf(bf16_hi(bv[i][3]), h1[3], p);
+    };
     float d = 0.0f;
+    if constexpr (kTurn) {
+      float* mine = parts[wave];
+      int piece = lane % per;
+      const int step = kWave % per;
 #pragma unroll
-    for (int i = 0; i < PIECES; ++i) {
-      if (8 * i < R) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          d = fmaf(bf16_lo(bv[i][q]), hs[8 * i + 2 * q], d);
-          d = fmaf(bf16_hi(bv[i][q]), hs[8 * i + 2 * q + 1], d);
+      for (int i = 0; i < PIECES; ++i) {
+        if (i < per) {
+          const int at = kWave * i + lane;
+          mine[at + at / 8] = product(i, piece);
+          piece = piece + step < per ? piece + step : piece + step - per;
         }
       }
+      lora_wave_order();
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) {
+        const int at = lane * per + i;
+        if (i < per) d += mine[at + at / 8];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i)
+        if (i < per) d += product(i, i);
     }
     if constexpr (BF16) bits = __builtin_bit_cast(uint16_t, (__bf16)(bf16_to_f32((uint16_t)bits) + d));
     else bits = __float_as_uint(__uint_as_float(bits) + d);
@@ -513,17 +553,17 @@ bool lora_few(int T, int R) { return T <= 256 && R <= 64 && T * R <= 4096; }
 hipError_t launch_lora_few(const void* base, bool bf16, int64_t ldb, const uint16_t* x, int64_t ldx, int T, int K,
                            int N, const uint16_t* a, const uint16_t* b, int L, int R, const int32_t* adapter,
                            const float* scale, void* out, int64_t ldo, hipStream_t st) {
-  const dim3 grid(cdiv(N, kFewThreads), T);
-#define I8H_FEW(TYPE, PIECES)                                                                                 \
-  k_lora_few<TYPE, PIECES><<<grid, kFewThreads, 0, st>>>(base, ldb, x, ldx, K, N, a, b, L, R, adapter, scale, out, ldo)
+#define I8H_FEW(TYPE, PIECES, SUMS)                                                                                     \
+  k_lora_few<TYPE, PIECES, SUMS><<<dim3(cdiv(N, kFewThreads), T), kFewThreads, 0, st>>>(base, ldb, x, ldx, K, N, a, b, L, \
+                                                                                        R, adapter, scale, out, ldo)
   if (bf16) {
-    if (R <= 16) I8H_FEW(true, 2);
-    else if (R <= 32) I8H_FEW(true, 4);
-    else I8H_FEW(true, 8);
+    if (R <= 16) I8H_FEW(true, 2, 1);
+    else if (R <= 32) I8H_FEW(true, 4, 2);
+    else I8H_FEW(true, 8, 4);
   } else {
-    if (R <= 16) I8H_FEW(false, 2);
-    else if (R <= 32) I8H_FEW(false, 4);
-    else I8H_FEW(false, 8);
+    if (R <= 16) I8H_FEW(false, 2, 1);
+    else if (R <= 32) I8H_FEW(false, 4, 2);
+    else I8H_FEW(false, 8, 4);
   }
 #undef I8H_FEW
   return hipGetLastError();
