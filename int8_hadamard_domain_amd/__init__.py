@@ -795,9 +795,10 @@ def linear_i8f16_lora(x, codes, scales, lora_a, lora_b, adapter, lora_scale, out
     T, K = x.shape
     dev = x.device
     _dev(codes, "codes", torch.int8, 2, device=dev)
-    N = codes.shape[0]
+    N, k = codes.shape
     L, R = _lora(lora_a, lora_b, adapter, lora_scale, T, K, N, dev)
-    _dev(codes, "codes", torch.int8, shape=(N, K))
+    if k != K:
+        _dev(codes, "codes", torch.int8, shape=(N, K))
     _dev(scales, "scales", torch.float16, shape=(N, K // 128), device=dev)
     if out is None:
         out = torch.empty((T, N), dtype=torch.float32, device=dev)

@@ -544,10 +544,10 @@ hipError_t launch_lora_shrink(const uint16_t* x, int64_t ldx, int T, int K, cons
 // Few rows of low rank take one launch on the vector unit, which reads A and B once a row: what it costs grows with T R,
 // and it does not mind that every row has another adapter; the two kernels work once for each adapter of a tile. Measured
 // (2048 x 4096 bf16, 48 adapters), us here and there with as many requests as rows, then with 4 (128 rows: 8) requests:
-//    64 rows, rank 16    6.4  36.8     3.9   9.7      and past the border:
-//    64 rows, rank 64   23.9  54.4    20.5  13.2      128 rows, rank 64   44.0  58.0    33.3  16.1
-//   128 rows, rank 16    9.3  37.4     6.8  10.5      512 rows, rank 8    22.4  39.1    22.8  10.8
-//   256 rows, rank 16   14.9  37.4     9.5   9.6
+//    64 rows, rank 16    5.4  24.4     3.8   9.0      and past the border:
+//    64 rows, rank 64   15.6  35.0    12.3  11.8      128 rows, rank 64   28.4  36.7    22.3  13.3
+//   128 rows, rank 16    8.4  25.2     6.4   9.3      256 rows, rank 32   24.7  28.5    19.2   9.8
+//   256 rows, rank 16   13.8  25.7     8.7   8.8      512 rows, rank 8    18.3  29.7    18.5  10.4
 bool lora_few(int T, int R) { return T <= 256 && R <= 64 && T * R <= 4096; }
 
 hipError_t launch_lora_few(const void* base, bool bf16, int64_t ldb, const uint16_t* x, int64_t ldx, int T, int K,

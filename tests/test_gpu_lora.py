@@ -130,6 +130,20 @@ def test_broken_adapters_stay_in_their_rows(gpu_available, value):
             assert not bool(torch.isfinite(got[mine].float()).any())
 
 
+@pytest.mark.parametrize("T", [5, 300, 1500])
+def test_rows_without_an_adapter_keep_their_bits(gpu_available, T):
+    """NaN payloads, signed zeros and subnormals of base pass through, beside rows that have an adapter."""
+    K, N, R = 64, 300, 16
+    for dtype, bits in ((F32, torch.int32), (BF16, torch.int16)):
+        base, x, a, b, s, ad = problem(T, K, N, R, 3, "mixed", dtype)
+        info = torch.iinfo(bits)
+        base = torch.randint(info.min, info.max, (T, N), dtype=bits, device="cuda").view(dtype)
+        base[:, 0] = -0.0
+        out = i8h.lora_add(base, x, a, b, ad, s)
+        none = ad < 0
+        assert bool(none.any()) and torch.equal(out.view(bits)[none], base.view(bits)[none])
+
+
 def test_inner_sums_are_not_rounded(gpu_available):
     """h = 1 + 2^-20 with B = 2^10 and a base of -2^10: what a product of bf16 inner sums would lose comes out whole."""
     T, K, N, R = 5, 8, 16, 8
@@ -209,3 +223,24 @@ def test_refusals(gpu_available):
     wide = torch.zeros((6, 40), device="cuda")
     with pytest.raises(i8h.I8HError):                                   # out meets base in part
         i8h.lora_add(wide[:, :16], x, a, b, ad, s, out=wide[:, 8:24])
+
+
+def test_linear_refusals(gpu_available):
+    T, K, N = 6, 128, 32
+    _, x, a, b, s, ad = problem(T, K, N, 8, 2, "one", F32)
+    codes = torch.zeros((N, K), dtype=torch.int8, device="cuda")
+    scales = torch.zeros((N, 1), dtype=torch.float16, device="cuda")
+    for bad in ((x[:, :64], codes, scales, a, b, ad, s), (x, codes[:, :64], scales, a, b, ad, s), (x, codes, scales[:16], a, b, ad, s),
+                (x, codes.t(), scales, a, b, ad, s), (x, codes, scales, a[:, :, :64], b, ad, s), (x, codes, scales, a, b[:, :16], ad, s),
+                (x, codes, scales, a, b, ad[:5], s), (x, codes, scales, a, b, ad, s[:1]), (x[0], codes, scales, a, b, ad, s)):
+        with pytest.raises(ValueError):
+            i8h.linear_i8f16_lora(*bad)
+    for bad in ((x.float(), codes, scales, a, b, ad, s), (x, codes.int(), scales, a, b, ad, s),
+                (x, codes, scales.bfloat16(), a, b, ad, s), (x, codes, scales, a, b, ad.long(), s)):
+        with pytest.raises(TypeError):
+            i8h.linear_i8f16_lora(*bad)
+    with pytest.raises(ValueError):
+        i8h.linear_i8f16_lora(x, codes, scales, a, b, ad, s, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(i8h.I8HError):                                   # columns are multiples of 16
+        i8h.linear_i8f16_lora(x, codes[:24], scales[:24], a, b[:, :24].contiguous(), ad, s)
+    assert i8h.linear_i8f16_lora(x[:0], codes, scales, a, b, ad[:0], s).shape == (0, N)
