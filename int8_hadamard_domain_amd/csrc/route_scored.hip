@@ -680,7 +680,8 @@ __device__ __forceinline__ void exclusive_scan(const int* tot, int* off, int E, 
   if (lane == kWave - 1) wave_tot[wave] = inc;
   __syncthreads();
   int at = inc - s;
-  for (int i = 0; i < wave; ++i) at += wave_tot[i];
+#pragma unroll
+  for (int i = 0; i < WAVES - 1; ++i) at += i < wave ? wave_tot[i] : 0;      // (all read at once)
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     if (e0 + i < E) off[e0 + i] = at;
@@ -690,6 +691,7 @@ __device__ __forceinline__ void exclusive_scan(const int* tot, int* off, int E, 
 
 // Rank of the thread's pair among the workgroup's pairs of the same expert
 // with a lower thread index. count [waves][ld] in LDS, zero on entry.
+template <int WAVES>
 __device__ __forceinline__ int stable_rank(bool valid, int e, int E, int ld, int* count) {
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   uint64_t same = __ballot(valid);
@@ -701,17 +703,44 @@ __device__ __forceinline__ int stable_rank(bool valid, int e, int E, int ld, int
   int rank = __popcll(same & lanes_below(lane));
   if (valid && rank == 0) count[wave * ld + e] = __popcll(same);
   __syncthreads();
-  if (valid)
-    for (int i = 0; i < wave; ++i) rank += count[i * ld + e];
+#pragma unroll
+  for (int i = 0; i < WAVES - 1; ++i) {
+    const int c = count[i * ld + e];           // (all read at once)
+    rank += i < wave ? c : 0;
+  }
   return rank;
 }
 
-// Adds the counts of two packed pairs of experts over the lanes `cols` apart and further.
-__device__ __forceinline__ uint32_t add_lanes(uint32_t v, int cols) {
-#define I8H_STEP(M) if (cols <= M) v += (uint32_t)xor_lane_i<M>((int)v);
-  I8H_STEP(1) I8H_STEP(2) I8H_STEP(4) I8H_STEP(8) I8H_STEP(16) I8H_STEP(32)
+// Adds the packed counts of a wave, `cols` (a power of two) lanes a chunk, and puts lane c's sums at part[16 c ..]. A step
+// at a time for all of them: a branch a count and step took 2,000 cycles. Over lanes 16 and 32 apart two counts share
+// an exchange, each half of the lanes keeping one of them.
+__device__ __forceinline__ void put_sums(uint32_t (&v)[16], int cols, int epad, int lane, uint32_t* part) {
+#define I8H_STEP(M)                                                                               \
+  if (cols <= M) {                                                                                \
+    _Pragma("unroll") for (int i = 0; i < 16; ++i) v[i] += (uint32_t)xor_lane_i<M>((int)v[i]);    \
+  }
+  I8H_STEP(1) I8H_STEP(2) I8H_STEP(4) I8H_STEP(8)
+  if (cols <= 16) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const auto s = __builtin_amdgcn_permlane16_swap(v[i], v[i + 8], false, false);
+      v[i] = s[0] + s[1];                      // odd rows of 16 lanes: i + 8
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const auto s = __builtin_amdgcn_permlane32_swap(v[i], v[i + 4], false, false);
+      v[i] = s[0] + s[1];                      // the upper half: i + 4
+    }
+    uint32_t* to = part + 16 * (lane % 16) + 4 * (lane / 32) + 8 * (lane / 16 % 2);
+    if (lane % 16 < cols && 16 * (lane % 16) < epad) *reinterpret_cast<u32x4*>(to) = u32x4{v[0], v[1], v[2], v[3]};
+  } else {
+    I8H_STEP(32)
+    if (lane < cols && 16 * lane < epad) {
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) *reinterpret_cast<u32x4*>(part + 16 * lane + i) = u32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
+    }
+  }
 #undef I8H_STEP
-  return v;
 }
 
 // The permutation of `mult` chunks' pairs, a thread each: 8.0 us for 131072 pairs
@@ -727,7 +756,7 @@ k_scored_scatter(const int32_t* __restrict__ ids, int P, int E, int epad, int co
                  const int32_t* __restrict__ total, int32_t* __restrict__ expert_off,
                  int32_t* __restrict__ sorted_pairs, int32_t* __restrict__ pair_pos) {
   constexpr int kWaves = kScScatterThreads / kWave;
-  extern __shared__ int sm[];                  // tot, base, pre [epad] each, count [waves][epad]
+  extern __shared__ __align__(16) int sm[];    // tot, base, pre [epad] each, count [waves][epad]
   int *tot = sm, *base = tot + epad, *pre = base + epad, *count = pre + epad;
   __shared__ int wave_tot[kWaves];
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave, wg = blockIdx.x;
@@ -744,7 +773,7 @@ k_scored_scatter(const int32_t* __restrict__ ids, int P, int E, int epad, int co
     uint32_t* part = reinterpret_cast<uint32_t*>(count);
     const int col = tid % cols, rows = kScScatterThreads / cols;
     const bool live = 16 * col < epad;
-    uint32_t all[8] = {}, ahead[8] = {};       // [2 i + h]: bytes 4 i + h and 4 i + h + 2 of the 16
+    uint32_t sums[16] = {};                    // [2 i + h]: bytes 4 i + h and 4 i + h + 2 of the 16; 8 on: of chunks before
     for (int c0 = tid / cols; c0 < nchunks; c0 += 4 * rows) {
       u32x4 h[4];
 #pragma unroll
@@ -759,25 +788,14 @@ k_scored_scatter(const int32_t* __restrict__ ids, int P, int E, int epad, int co
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t even = h[u][i] & 0x00ff00ffu, odd = (h[u][i] >> 8) & 0x00ff00ffu;
-          all[2 * i] += even;
-          all[2 * i + 1] += odd;
-          ahead[2 * i] += even & mask;
-          ahead[2 * i + 1] += odd & mask;
+          sums[2 * i] += even;
+          sums[2 * i + 1] += odd;
+          sums[8 + 2 * i] += even & mask;
+          sums[9 + 2 * i] += odd & mask;
         }
       }
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      all[i] = add_lanes(all[i], cols);
-      ahead[i] = add_lanes(ahead[i], cols);
-    }
-    if (lane < cols && live) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        part[wave * epad + 16 * col + i] = all[i];
-        part[wave * epad + 16 * col + 8 + i] = ahead[i];
-      }
-    }
+    put_sums(sums, cols, epad, lane, part + wave * epad);
     __syncthreads();
     for (int e = tid; e < epad; e += kScScatterThreads) {
       const int b = e % 16, word = 2 * (b / 4) + b % 2, shift = b & 2 ? 16 : 0;
@@ -795,7 +813,7 @@ k_scored_scatter(const int32_t* __restrict__ ids, int P, int E, int epad, int co
   for (int i = tid; i < kWaves * epad; i += kScScatterThreads) count[i] = 0;
   __syncthreads();
   exclusive_scan<kWaves>(tot, base, E, wave_tot);
-  const int rank = stable_rank(valid, id, E, epad, count);   // (its barrier also orders base)
+  const int rank = stable_rank<kWaves>(valid, id, E, epad, count);   // (its barrier also orders base)
   if (wg == 0) {
     for (int e = tid; e < E; e += kScScatterThreads) expert_off[e] = base[e];
     if (tid == 0) expert_off[E] = P;
@@ -843,7 +861,7 @@ k_scored_small(const X* __restrict__ logits, int T, ScoredRule R, bool vec, int3
   const bool valid = p < P;
   const int id = valid ? chosen[p] : 0;
   exclusive_scan<kWaves>(tot, base, R.E, wave_tot);   // (its barrier also orders count)
-  const int rank = stable_rank(valid, id, R.E, R.E, count);
+  const int rank = stable_rank<kWaves>(valid, id, R.E, R.E, count);
   for (int e = threadIdx.x; e < R.E; e += kScSmallThreads) expert_off[e] = base[e];
   if (p == 0) expert_off[R.E] = P;
   if (valid) {
