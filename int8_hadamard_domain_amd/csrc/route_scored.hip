@@ -17,8 +17,8 @@
 //   k_scored_scatter  per chunk: first rows of the experts, stable ranks
 //
 // Measured (medians on MI355X): one token of 128 experts 5.2 us in one launch;
-// 128 tokens 4.5 (rows) + 6.3 (scatter); 1999 tokens of 160 experts, 3 of 8
-// groups, 9.3 + 7.4; 16384 tokens of 256 experts, 4 of 8 groups, 23.7 + 8.0
+// 128 tokens 4.5 (rows) + 4.4 (scatter); 1999 tokens of 160 experts, 3 of 8
+// groups, 9.3 + 5.6; 16384 tokens of 256 experts, 4 of 8 groups, 23.8 + 5.9
 // (the bytes alone 3.7). Few tokens: the chain of dependent steps of one token,
 // 2.3 us, and of the permutation. Many: the vector unit's issue, 380
 // instructions a token by a whole wave.
@@ -743,9 +743,9 @@ __device__ __forceinline__ void put_sums(uint32_t (&v)[16], int cols, int epad, 
 #undef I8H_STEP
 }
 
-// The permutation of `mult` chunks' pairs, a thread each: 8.0 us for 131072 pairs
-// of 256 experts, of which most is the chain counts, sums, scan, ranks, store; the
-// bytes would take 0.6. SCANNED: pre and
+// The permutation of `mult` chunks' pairs, a thread each: 5.9 us for 131072 pairs
+// of 256 experts, of which most is the chain counts, sums, scan, ranks, store (the
+// bytes would take 0.6). SCANNED: pre and
 // total hold the chunks' running sums and the totals, else the workgroup adds
 // up the counts of all chunks itself: 16 experts a load, `cols` (a power of
 // two) lanes a chunk, sums in pairs of 16 bits (at most 256 chunks of 64).
@@ -825,10 +825,10 @@ k_scored_scatter(const int32_t* __restrict__ ids, int P, int E, int epad, int co
   }
 }
 
-// Few tokens in one workgroup. It wins up to 32 tokens, where a wave has two; us
-// here and in two launches, 128 experts, top 8: 16 tokens 7.5 and 9.8, 32 tokens
-// 9.7 and 9.8, 64 tokens 14.1 and 10.5, 128 tokens 22.8 and 10.7 (64 experts: 32
-// tokens 8.1 and 9.3, 48 tokens 9.9 and 9.5; 256 experts: 32 tokens 10.1 and 10.5).
+// Few tokens in one workgroup, up to 32 of them, where a wave has two; us here and
+// in two launches, 128 experts, top 8: 16 tokens 7.1 and 7.8, 32 tokens 9.2 and 8.0,
+// 64 tokens 14.1 and 8.6, 128 tokens 22.8 and 8.7. A call of 32 tokens takes the
+// host 14.8 us with one launch and no workspace, 19.6 with two.
 template <int VPL, typename X>
 __global__ void __launch_bounds__(kScSmallThreads)
 k_scored_small(const X* __restrict__ logits, int T, ScoredRule R, bool vec, int32_t* __restrict__ ids,
