@@ -737,7 +737,8 @@ __device__ __forceinline__ void put_sums(uint32_t (&v)[16], int cols, int epad, 
     I8H_STEP(32)
     if (lane < cols && 16 * lane < epad) {
 #pragma unroll
-      for (int i = 0; i < 16; i += 4) *reinterpret_cast<u32x4*>(part + 16 * lane + i) = u32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
+      for (int i = 0; i < 16; i += 4)
+        *reinterpret_cast<u32x4*>(part + 16 * lane + i) = u32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
     }
   }
 #undef I8H_STEP
