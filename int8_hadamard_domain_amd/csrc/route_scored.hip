@@ -522,17 +522,24 @@ __device__ __forceinline__ bool choose(const float (&v)[VPL], const float (&b)[V
     }
     ch.w = (float)(w * (double)R.scale);
   } else {
-    float w = R.sigmoid ? __builtin_amdgcn_rcpf(1.0f + exp_carried(-l)) : exp_carried(l - mx);
-    w = chosen && l != -INFINITY ? w : 0.0f;
-    if (R.renorm) {
-      const float total = reduce_add(w);
-      // scores that float32 cannot hold in full (a sigmoid far below 0); masked whole, they are 0 indeed
-      if (total < 0x1p-100f && __ballot(chosen && l != -INFINITY) != 0) return false;
-      w = total == 0.0f ? 0.0f : w * __builtin_amdgcn_rcpf(total);
-    } else if (!R.sigmoid) {
-      w *= __builtin_amdgcn_rcpf(S);
+    // The score before the softmax's sum, its exponential's argument x. Below e^-746 it is 0 in float64 too.
+    const float x = R.sigmoid ? l : l - mx;
+    const bool some = chosen && x > -746.0f;
+    float w = R.sigmoid ? __builtin_amdgcn_rcpf(1.0f + exp_carried(-l)) : exp_carried(x);
+    w = some ? w : 0.0f;
+    const float total = R.renorm ? reduce_add(w) : R.sigmoid ? 1.0f : S;
+    const float by = R.scale * (total == 0.0f ? 1.0f : __builtin_amdgcn_rcpf(total));
+    if (!(fabsf(by) < INFINITY)) return false;
+    // A score near float32's smallest normal value, or below, may be short of bits or 0. It is about e^x at most, so its
+    // weight is below 2^-127, and 0 here, unless x lies above the border; one that counts is left to float64, and so is a
+    // total that such scores may have a part in.
+    const bool small = some && w < 0x1p-125f;
+    if (__ballot(small) != 0) {
+      const float border = -88.1f - 0.6931472f * __builtin_amdgcn_logf(fabsf(by));
+      if (total < 0x1p-90f || __ballot(small && x > border) != 0) return false;
+      w = small ? 0.0f : w;
     }
-    ch.w = w * R.scale;
+    ch.w = w * by;                                     // (the scale first: w / total may have too few bits)
   }
   ch.rank = chosen ? rank : kMaxTopk;
   return true;

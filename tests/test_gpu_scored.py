@@ -189,3 +189,49 @@ def test_long_batch(gpu_available):
     ref = scored.route(l[rows].cpu().numpy(), k, "sigmoid", r["bias"], 8, 4, 2, True, 2.5)
     assert np.array_equal(got["topk_ids"][rows].cpu().numpy(), ref["topk_ids"])
     assert np.abs(got["topk_w"][rows].cpu().numpy() / ref["topk_w"] - 1).max() <= 40 * 2.0 ** -24
+
+
+SMALL = {"sigmoid": [[-60, -95], [-65, -90, -100], [-69, -120], [-86, -87, -88, -89], [-60, -100, -150, -700, -800, -3.4e38],
+                     [-104, -105, -110, -300], [0, -95, -200], [-745, -746, -747], [-750, -1e30], [-60, -math.inf]],
+         "softmax": [[0, -95], [-60, -95], [-60, -61, -95, -150], [-75, -80], [-300, -301, -700], [-800, -3.4e38],
+                     [-60, -math.inf], [-86, -87, -88, -89]]}
+
+
+@pytest.mark.parametrize("T", [20, 90])
+@pytest.mark.parametrize("renorm,scale", [(True, 2.5), (True, 2.0 ** 90), (True, -2.0 ** 127), (False, 2.5),
+                                          (False, 2.0 ** 120), (False, 2.0 ** -120)])
+@pytest.mark.parametrize("by", ["bias", "groups", "logit"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_weights_of_small_scores(gpu_available, score, by, renorm, scale, T):
+    """Chosen scores far below one, and below float32's smallest normal value, keep the bound: each weight by itself, not
+    as a part of the largest. Under softmax a bias (or, by two values, a group) keeps the largest logit, 0, out."""
+    E, size = 24, 12
+    rows = np.full((T, E), -math.inf, dtype=np.float32)
+    bias = None
+    for t in range(T):
+        small = SMALL[score][t % len(SMALL[score])]
+        rows[t, [(5 + t + 7 * j) % size for j in range(len(small))]] = small      # (7 and 12 share no factor)
+        rows[t, size + t % size] = 0.0 if score == "softmax" else -math.inf
+    if by == "bias":
+        bias = np.where(np.arange(E) < size, 0.5, -0.5).astype(np.float32)
+        bias[:size] += np.arange(size, dtype=np.float32) * np.float32(2.0 ** -6)
+        r = rule(score, bias, 1, 1, 1, renorm, scale)
+    elif by == "groups":
+        bias = np.where(np.arange(E) < size, 1.0, -1.0).astype(np.float32)
+        r = rule(score, bias, 2, 1, 2, renorm, scale)
+    else:
+        r = rule(score, None, 1, 1, 1, renorm, scale)
+    l = torch.from_numpy(rows).cuda()
+    got = call(l, 12, r)
+    check(l, 12, r, got)
+    w = got["topk_w"].cpu().numpy()
+    assert np.all(w[np.take_along_axis(rows, got["topk_ids"].cpu().numpy().astype(np.int64), 1) == -math.inf] == 0)
+
+
+def test_weights_of_spread_logits(gpu_available):
+    """Sigmoid logits over -60 .. -130, where the scores leave float32's range one after the other."""
+    g = torch.Generator().manual_seed(4)
+    l = (-60 - 70 * torch.rand((700, 8), generator=g)).cuda()
+    for renorm, scale in ((True, 1.0), (True, 2.0 ** 100), (False, 2.0 ** 100)):
+        check(l, 8, rule("sigmoid", None, 1, 1, 1, renorm, scale))
+        check(l, 4, rule("sigmoid", None, 4, 2, 2, renorm, scale))
