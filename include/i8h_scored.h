@@ -38,8 +38,13 @@ enum { I8H_SCORE_SOFTMAX = 0, I8H_SCORE_SIGMOID = 1 };
  * Ties go to the lower index, of groups as of experts. A NaN (a NaN logit, or
  * bias; +inf under softmax makes the whole token's scores NaN) ranks after
  * every number, so every id is an expert. The order is that of c and of the
- * worths in float64; weights are float32. A -inf logit masks an expert:
- * its score is 0, and only a bias, or a lack of others, has it chosen.
+ * worths in float64. A -inf logit masks an expert: its score is 0, and only a
+ * bias, or a lack of others, has it chosen.
+ *
+ * Weights are computed in float32 (in float64 where a score that counts leaves
+ * its range), each within 40 units of 2^-24 of its own value, for
+ * I8H_SCORE_SOFTMAX (40 + 2 d) units with d the distance of its logit from the
+ * token's largest; a weight below 2^-126 may be 0.
  *
  * logits [T, E] (logits_type: I8H_F32 or I8H_BF16, aligned to the element);
  * bias [E] float32 or NULL; topk_ids, topk_w, expert_off, sorted_pairs and
