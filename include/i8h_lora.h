@@ -12,7 +12,9 @@
  * them. Adapters of smaller rank are padded with zeros to R. Products are
  * exact, sums float32; the inner sums enter the second product as float32
  * values (as three bf16 parts), not rounded. Results are the same, bit for
- * bit, in every run. (An infinity in B may give NaN where a part is 0.)
+ * bit, in every run. An infinity in B gives one, or NaN where it meets an
+ * inner sum of 0 or an infinity of the other sign (a subnormal inner sum may
+ * count as 0 there).
  */
 #ifndef I8H_LORA_H
 #define I8H_LORA_H

@@ -335,20 +335,28 @@ k_linear_lora(const uint16_t* __restrict__ x, int T, int K, const int8_t* __rest
           const uint32_t mine = lora_rows(ad[o] == l);
           left &= ~mine;
           f32x4 d[NT];
+          const auto products = [&](auto finite) {
 #pragma unroll
-          for (int j = 0; j < NT; ++j) d[j] = {0.f, 0.f, 0.f, 0.f};
-          for (int r = 0; r < rc; r += 32) {
-            if (!ready) load_b(l, r0 + r, rc, bv[o]);
-            ready = false;
+            for (int j = 0; j < NT; ++j) d[j] = {0.f, 0.f, 0.f, 0.f};
+            for (int r = 0; r < rc; r += 32) {
+              if (!ready) load_b(l, r0 + r, rc, bv[o]);
+              ready = false;
 #pragma unroll
-            for (int p = 0; p < 3; ++p) {
-              bf16x8 hv = __builtin_bit_cast(bf16x8, u32x4{0u, 0u, 0u, 0u});
-              if (r + 8 * kq < rc)
-                hv = *reinterpret_cast<const bf16x8*>(sm + (p * S::kRows + row0 + c) * ld + 2 * (r + 8 * kq));
+              for (int p = 0; p < 3; ++p) {
+                bf16x8 hv = __builtin_bit_cast(bf16x8, u32x4{0u, 0u, 0u, 0u});
+                if (r + 8 * kq < rc)
+                  hv = *reinterpret_cast<const bf16x8*>(sm + (p * S::kRows + row0 + c) * ld + 2 * (r + 8 * kq));
 #pragma unroll
-              for (int j = 0; j < NT; ++j) d[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hv, bv[o][j], d[j], 0, 0, 0);
+                for (int j = 0; j < NT; ++j) {
+                  d[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hv, bv[o][j], d[j], 0, 0, 0);
+                  if constexpr (decltype(finite)::value) bv[o][j] = lora_finite(bv[o][j]);
+                }
+              }
             }
-          }
+          };
+          products(std::false_type{});
+          const float all = lora_total(d);
+          if (__builtin_expect(__ballot(all != all) != 0, 0)) products(std::true_type{});
           // the rows of other adapters keep what they have, whatever this one holds
 #pragma unroll
           for (int j = 0; j < NT; ++j)

@@ -393,7 +393,7 @@ struct Piece {
 // copy takes 45 here; 2048 x 2048 bf16 rows of rank 64 9.2 us, 1.8 TB/s, bound
 // by the chain of h, B and the products in each workgroup).
 template <bool BF16, int MT>
-__global__ void __launch_bounds__(kAddThreads, BF16 ? 3 : 4)
+__global__ void __launch_bounds__(kAddThreads, BF16 && MT == 2 ? 3 : 4)
 k_lora_add(const void* base, int64_t ldb, int T, int N, const uint16_t* __restrict__ b, int L, int R,
            const int32_t* __restrict__ adapter, const float* __restrict__ h, int slices, int colgroups, int wgs,
            void* out, int64_t ldo, bool vec) {
@@ -437,13 +437,7 @@ k_lora_add(const void* base, int64_t ldb, int T, int N, const uint16_t* __restri
     for (int g = 0; g < kPasses; ++g) {
       const int ng = n0 + kCols * g, n = n1 + kCols * g;
       f32x4 sum[MT][2 * kNT];
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int j = 0; j < 2 * kNT; ++j) sum[m][j] = {0.f, 0.f, 0.f, 0.f};
       uint32_t left[MT];
-#pragma unroll
-      for (int m = 0; m < MT; ++m) left[m] = rows[m];
       // 32 of R of the pass's rows of B, a step ahead of their use: an adapter's first while the one before multiplies
       u32x4 w[2 * kNT];
       const auto fetch = [&](int l, int r0) {
@@ -462,40 +456,53 @@ k_lora_add(const void* base, int64_t ldb, int T, int N, const uint16_t* __restri
           if (l < 0 && left[m] != 0) l = __builtin_amdgcn_readlane(ad[m], __ffs(left[m]) - 1);
         return l;
       };
-      int ahead = first();
-      if (ahead >= 0) fetch(ahead, 0);
-      while (ahead >= 0) {
-        const int l = ahead;
+      const auto products = [&](auto finite) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m) left[m] &= ~lora_rows(ad[m] == l);
-        f32x4 d[MT][2 * kNT];
+        for (int m = 0; m < MT; ++m) {
+          left[m] = rows[m];
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int j = 0; j < 2 * kNT; ++j) d[m][j] = {0.f, 0.f, 0.f, 0.f};
-        ahead = first();
-        for (int r0 = 0; r0 < R; r0 += 32) {
-          lora_wave_order();
-#pragma unroll
-          for (int i = 0; i < 2 * kNT; ++i)
-            *reinterpret_cast<u32x4*>(own + (16 * i + lane / 4) * kAddBRow + 16 * (lane % 4)) = w[i];
-          lora_wave_order();
-          bf16x8 bv[2 * kNT];
-#pragma unroll
-          for (int j = 0; j < 2 * kNT; ++j)
-            bv[j] = *reinterpret_cast<const bf16x8*>(own + (16 * j + c) * kAddBRow + 16 * kq);
-          if (r0 + 32 < R) fetch(l, r0 + 32);
-          else if (ahead >= 0) fetch(ahead, 0);
-          lora_multiply<MT, kNT>(bv, R, r0, sm, ld, lane, d);
+          for (int j = 0; j < 2 * kNT; ++j) sum[m][j] = {0.f, 0.f, 0.f, 0.f};
         }
-        // the rows of other adapters keep what they have, whatever this one holds
+        int ahead = first();
+        if (ahead >= 0) fetch(ahead, 0);
+        while (ahead >= 0) {
+          const int l = ahead;
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+          for (int m = 0; m < MT; ++m) left[m] &= ~lora_rows(ad[m] == l);
+          f32x4 d[MT][2 * kNT];
 #pragma unroll
-          for (int j = 0; j < 2 * kNT; ++j)
+          for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sum[m][j][i] = ad[m] == l ? d[m][j][i] : sum[m][j][i];
-      }
+            for (int j = 0; j < 2 * kNT; ++j) d[m][j] = {0.f, 0.f, 0.f, 0.f};
+          ahead = first();
+          for (int r0 = 0; r0 < R; r0 += 32) {
+            lora_wave_order();
+#pragma unroll
+            for (int i = 0; i < 2 * kNT; ++i)
+              *reinterpret_cast<u32x4*>(own + (16 * i + lane / 4) * kAddBRow + 16 * (lane % 4)) = w[i];
+            lora_wave_order();
+            bf16x8 bv[2 * kNT];
+#pragma unroll
+            for (int j = 0; j < 2 * kNT; ++j)
+              bv[j] = *reinterpret_cast<const bf16x8*>(own + (16 * j + c) * kAddBRow + 16 * kq);
+            if (r0 + 32 < R) fetch(l, r0 + 32);
+            else if (ahead >= 0) fetch(ahead, 0);
+            lora_multiply<MT, kNT, decltype(finite)::value>(bv, R, r0, sm, ld, lane, d);
+          }
+          // the rows of other adapters keep what they have, whatever this one holds
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int j = 0; j < 2 * kNT; ++j)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) sum[m][j][i] = ad[m] == l ? d[m][j][i] : sum[m][j][i];
+        }
+      };
+      products(std::false_type{});
+      float all = 0.0f;
+#pragma unroll
+      for (int m = 0; m < MT; ++m) all += lora_total(sum[m]);
+      if (__builtin_expect(__ballot(all != all) != 0, 0)) products(std::true_type{});
       // 16 rows at a time through the wave's LDS
       constexpr int kTurn = kCols + 4;         // floats from row to row
       float* turn = reinterpret_cast<float*>(own);

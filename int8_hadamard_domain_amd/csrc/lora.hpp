@@ -114,24 +114,63 @@ __device__ __forceinline__ void lora_wave_order() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// Infinities of B. Of an inner sum's parts the first has its sign, and is 0 only
+// where it is (a subnormal one aside), but the others are often 0, and 0 times an
+// infinity is NaN. So where the products hold a NaN they are done again without
+// B's infinities and NaN in the second and third part: what is finite comes out
+// with the same bits, and the first part decides about the rest. The check is a
+// few additions; no finite adapter gets further.
+
+// The sum of a lane's products: NaN if one is (or if there are infinities of both
+// signs: then they are done again for nothing).
+template <int N>
+__device__ __forceinline__ float lora_total(const f32x4 (&d)[N]) {
+  float t = 0.0f;
+#pragma unroll
+  for (int j = 0; j < N; ++j) t += (d[j][0] + d[j][1]) + (d[j][2] + d[j][3]);
+  return t;
+}
+
+// Eight bf16 values, 0 for infinities and NaN.
+__device__ __forceinline__ bf16x8 lora_finite(const bf16x8& v) {
+  u32x4 w = __builtin_bit_cast(u32x4, v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if ((w[i] & 0x7f80u) == 0x7f80u) w[i] &= 0xffff0000u;
+    if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] &= 0x0000ffffu;
+  }
+  return __builtin_bit_cast(bf16x8, w);
+}
+
 // The products of the adapters' second half, 32 of R from r0 on: d[m][j] += B h
 // for the 16 MT rows in LDS (lora_split_rows) and 32 NT columns, bv[j] holding
 // row 16 j + lane % 16 of B: the lane gets row 16 m + lane % 16, columns
-// 16 j + 4 (lane / 16) .. + 3.
-template <int MT, int NT>
-__device__ __forceinline__ void lora_multiply(const bf16x8 (&bv)[2 * NT], int R, int r0, const uint8_t* sm, int ld,
+// 16 j + 4 (lane / 16) .. + 3. FINITE: see above; bv is changed.
+template <int MT, int NT, bool FINITE>
+__device__ __forceinline__ void lora_multiply(bf16x8 (&bv)[2 * NT], int R, int r0, const uint8_t* sm, int ld,
                                               int lane, f32x4 (&d)[MT][2 * NT]) {
   const int c = lane % 16, r = r0 + 8 * (lane / 16);
+  const auto part = [&](int m, int p) {
+    bf16x8 hv = __builtin_bit_cast(bf16x8, u32x4{0u, 0u, 0u, 0u});
+    if (r < R) hv = *reinterpret_cast<const bf16x8*>(sm + (p * 16 * MT + 16 * m + c) * ld + 2 * r);
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
+    for (int j = 0; j < 2 * NT; ++j)
+      d[m][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bv[j], hv, d[m][j], 0, 0, 0);
+  };
+  if constexpr (FINITE) {
+#pragma unroll 1
     for (int p = 0; p < 3; ++p) {
-      bf16x8 hv = __builtin_bit_cast(bf16x8, u32x4{0u, 0u, 0u, 0u});
-      if (r < R) hv = *reinterpret_cast<const bf16x8*>(sm + (p * 16 * MT + 16 * m + c) * ld + 2 * r);
 #pragma unroll
-      for (int j = 0; j < 2 * NT; ++j)
-        d[m][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bv[j], hv, d[m][j], 0, 0, 0);
+      for (int m = 0; m < MT; ++m) part(m, p);
+#pragma unroll
+      for (int j = 0; j < 2 * NT; ++j) bv[j] = lora_finite(bv[j]);
     }
+  } else {
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int p = 0; p < 3; ++p) part(m, p);
+  }
 }
 
 }  // namespace i8h
