@@ -1,6 +1,7 @@
-"""GPU parity of the adapters' kernels in each of their forms: one launch, 16
-and 32 rows of lora_add, each tile of linear_i8f16_lora. Bounds as in
-test_gpu_lora.py."""
+"""GPU parity of the adapters' and the scored routing's kernels in the forms
+that only large batches take: 16 and 32 rows of lora_add, each tile of
+linear_i8f16_lora, the scan of the routing's counts. Bounds as in
+test_gpu_lora.py and test_gpu_scored.py; where sums are exact, equality."""
 
 import math
 
@@ -9,9 +10,10 @@ import pytest
 import torch
 
 import int8_hadamard_domain_amd as i8h
-from oracle import lora
+from oracle import lora, scored
 from tests.test_gpu_batch_sizes import _check_linear, _linear
-from tests.test_gpu_lora import BF16, F32, f64, problem
+from tests.test_gpu_lora import BF16, F32, check_add, f64, problem
+from tests.test_gpu_scored import bias_of, call, logits_of, rule
 
 pytestmark = pytest.mark.gpu
 
@@ -19,6 +21,38 @@ pytestmark = pytest.mark.gpu
 ADD = [(5, 300), (300, 304), (8191, 1104)]
 # linear_i8f16_lora's tiles: 16 x 16, 32 x 32, 64 x 128, 128 x 128
 TILES = [(40, 48), (520, 272), (1030, 528), (2100, 1040)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,K,N,R,L,kind", [(8191, 72, 1104, 40, 6, "mixed"), (8192, 136, 1280, 16, 3, "runs"),
+                                            (8225, 64, 1031, 72, 5, "runs"), (8191, 64, 1104, 256, 3, "mixed"),
+                                            (16400, 40, 516, 8, 9, "mixed"), (33000, 64, 64, 232, 2, "runs")])
+def test_add_by_32_rows(gpu_available, T, K, N, R, L, kind, dtype):
+    """More than 1024 workgroups of 32 rows: whole and ragged ones, one step of R to eight, adapters mixed and in runs."""
+    print(f"lora_add by 32 rows T={T} K={K} N={N} R={R} L={L} {kind} {dtype}", flush=True)
+    base, x, a, b, s, ad = problem(T, K, N, R, L, kind, dtype)
+    out = torch.full((T + 1, N), 3.0, dtype=dtype, device="cuda")
+    i8h.lora_add(base, x, a, b, ad, s, out=out[:T])
+    assert bool((out[T] == 3.0).all())
+    check_add(out[:T], base, x, a, b, s, ad)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shift", [1, 4, 8])
+def test_slices_by_32_rows(gpu_available, dtype, shift):
+    """Column slices, on and off the vectors' alignment; what lies beside them stays."""
+    T, K, N = 8200, 64, 1040
+    base, x, a, b, s, ad = problem(T, K, N, 24, 4, "mixed", dtype)
+    wide = torch.full((T, 2 * N + 24), 7.0, dtype=dtype, device="cuda")
+    vb, vo = wide[:, shift:N + shift], wide[:, N + 16:2 * N + 16]
+    vb.copy_(base)
+    print(f"slices by 32 rows shift={shift} {dtype}", flush=True)
+    i8h.lora_add(vb, x, a, b, ad, s, out=vo)
+    check_add(vo, base, x, a, b, s, ad)
+    assert torch.equal(vb, base) and bool((wide[:, N + shift:N + 16] == 7).all()) and bool((wide[:, 2 * N + 16:] == 7).all())
+    want = vo.clone()
+    i8h.lora_add(vb, x, a, b, ad, s, out=vb)
+    assert torch.equal(vb, want) and torch.equal(vo, want)
 
 
 # --------------------------------------------------------------------------------------------------- infinities in B
@@ -89,3 +123,28 @@ def test_infinities_in_b_of_the_linear(gpu_available, T, N, R):
     fine = torch.from_numpy(np.isfinite(ref)).cuda()
     assert torch.equal(got[fine], plain[fine])
     _check_linear(plain, x, codes, scales, a, b2, s, ad)
+
+
+# ----------------------------------------------------------------------------------------------- the scan of the counts
+
+@pytest.mark.parametrize("T,E,k,groups,keep,top", [(4200, 60, 32, 1, 1, 1), (17000, 16, 3, 4, 2, 2), (16500, 160, 6, 8, 3, 1),
+                                                   (16385, 384, 8, 6, 3, 2), (9000, 1000, 20, 4, 2, 2), (16400, 1024, 1, 1, 1, 1),
+                                                   (70001, 64, 4, 1, 1, 1)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_more_chunks_than_one_scatter_adds_up(gpu_available, T, E, k, groups, keep, top, score):
+    """More than 256 chunks: the permutation whole, against torch's stable sort; the choice against the oracle in a sample."""
+    print(f"scored scan T={T} E={E} k={k} {score}", flush=True)
+    l = logits_of(T, E, T, mask=0.05)
+    r = rule(score, bias_of(E, 2), groups, keep, top, True, 2.5)
+    got = call(l, k, r)
+    flat = got["topk_ids"].flatten().long()
+    order = torch.sort(flat, stable=True).indices
+    assert torch.equal(order.int(), got["sorted_pairs"])
+    assert torch.equal(got["pair_pos"][order], torch.arange(T * k, dtype=torch.int32, device="cuda"))
+    assert torch.equal(got["expert_off"], torch.searchsorted(flat[order].contiguous(), torch.arange(E + 1, device="cuda")).int())
+    rows = torch.cat([torch.arange(0, T, 211), torch.tensor([T - 1])]).cuda()
+    ref = scored.route(l[rows].cpu().numpy(), k, score, r["bias"], groups, keep, top, True, 2.5)
+    assert np.array_equal(got["topk_ids"][rows].cpu().numpy(), ref["topk_ids"])
+    # distances from the largest logit are below 40 here: (40 + 2 d) 2^-24
+    w = got["topk_w"][rows].cpu().numpy()
+    assert np.all(np.abs(w - ref["topk_w"]) <= 120 * 2.0 ** -24 * np.abs(ref["topk_w"]) + 2.0 ** -126)
