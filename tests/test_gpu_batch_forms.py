@@ -55,6 +55,53 @@ def test_slices_by_32_rows(gpu_available, dtype, shift):
     assert torch.equal(vb, want) and torch.equal(vo, want)
 
 
+# ------------------------------------------------------------------------------------- inner sums of 24 significant bits
+
+def _whole_sums(T, N, K):
+    """Inner sums 1 + 2^-12 + 2^-23, 1 and 1 + 2^-12, times a power of two a row, in columns 0, 33 and 130 of R. Even
+    columns of the output are the first less the second times 2^10, odd ones the first less the third: every sum on the
+    way is exact in float32, in any order."""
+    R = 136
+    g = torch.Generator().manual_seed(T)
+    up = torch.randint(-3, 4, (T,), generator=g).float()
+    x = torch.exp2(up)[:, None].expand(T, K).to(BF16).cuda()
+    a = torch.zeros((2, R, K), dtype=BF16, device="cuda")
+    a[1, [0, 33, 130], 3] = 1.0
+    a[1, [0, 130], K // 2] = 2.0 ** -12
+    a[1, 0, K - 1] = 2.0 ** -23
+    b = torch.zeros((2, N, R), dtype=BF16, device="cuda")
+    b[1, :, 0] = 1024.0
+    b[1, 0::2, 33] = -1024.0
+    b[1, 1::2, 130] = -1024.0
+    ad = torch.randint(-1, 2, (T,), generator=g).int().cuda()
+    want = torch.where(torch.arange(N) % 2 == 0, 0.25 + 2.0 ** -13, 2.0 ** -13)[None] * torch.exp2(up)[:, None]
+    return x, a, b, ad, torch.tensor([1.0, 1.0], device="cuda"), torch.where((ad == 1).cpu()[:, None], want, 0.0 * want).cuda()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,N", ADD)
+def test_inner_sums_are_whole_in_every_add(gpu_available, T, N, dtype):
+    print(f"whole inner sums T={T} N={N} {dtype}", flush=True)
+    x, a, b, ad, s, want = _whole_sums(T, N, 520)
+    out = i8h.lora_add(torch.zeros((T, N), dtype=dtype, device="cuda"), x, a, b, ad, s)
+    assert torch.equal(out, want.to(dtype))
+    # and of rank 8: five rows take one launch
+    keep = [0, 33, 130, 1, 2, 3, 4, 5]
+    out = i8h.lora_add(torch.zeros((T, N), dtype=dtype, device="cuda"), x, a[:, keep].contiguous(), b[:, :, keep].contiguous(),
+                       ad, s)
+    assert torch.equal(out, want.to(dtype))
+
+
+@pytest.mark.parametrize("T,N", TILES)
+def test_inner_sums_are_whole_in_every_tile(gpu_available, T, N):
+    print(f"whole inner sums, linear T={T} N={N}", flush=True)
+    K = 640
+    x, a, b, ad, s, want = _whole_sums(T, N, K)
+    codes = torch.zeros((N, K), dtype=torch.int8, device="cuda")
+    scales = torch.ones((N, K // 128), dtype=torch.float16, device="cuda")
+    assert torch.equal(i8h.linear_i8f16_lora(x, codes, scales, a, b, ad, s), want)
+
+
 # --------------------------------------------------------------------------------------------------- infinities in B
 
 def _formula(base, x, a, b, s, ad):

@@ -59,3 +59,17 @@ def test_lora_hand_case():
     d, lim = lora.delta(x, a, b, [0, 2, 1], [2.0, 1.0])
     assert d.tolist() == [[6.0, 60.0], [0.0, 0.0], [4.0, 1.0]]
     assert (lim[1] == 0).all() and (lim[0] > 0).all() and (lim[[0, 2]] < 1e-4).all()
+
+
+def test_whole_sums_would_show_a_lost_part():
+    """The inner sum of the GPU tests that take it whole: each of its three bf16 parts, dropped, changes what they expect."""
+    h = np.float32(1 + 2.0 ** -12 + 2.0 ** -23)
+    parts = []
+    for _ in range(3):
+        p = (np.array([h], np.float32).view(np.uint32) & np.uint32(0xffff0000)).view(np.float32)[0]
+        parts.append(float(p))
+        h = np.float32(h - p)
+    assert parts == [1.0, 2.0 ** -12, 2.0 ** -23] and h == 0
+    for lost in range(3):
+        left = sum(p for i, p in enumerate(parts) if i != lost)
+        assert 1024 * (left - 1) != 0.25 + 2.0 ** -13 and 1024 * (left - 1 - 2.0 ** -12) != 2.0 ** -13
