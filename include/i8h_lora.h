@@ -29,7 +29,8 @@ extern "C" {
 
 /* Device scratch of both calls, in bytes: the inner sums, T x R float32, in up
  * to 8 slices of K. lora_add takes none for few rows of low rank (T <= 256,
- * R <= 64, T * R <= 4096): its own size is 0 there, else the same. */
+ * R <= 64, T * R <= 4096): its own size is 0 there, else the same. Sizes never
+ * fall as T or R grow: scratch for the largest batch serves smaller ones. */
 size_t lora_workspace_size(int T, int R);
 size_t lora_add_workspace_size(int T, int R);
 

@@ -53,7 +53,9 @@ enum { I8H_SCORE_SOFTMAX = 0, I8H_SCORE_SIGMOID = 1 };
  * groups) (else I8H_EINVAL); groups <= I8H_MAX_GROUPS, E and topk as in i8h.h,
  * T * topk below 2^31 and the workspace's counts too (else I8H_EUNSUPPORTED).
  * workspace: at least moe_route_scored_workspace_size(T, E, topk) bytes,
- * 256-B aligned, contents on entry ignored (may be NULL when that size is 0). */
+ * 256-B aligned, contents on entry ignored (may be NULL when that size is 0).
+ * Sizes never fall as T, E or topk grow: one for the largest batch serves
+ * smaller ones. */
 size_t moe_route_scored_workspace_size(int T, int E, int topk);
 int moe_route_scored_permute(const void* logits, int logits_type, int T, int E, int topk, int score,
                              const float* bias, int groups, int topk_groups, int group_top, int renormalize,

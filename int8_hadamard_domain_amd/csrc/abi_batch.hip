@@ -102,7 +102,7 @@ int moe_route_scored_permute(const void* logits, int logits_type, int T, int E, 
 
 size_t lora_workspace_size(int T, int R) {
   if (T <= 0 || R <= 0) return 0;
-  return round_up((size_t)i8h::lora_slices(T) * T * R * sizeof(float), 256);
+  return round_up((size_t)i8h::lora_sums(T) * R * sizeof(float), 256);
 }
 
 size_t lora_add_workspace_size(int T, int R) { return i8h::lora_few(T, R) ? 0 : lora_workspace_size(T, R); }

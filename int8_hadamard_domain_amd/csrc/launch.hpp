@@ -128,8 +128,8 @@ hipError_t launch_route_scored(const void* logits, bool bf16, int T, int E, int 
                                hipStream_t st);
 
 // low-rank adapters (lora.hip): h [slices, T, R] float32 holds the scaled inner
-// sums of slices of K, at most lora_slices(T) of them
-int lora_slices(int T);
+// sums of slices of K, at most lora_sums(T) rows in all
+int64_t lora_sums(int T);
 hipError_t launch_lora_shrink(const uint16_t* x, int64_t ldx, int T, int K, const uint16_t* a, int L, int R,
                               const int32_t* adapter, const float* scale, float* h, int* slices, hipStream_t st);
 // the dense int8 linear with the adapters' products (linear_lora.hip)

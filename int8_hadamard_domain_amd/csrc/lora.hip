@@ -529,7 +529,13 @@ k_lora_add(const void* base, int64_t ldb, int T, int N, const uint16_t* __restri
 
 }  // namespace
 
-int lora_slices(int T) { return std::max(1, std::min(kLoraSlices, 512 / ((T - 1) / kShRows + 1))); }
+// As many slices as make 512 workgroups of the tiles.
+constexpr int kShFill = 512;
+static int lora_slices(int T) { return std::max(1, std::min(kLoraSlices, kShFill / ((T - 1) / kShRows + 1))); }
+
+// Never less for more rows: slices times rows go up and down with T (4096 rows are 8 slices, 4097 are 7), at most to
+// kShFill tiles.
+int64_t lora_sums(int T) { return std::min((int64_t)kLoraSlices * T, std::max((int64_t)kShFill * kShRows, (int64_t)T)); }
 
 hipError_t launch_lora_shrink(const uint16_t* x, int64_t ldx, int T, int K, const uint16_t* a, int L, int R,
                               const int32_t* adapter, const float* scale, float* h, int* slices, hipStream_t st) {

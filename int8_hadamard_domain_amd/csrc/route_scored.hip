@@ -903,7 +903,6 @@ struct Deal {
   }
   bool scanned() const { return chunks > kScScanFrom; }
   size_t hist_bytes() const { return ((size_t)chunks * epad + 255) / 256 * 256; }
-  size_t bytes(int E) const { return hist_bytes() + (scanned() ? (size_t)(wgs + 1) * E * sizeof(int32_t) : 0); }
 };
 
 template <int VPL, typename X>
@@ -958,7 +957,15 @@ bool scored_fits(int T, int E, int k) {
   return Deal(T, E, k).chunks * kWave * sc_waves<1>() < ((int64_t)1 << 32);
 }
 
-size_t scored_workspace_bytes(int T, int E, int k) { return small_form(T, E) ? 0 : Deal(T, E, k).bytes(E); }
+// Never less for more tokens: up to kScFill chunks their number goes up and down with T (256 tokens are 256 chunks, 257
+// are 129), so that from kScFill tokens on there is room for kScFill of them.
+size_t scored_workspace_bytes(int T, int E, int k) {
+  if (small_form(T, E)) return 0;
+  Deal d(T, E, k);
+  const size_t sums = d.scanned() ? (size_t)(d.wgs + 1) * E * sizeof(int32_t) : 0;
+  d.chunks = std::max<int64_t>(d.chunks, std::min(T, kScFill));
+  return d.hist_bytes() + sums;
+}
 
 hipError_t launch_route_scored(const void* logits, bool bf16, int T, int E, int k, bool sigmoid, const float* bias,
                                int groups, int keep, int top, bool renorm, float scale, int32_t* ids, float* w,

@@ -154,3 +154,34 @@ def test_limits(L):
         assert linear(*bad) == EUNSUP, bad
     for T, R in ((1, 8), (64, 64), (1 << 20, 256), ((1 << 26), 256)):
         assert L.lora_workspace_size(T, R) >= 4 * T * R
+
+
+def _falls(sizes):
+    return [(i, a, b) for i, (a, b) in enumerate(zip(sizes, sizes[1:])) if b < a]
+
+
+def test_workspace_sizes_never_fall(L):
+    """A workspace for the largest batch serves every smaller one, and one for the most experts, choices or the highest
+    rank every lower: the sizes do not fall as any of these grow (lora_add's own are 0 or the common one)."""
+    ts = sorted(set(range(1, 3000)) | {64 * i + d for i in range(40, 600) for d in (-1, 0, 1)} |
+                {b + d for b in (1 << 14, 16640, 32768, 65536, 1 << 20, 1 << 24) for d in (-1, 0, 1, 2)})
+    for R in (8, 32, 256):
+        sizes = [L.lora_workspace_size(T, R) for T in ts]
+        assert not _falls(sizes), (R, _falls(sizes)[:3])
+        assert all(s >= 4 * T * R for s, T in zip(sizes, ts))
+        own = [L.lora_add_workspace_size(T, R) for T in ts]
+        assert not _falls(own) and all(o in (0, s) for o, s in zip(own, sizes))
+    for T in (1, 64, 65, 256, 300, 5000):
+        assert not _falls([L.lora_workspace_size(T, R) for R in range(8, 264, 8)])
+        assert not _falls([L.lora_add_workspace_size(T, R) for R in range(8, 264, 8)])
+    for E in (1, 16, 60, 256, 257, 384, 1024):
+        for k in (1, 2, 5, 8, 9, 20, 32):
+            sizes = [L.moe_route_scored_workspace_size(T, E, k) for T in ts]
+            assert not _falls(sizes), (E, k, _falls(sizes)[:3])
+    for T in (1, 33, 256, 257, 300, 1999, 4097, 16384, 16385, 70000):
+        for k in (1, 8, 32):
+            sizes = [L.moe_route_scored_workspace_size(T, E, k) for E in range(1, 1025)]
+            assert not _falls(sizes), (T, k, _falls(sizes)[:3])
+        for E in (16, 256, 1024):
+            sizes = [L.moe_route_scored_workspace_size(T, E, k) for k in range(1, 33)]
+            assert not _falls(sizes), (T, E, _falls(sizes)[:3])
