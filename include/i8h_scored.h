@@ -49,9 +49,10 @@ enum { I8H_SCORE_SOFTMAX = 0, I8H_SCORE_SIGMOID = 1 };
  * logits [T, E] (logits_type: I8H_F32 or I8H_BF16, aligned to the element);
  * bias [E] float32 or NULL; topk_ids, topk_w, expert_off, sorted_pairs and
  * pair_pos as for moe_route_permute. E % groups == 0, 1 <= topk_groups <=
- * groups, group_top 1 or 2 and at most E / groups, topk <= topk_groups * (E /
- * groups) (else I8H_EINVAL); groups <= I8H_MAX_GROUPS, E and topk as in i8h.h,
- * T * topk below 2^31 and the workspace's counts too (else I8H_EUNSUPPORTED).
+ * groups, group_top 1 or 2 and with more than one group at most E / groups,
+ * topk <= topk_groups * (E / groups) (else I8H_EINVAL); groups <=
+ * I8H_MAX_GROUPS, E and topk as in i8h.h, T <= (2^22 - 1) * min(64, 512 / topk),
+ * so that T * topk is below 2^31 (else I8H_EUNSUPPORTED).
  * workspace: at least moe_route_scored_workspace_size(T, E, topk) bytes,
  * 256-B aligned, contents on entry ignored (may be NULL when that size is 0).
  * Sizes never fall as T, E or topk grow: one for the largest batch serves

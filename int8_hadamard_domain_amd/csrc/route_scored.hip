@@ -13,7 +13,7 @@
 //   k_scored_small    up to 32 tokens: everything in one workgroup
 //   k_scored_rows     per chunk of tokens: a wave per token chooses its
 //                     experts; the chunk's histogram
-//   k_scored_scan     more than 64 chunks: the histograms' running sums
+//   k_scored_scan     more than 256 chunks: the histograms' running sums
 //   k_scored_scatter  per chunk: first rows of the experts, stable ranks
 //
 // Measured (medians on MI355X): one token of 128 experts 5.2 us in one launch;
@@ -953,7 +953,8 @@ hipError_t launch(const void* logits, int T, const ScoredRule& R, int32_t* ids, 
 }  // namespace
 
 bool scored_fits(int T, int E, int k) {
-  // offsets into the counts and the chunks' first pairs are 64-bit; a launch holds fewer than 2^32 threads
+  // offsets into the counts and the chunks' first pairs are 64-bit; a launch holds fewer than 2^32 threads, and a chunk
+  // takes up to 1024
   return Deal(T, E, k).chunks * kWave * sc_waves<1>() < ((int64_t)1 << 32);
 }
 

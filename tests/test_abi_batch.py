@@ -185,3 +185,16 @@ def test_workspace_sizes_never_fall(L):
         for E in (16, 256, 1024):
             sizes = [L.moe_route_scored_workspace_size(T, E, k) for k in range(1, 33)]
             assert not _falls(sizes), (T, E, _falls(sizes)[:3])
+
+
+def test_scored_routing_limits(L):
+    """The documented limits, from both sides (a call within them gets as far as the missing logits)."""
+    def call(T, E, k, groups=1, keep=1, top=1):
+        return L.moe_route_scored_permute(None, 0, T, E, k, 0, None, groups, keep, top, 1, 1.0, A[2], A[3], A[4], A[5], A[6],
+                                          A[7], 1 << 62, None)
+    for k in (1, 3, 8, 9, 20, 32):
+        most = ((1 << 22) - 1) * min(64, 512 // k)
+        assert call(most, 1024, k) == EINVAL and call(most + 1, 1024, k) == EUNSUP, k
+    assert call(5, 1024, 32, 64, 64) == EINVAL and call(5, 1025, 4) == EUNSUP and call(5, 1024, 33) == EUNSUP
+    # one group: its worth decides nothing, and group_top is not held against its size
+    assert call(0, 1, 1, top=2) == OK and call(0, 2, 1, 2, 1, top=2) == EINVAL
