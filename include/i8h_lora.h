@@ -54,7 +54,9 @@ int lora_add(const void* base, int base_type, int64_t ldb, const uint16_t* x, in
 
 /* y[t] = linear_i8f16's product + delta[t]: the dense int8 linear with f16
  * scales and its adapters in one product. x, codes, scales, y as for
- * linear_i8f16 (K % 128 == 0, N % 16 == 0), the adapters and limits as above;
+ * linear_i8f16 (K % 128 == 0, N % 16 == 0), the adapters and limits as above
+ * (up to 32 tokens of low rank, linear_i8f16 and lora_add in place on its
+ * output are the faster calls);
  * T * K < 2^31 (else I8H_EUNSUPPORTED). y overlaps no input. workspace: at
  * least lora_workspace_size(T, R) bytes. */
 int linear_i8f16_lora(const uint16_t* x, int T, int K, const int8_t* codes, const uint16_t* scales, int N,

@@ -21,9 +21,9 @@
 // bf16 parts (their sum is the float32 value), the rows of other adapters
 // dropped after the product.
 //
-// Measured (4096 x 2048, medians, without the shrink): 16 tokens of rank 16 7.0
-// us, 128 tokens 14.2 (both bound by the chain first loads, stages, join,
-// adapters), 1024 tokens of rank 32 34.6 us: 496 TFLOP/s. Of its 65,000 cycles
+// Measured (4096 x 2048, medians, without the shrink): 16 tokens of rank 16 6.8
+// us, 128 tokens 14.0 (both bound by the chain first loads, stages, join,
+// adapters), 1024 tokens of rank 32 35.2 us: 498 TFLOP/s. Of its 65,000 cycles
 // 8,000 go by before the first products (every CU asks for its first 96 KB at
 // once), 11,000 in the join and the adapters; each of the eight stages takes
 // 5,500, of which the matrix units need 2,050: the tokens' copies go at 31 bytes
@@ -33,6 +33,10 @@
 // exchanged between lanes and registers (43.4), the next stage's decoding between
 // this one's products with both of these (40.3, and 69.8 against 69.9 at 2048
 // tokens), codes through LDS as well (55), two workgroups of four waves a CU (47).
+// Up to 32 tokens of low rank the plain linear and lora_add in place on its output
+// take less, in a graph and us, this and those with rank 16: 1 token 11.0, 8.5; 16
+// tokens 11.4, 9.3; 32 tokens 13.7, 11.3; 64 tokens 14.8, 18.5; 128 tokens 18.6,
+// 34.7. Of rank 64: 16 tokens 13.0, 14.0; 64 tokens 16.5, 26.8.
 
 #include <algorithm>
 #include <type_traits>

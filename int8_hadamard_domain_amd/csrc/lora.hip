@@ -59,7 +59,7 @@ __device__ __forceinline__ u32x4 load16(const void* p, uint32_t off) {
 // at different stages: rows lie a power of two apart more often than not, and
 // all tiles at the same piece of K would ask the same L2 channels. The next
 // adapter's first loads are issued before this one's sums are added up.
-// 11.7 us for 2048 rows of K = 4096 and rank 64, five requests: 1.5 TB/s; 13.9 us
+// 11.3 us for 2048 rows of K = 4096 and rank 64, five requests: 1.7 TB/s; 13.7 us
 // for 8191 rows of K = 2048 and rank 32. Bound by the chain adapter, first loads,
 // four or eight stages, sums in LDS: the loads of two stages in flight are all
 // that the registers hold.
@@ -389,9 +389,9 @@ struct Piece {
 // layouts deal a row to lanes 16 apart; so base and out are loaded and stored
 // with 128 bytes of a row on neighbouring lanes, B 64 bytes of a row on four,
 // and a wave's own LDS turns B's rows and the products into the other order
-// (64 us without, 55 with, of 8191 x 4096 float32 rows: 268 MB at 4.8 TB/s, a
-// copy takes 45 here; 2048 x 2048 bf16 rows of rank 64 9.2 us, 1.8 TB/s, bound
-// by the chain of h, B and the products in each workgroup).
+// (64 us without, 55 with, of 8191 x 4096 float32 rows: 278 MB at 5.0 TB/s, where
+// a copy of 268 MB takes 51 us; 2048 x 2048 bf16 rows of rank 64 9.2 us, 1.8 TB/s,
+// bound by the chain of h, B and the products in each workgroup).
 template <bool BF16, int MT>
 __global__ void __launch_bounds__(kAddThreads, BF16 && MT == 2 ? 3 : 4)
 k_lora_add(const void* base, int64_t ldb, int T, int N, const uint16_t* __restrict__ b, int L, int R,

@@ -17,11 +17,13 @@
 //   k_scored_scatter  per chunk: first rows of the experts, stable ranks
 //
 // Measured (medians on MI355X): one token of 128 experts 5.2 us in one launch;
-// 128 tokens 4.5 (rows) + 4.4 (scatter); 1999 tokens of 160 experts, 3 of 8
-// groups, 9.3 + 5.6; 16384 tokens of 256 experts, 4 of 8 groups, 23.8 + 5.9
+// 128 tokens 4.6 (rows) + 4.2 (scatter); 1999 tokens of 160 experts, 3 of 8
+// groups, 9.3 + 5.3; 16384 tokens of 256 experts, 4 of 8 groups, 23.9 + 5.9
 // (the bytes alone 3.7). Few tokens: the chain of dependent steps of one token,
-// 2.3 us, and of the permutation. Many: the vector unit's issue, 380
-// instructions a token by a whole wave.
+// 2.3 us, and of the permutation. Many: the vector unit's issue, 372
+// instructions a token by a whole wave. The rule, the lists and the float64 path
+// need more scalar registers than there are: 33 to 51 of them (148 past 512
+// experts) are kept in lanes of vector registers, which costs vector instructions.
 
 #include <algorithm>
 
