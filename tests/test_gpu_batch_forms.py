@@ -195,3 +195,37 @@ def test_more_chunks_than_one_scatter_adds_up(gpu_available, T, E, k, groups, ke
     # distances from the largest logit are below 40 here: (40 + 2 d) 2^-24
     w = got["topk_w"][rows].cpu().numpy()
     assert np.all(np.abs(w - ref["topk_w"]) <= 120 * 2.0 ** -24 * np.abs(ref["topk_w"]) + 2.0 ** -126)
+
+
+# -------------------------------------------------------------------------------------- broken values in large batches
+
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,N", ADD[1:])
+def test_broken_values_stay_in_their_rows(gpu_available, T, N, dtype, value):
+    """NaN and infinities in an adapter, in its scale, in its rows' inputs, and in rows without one: the other rows' bits
+    are those of the whole batch."""
+    print(f"broken values T={T} N={N} {dtype} {value}", flush=True)
+    base, x, a, b, s, ad = problem(T, 72, N, 40, 5, "mixed", dtype)
+    want = i8h.lora_add(base, x, a, b, ad, s)
+    mine, none = ad == 1, ad == -1
+    for what in ("a", "b", "b here and there", "s", "x", "x of none"):
+        a2, b2, s2, x2 = a.clone(), b.clone(), s.clone(), x.clone()
+        if what == "a":
+            a2[1] = value
+        elif what == "b":
+            b2[1] = value
+        elif what == "b here and there":
+            b2[1, ::17, 5] = value
+        elif what == "s":
+            s2[1] = value
+        else:
+            x2[mine if what == "x" else none] = value
+        got = i8h.lora_add(base, x2, a2, b2, ad, s2)
+        assert torch.equal(got[~mine], want[~mine]), what
+        broken = torch.zeros(N, dtype=torch.bool, device="cuda")
+        broken[::17] = what == "b here and there"
+        if what in ("a", "b", "s", "x"):
+            broken[:] = True
+        assert not bool(torch.isfinite(got[mine][:, broken].float()).any()), what
+        assert torch.equal(got[mine][:, ~broken], want[mine][:, ~broken]), what

@@ -235,3 +235,24 @@ def test_weights_of_spread_logits(gpu_available):
     for renorm, scale in ((True, 1.0), (True, 2.0 ** 100), (False, 2.0 ** 100)):
         check(l, 8, rule("sigmoid", None, 1, 1, 1, renorm, scale))
         check(l, 4, rule("sigmoid", None, 4, 2, 2, renorm, scale))
+
+
+@pytest.mark.parametrize("T", [9, 80])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_scales_that_are_not_ordinary(gpu_available, score, T):
+    """A scale of 0, an infinity or NaN meets each weight as its product in float64 does, rows masked whole among them."""
+    l = logits_of(T, 40, T, mask=0.1)
+    l[1] = -math.inf
+    l[2, :38] = -math.inf
+    for scale in (0.0, math.inf, -math.inf, math.nan, 3.4e38, 1e-45):
+        for renorm in (True, False):
+            r = rule(score, bias_of(40, 1), 4, 2, 1, renorm, scale)
+            got = call(l, 6, r)
+            with np.errstate(invalid="ignore", over="ignore"):
+                one = scored.route(l.cpu().numpy(), 6, score, r["bias"], 4, 2, 1, renorm, 1.0)
+                want = one["topk_w"] * float(np.float32(scale))
+                w = got["topk_w"].cpu().numpy().astype(np.float64)
+                assert np.array_equal(np.isnan(w), np.isnan(want)) and np.array_equal(got["topk_ids"].cpu().numpy(), one["topk_ids"])
+                # distances from the largest logit are below 30 here: (40 + 2 d) 2^-24
+                fine = (w == want) | np.isnan(want) | (np.abs(w - want) <= 100 * 2.0 ** -24 * np.abs(want) + 2.0 ** -126)
+            assert fine.all(), (scale, renorm)
